@@ -9,6 +9,7 @@ the library is missing or does not load, every call raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -39,6 +40,7 @@ SIGNATURES = {
     "pa_attn_fwd_chunks": (_I, [_VP, _VP, _VP, _VP, _I, _VP, _VP, _I, _I, _I, _I, _F, _VP]),
     "pa_attn_merge": (_I, [_VP, _VP, _I, _VP, _VP, _I, _I, _I, _I, _VP]),
     "pa_attn_chunks_noalloc": (_I, [_VP, _VP, _VP, _VP, _I, _VP, _VP, _I, _I, _I, _I, _F, _VP]),
+    "pa_attn_fwd_mod": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _VP, _F, _VP, _VP]),
     "pa_residual_diff": (_I, [_VP, _VP, ctypes.c_longlong, _VP, _VP]),
     "pa_status_string": (ctypes.c_char_p, [_I]),
     "pa_last_error": (ctypes.c_char_p, []),
@@ -47,6 +49,13 @@ SIGNATURES = {
     "pa_set_wait_limit_ms": (_I, [_I]),
     "pa_version": (_I, []),
 }
+
+
+class ScoreMod(ctypes.Structure):
+    """``pa_score_mod`` of include/pa_attn.h."""
+
+    _fields_ = [("softcap", _F), ("causal", _I), ("slopes", _VP), ("prefix_lens", _VP), ("doc_offsets", _VP),
+                ("n_docs", _I), ("q_offset", _I)]
 
 
 class PaError(RuntimeError):
@@ -279,6 +288,111 @@ def residual_diff(cur, prev, out=None, stream=None, check: bool = False):
                                          _stream_handle(stream, cur.device))
     _check(rc, "pa_residual_diff", check)
     return out
+
+
+@contextlib.contextmanager
+def _allocating_for(stream, device):
+    """Buffers allocated inside belong to the stream the kernels run on, so
+    that the allocator hands their memory on only behind those kernels."""
+    import torch
+    if stream is None:
+        yield
+        return
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        yield
+
+
+def _check_rows(name, t, ndim, device=None):
+    """A bf16 CUDA tensor whose last dimension is contiguous."""
+    import torch
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16 (got {t.dtype})")
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"{name} must live on {'a CUDA device' if device is None else device}")
+    if t.dim() != ndim or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name} must be a {ndim}-d tensor with a contiguous last dimension")
+
+
+def _check_vector(name, t, dtype, shape, device):
+    if t is None:
+        return None
+    import torch
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape)
+            or not t.is_contiguous() or t.device != device):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _lse_out(lse, shape, device):
+    import torch
+    if lse is None:
+        return torch.empty(shape, dtype=torch.float32, device=device)
+    _check_vector("lse", lse, torch.float32, shape, device)
+    return lse
+
+
+def attn_fwd_mod(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, slopes=None, causal: bool = False,
+                 prefix_lens=None, doc_offsets=None, q_offset: Optional[int] = None, out=None, lse=None, stream=None,
+                 check: bool = False):
+    """Attention with capped and biased scores and interval masks
+    (``pa_attn_fwd_mod``): q [B,Hq,Nq,d], k, v [B,Hkv,Nk,d] bf16, Hq a multiple
+    of Hkv, any strides that are multiples of 8 elements with the last
+    dimension contiguous.
+
+    ``softcap`` c > 0 turns a score s into c*tanh(s/c); ``slopes`` [Hq] float32
+    subtracts slopes[h] * |p_i - j|.  Row i stands at p_i = i + ``q_offset``
+    (default Nk - Nq: the queries are the last keys).  ``causal`` hides keys
+    behind p_i, except the first ``prefix_lens`` keys ([B] int32; of each
+    document [B,n_docs] with documents).  ``doc_offsets`` [B,n_docs+1] int32
+    cuts the keys into documents; a row sees its own only.  Rows that see
+    nothing get o = 0 and lse = -inf.  Returns (o, lse) like attn_fwd; o has
+    q's layout.  With very few query rows use ``attn_shared_prefix``, which
+    splits the keys over the GPU.
+    """
+    import torch
+    _check_rows("q", q, 4)
+    _check_rows("k", k, 4, q.device)
+    _check_rows("v", v, 4, q.device)
+    B, Hq, Nq, d = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    if k.shape[0] != B or k.shape[3] != d or v.shape != k.shape or Hkv < 1 or Hq % Hkv:
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
+    n_docs = 0
+    if doc_offsets is not None:
+        if doc_offsets.dim() != 2 or doc_offsets.shape[1] < 2:
+            raise ValueError("doc_offsets must be [B, n_docs + 1] with n_docs >= 1")
+        n_docs = doc_offsets.shape[1] - 1
+    mod = ScoreMod(float(softcap), 1 if causal else 0, _check_vector("slopes", slopes, torch.float32, (Hq,), q.device),
+                   None, _check_vector("doc_offsets", doc_offsets, torch.int32, (B, n_docs + 1), q.device), n_docs,
+                   int(Nk - Nq if q_offset is None else q_offset))
+    if prefix_lens is not None:
+        shape = (B, n_docs) if n_docs else (B,)
+        if not n_docs and prefix_lens.dim() == 2:
+            shape = (B, 1)
+        mod.prefix_lens = _check_vector("prefix_lens", prefix_lens, torch.int32, shape, q.device)
+    with _allocating_for(stream, q.device):
+        if out is None:
+            out = torch.empty_like(q)  # keeps a dense layout such as [B, Nq, Hq, d]
+            if out.stride(-1) != 1:
+                out = torch.empty((B, Hq, Nq, d), dtype=torch.bfloat16, device=q.device)
+        lse = _lse_out(lse, (B, Hq, Nq), q.device)
+    _check_rows("out", out, 4, q.device)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    strides = None
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()):
+        strides = (ctypes.c_longlong * 12)(*[s for t in (q, k, v, out) for s in t.stride()[:3]])
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    rc = load_library().pa_attn_fwd_mod(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B,
+                                         Hq, Hkv, Nq, Nk, d, strides, float(scale), ctypes.byref(mod),
+                                         _stream_handle(stream, q.device))
+    _check(rc, "pa_attn_fwd_mod", check)
+    return out, lse
 
 
 def attn_merge(o_parts, lse_parts, out=None, lse=None, stream=None, check: bool = False):

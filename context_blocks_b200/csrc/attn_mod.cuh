@@ -1,0 +1,546 @@
+// Attention with modified scores and interval masks (pa_attn_fwd_mod) on sm_100a.
+//
+// Row i of the call stands at position p_i = i + q_offset among the keys and
+// sees one interval [lo_i, hi_i) of them:
+//     no mask      [0, Nk)
+//     causal       [0, max(p_i + 1, prefix))
+//     documents    [start, end) of the document that holds p_i, and with
+//                  causal [start, min(end, max(p_i + 1, start + prefix)))
+// Scores are capped and biased as score_mod.cuh says.  A row that sees nothing
+// gets O = 0 and LSE = -inf.
+//
+// Work: an item is 256 query rows (two tiles of 128) of one (batch, head); only
+// the key tiles that some row of a tile sees are loaded, and a query tile takes
+// part only in those its own rows see.  Warps:
+//   0-3, 4-7   softmax of query tile 0 and 1, a row a thread (208 registers)
+//   8          tcgen05.mma issue      9   TMA loads (Q of the item, K/V ring)
+//   10         scheduler: the next item, its intervals' hull per query tile and
+//              the documents it spans, through a two-slot ring in shared memory
+//   11         idle (completes the register split's warpgroup)
+// Key tiles are walked from the last to the first: the nearest keys come
+// first, so a bias that falls with distance settles the row maximum at once
+// instead of moving it with every tile.
+// Tensor memory and shared memory are laid out as in attn_fwd.cuh.
+//
+// Bound: the special-function unit and the tensor pipe, as the plain forward;
+// a cap adds an ex2 and a reciprocal a score.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "score_mod.cuh"
+
+namespace pa {
+namespace mod {
+
+constexpr int kStages = 4;
+constexpr int kMmaWarp = 8;
+constexpr int kTmaWarp = 9;
+constexpr int kSchedWarp = 10;
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168;
+constexpr int kSoftmaxRegs = 208;
+constexpr int kControlRegs = 88;
+static_assert(kControlRegs + 2 * kSoftmaxRegs == 3 * kLaunchRegs, "register split must sum to the launch allocation");
+
+struct FwdModParams {
+  __nv_bfloat16* o;
+  float* lse;  // [B, Hq, Nq]
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  long long q_s[3], k_s[3], v_s[3], o_s[3];  // element strides: batch, head, row
+  int B, Hq, G;                              // G = Hq / Hkv
+  int Nq, Nk;
+  int items, blocks_per_bh;
+  int q_offset;
+  int causal;
+  const int* prefix;  // [B, max(n_docs, 1)] or null
+  const int* docs;    // [B, n_docs + 1] or null
+  int n_docs;
+  ScoreMod sm;
+  int* status;
+  unsigned long long timeout_ns;
+};
+
+// Index of the last of off[0 .. n] that is <= pos, looked for in [t0, t1]
+// (t0 is returned where none above it is; -1 stands for "none").
+__device__ __forceinline__ int find_doc(const int* off, int pos, int t0, int t1) {
+  while (t0 < t1) {
+    const int t = t0 + (t1 - t0 + 1) / 2;
+    if (__ldg(off + t) <= pos)
+      t0 = t;
+    else
+      t1 = t - 1;
+  }
+  return t0;
+}
+
+// Keys [x, y) that the row at `pos` of batch b sees, its document being t.
+__device__ __forceinline__ int2 row_interval(const FwdModParams& p, int b, int pos, int t) {
+  int lo = 0, hi = p.Nk, pre = 0;
+  if (p.docs != nullptr) {
+    if (t < 0 || t >= p.n_docs) return make_int2(0, 0);
+    const int* off = p.docs + static_cast<long long>(b) * (p.n_docs + 1) + t;
+    lo = min(max(__ldg(off), 0), p.Nk);
+    hi = min(max(__ldg(off + 1), lo), p.Nk);
+    if (p.prefix != nullptr) pre = __ldg(p.prefix + static_cast<long long>(b) * p.n_docs + t);
+  } else if (p.prefix != nullptr) {
+    pre = __ldg(p.prefix + b);
+  }
+  if (p.causal) {
+    pre = min(max(pre, 0), p.Nk);
+    hi = max(lo, min(hi, max(pos + 1, lo + pre)));
+  }
+  return make_int2(lo, hi);
+}
+
+// What the scheduler tells the other warps about an item (item < 0: no more).
+struct ItemSlot {
+  int item;
+  int first[2], last[2];  // key tiles [first, last) of query tile 0 and 1
+  int doc0, doc1;         // documents of the item's first and last row
+};
+
+template <int D>
+struct Layout {
+  static constexpr int kBoxBytes = 128 * 128;
+  static constexpr int kBoxes = D / 64;
+  static constexpr int kTileBytes = kBoxes * kBoxBytes;
+  static constexpr int kQOff = 0;
+  static constexpr int kRingOff = kQOff + kQTiles * kTileBytes;
+  static constexpr int kStageOff = kRingOff + kStages * kTileBytes;
+  static constexpr int kStageWarpBytes = 32 * 128;
+  static constexpr int kBarOff = kStageOff + 8 * kStageWarpBytes;
+  // q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], p_part[2], p_full[2],
+  // o_full[2], drain, item_full[2], item_empty[2]
+  static constexpr int kNumBars = 2 + 2 * kStages + 8 + 1 + 4;
+  static constexpr int kItemOff = kBarOff + kNumBars * 8;
+  static constexpr int kTmemSlotOff = kItemOff + 2 * static_cast<int>(sizeof(ItemSlot));
+  static constexpr int kAbortOff = kTmemSlotOff + 4;
+  static constexpr int kBytes = kAbortOff + 4;
+  // Never two CTAs an SM: each takes all of tensor memory.
+  static constexpr int kMinOneCtaPerSm = 120 * 1024;
+  static constexpr int kAllocBytes = (kBytes + 1024 > kMinOneCtaPerSm) ? (kBytes + 1024) : kMinOneCtaPerSm;
+};
+
+template <int D, bool kCap, bool kBias>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_mod_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ FwdModParams p) {
+  using L = Layout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = smem_raw + (base - raw);
+
+  const uint32_t sQ = base + L::kQOff;
+  const uint32_t sRing = base + L::kRingOff;
+  const uint32_t bars = base + L::kBarOff;
+  const uint32_t bar_q_full = bars, bar_q_empty = bars + 8;
+  const uint32_t bar_kv_full0 = bars + 8 * 2;
+  const uint32_t bar_kv_empty0 = bars + 8 * (2 + kStages);
+  const uint32_t bar_s_full0 = bars + 8 * (2 + 2 * kStages);
+  const uint32_t bar_p_part0 = bars + 8 * (4 + 2 * kStages);
+  const uint32_t bar_p_full0 = bars + 8 * (6 + 2 * kStages);
+  const uint32_t bar_o_full0 = bars + 8 * (8 + 2 * kStages);
+  const uint32_t bar_drain = bars + 8 * (10 + 2 * kStages);
+  const uint32_t bar_item_full0 = bars + 8 * (11 + 2 * kStages);
+  const uint32_t bar_item_empty0 = bars + 8 * (13 + 2 * kStages);
+  volatile ItemSlot* slots = reinterpret_cast<volatile ItemSlot*>(gbase + L::kItemOff);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kTmemSlotOff);
+  volatile int* abort_word = reinterpret_cast<volatile int*>(gbase + L::kAbortOff);
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  const uint64_t lim = p.timeout_ns;
+
+  if (threadIdx.x == 0) {
+    mbar_init(bar_q_full, 1);
+    mbar_init(bar_q_empty, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar_kv_full0 + 8 * s, 1);
+      mbar_init(bar_kv_empty0 + 8 * s, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_s_full0 + 8 * i, 1);
+      mbar_init(bar_p_part0 + 8 * i, 4);  // one arrival per softmax warp
+      mbar_init(bar_p_full0 + 8 * i, 4);
+      mbar_init(bar_o_full0 + 8 * i, 1);
+      mbar_init(bar_item_full0 + 8 * i, 1);
+      mbar_init(bar_item_empty0 + 8 * i, 10);  // 8 softmax warps, MMA, TMA
+    }
+    mbar_init(bar_drain, 1);
+    *abort_word = 0;
+    fence_barrier_init();
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    prefetch_tensormap(&tm_q);
+    prefetch_tensormap(&tm_k);
+    prefetch_tensormap(&tm_v);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto wait_all = [&](uint32_t bar, uint32_t parity) {
+    const bool got = mbar_wait_hint(bar, parity, abort_word, p.status, kStatusTimeout, lim, kSuspendHintNs);
+    return __all_sync(0xffffffffu, got);
+  };
+  // The it-th item of this CTA, copied out of its slot; false at the end (or
+  // where a wait gave up, with `ok` cleared).
+  auto next_item = [&](int it, ItemSlot& x, bool& ok) {
+    const int s = it & 1;
+    if (!wait_all(bar_item_full0 + 8 * s, (it >> 1) & 1)) {
+      ok = false;
+      return false;
+    }
+    x.item = slots[s].item;
+    x.first[0] = slots[s].first[0], x.first[1] = slots[s].first[1];
+    x.last[0] = slots[s].last[0], x.last[1] = slots[s].last[1];
+    x.doc0 = slots[s].doc0, x.doc1 = slots[s].doc1;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_item_empty0 + 8 * s);
+    return x.item >= 0;
+  };
+  auto first_of = [](const ItemSlot& x, int i) { return i ? x.first[1] : x.first[0]; };
+  auto last_of = [](const ItemSlot& x, int i) { return i ? x.last[1] : x.last[0]; };
+  // Key tiles of an item: the hull of its query tiles' ranges.
+  auto hull = [](const ItemSlot& x, int& a, int& b) {
+    const bool has0 = x.first[0] < x.last[0], has1 = x.first[1] < x.last[1];
+    a = has0 && has1 ? min(x.first[0], x.first[1]) : has0 ? x.first[0] : x.first[1];
+    b = has0 && has1 ? max(x.last[0], x.last[1]) : has0 ? x.last[0] : x.last[1];
+  };
+
+  if (warp > kSchedWarp) {
+    setmaxnreg_dec<kControlRegs>();
+  } else if (warp == kSchedWarp) {
+    setmaxnreg_dec<kControlRegs>();
+    // ----------------------------------------------------------- scheduler
+    int it = 0;
+    for (int item = blockIdx.x;; item += gridDim.x, ++it) {
+      const int s = it & 1;
+      if (!wait_all(bar_item_empty0 + 8 * s, ((it >> 1) & 1) ^ 1)) break;
+      if (item >= p.items) {
+        if (lane == 0) slots[s].item = -1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_item_full0 + 8 * s);
+        break;
+      }
+      // Items run from the last query rows to the first: with a causal mask the
+      // long ones come first.
+      const int bh = item % (p.B * p.Hq);
+      const int row0 = (p.blocks_per_bh - 1 - item / (p.B * p.Hq)) * (kQTiles * kBM);
+      const int b = bh / p.Hq;
+      const int rows = min(p.Nq - row0, kQTiles * kBM);
+      int doc0 = 0, doc1 = 0;
+      if (p.docs != nullptr) {
+        const int* off = p.docs + static_cast<long long>(b) * (p.n_docs + 1);
+        doc0 = find_doc(off, row0 + p.q_offset, -1, p.n_docs);
+        doc1 = find_doc(off, row0 + rows - 1 + p.q_offset, doc0, p.n_docs);
+      }
+      int lo[2] = {0x7fffffff, 0x7fffffff}, hi[2] = {0, 0};
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int r = u * 32 + lane;
+        if (r < rows) {
+          const int pos = row0 + r + p.q_offset;
+          int t = 0;
+          if (p.docs != nullptr) t = find_doc(p.docs + static_cast<long long>(b) * (p.n_docs + 1), pos, doc0, doc1);
+          const int2 v = row_interval(p, b, pos, t);
+          if (v.x < v.y) {
+            lo[u / 4] = min(lo[u / 4], v.x);
+            hi[u / 4] = max(hi[u / 4], v.y);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        lo[i] = __reduce_min_sync(0xffffffffu, lo[i]);
+        hi[i] = __reduce_max_sync(0xffffffffu, hi[i]);
+      }
+      if (lane == 0) {
+        slots[s].item = item;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          slots[s].first[i] = hi[i] > 0 ? lo[i] / kBN : 0;
+          slots[s].last[i] = hi[i] > 0 ? (hi[i] + kBN - 1) / kBN : 0;
+        }
+        slots[s].doc0 = doc0;
+        slots[s].doc1 = doc1;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_item_full0 + 8 * s);
+    }
+  } else if (warp == kTmaWarp) {
+    setmaxnreg_dec<kControlRegs>();
+    // ------------------------------------------------------------ producer
+    const bool leader = elect_one();
+    bool ok = true;
+    int idx = 0;      // ring loads issued so far (over all items)
+    int q_loads = 0;  // items whose Q was issued
+    ItemSlot x;
+    for (int it = 0; ok && next_item(it, x, ok); ++it) {
+      int a, b;
+      hull(x, a, b);
+      if (a >= b) continue;
+      const int bh = x.item % (p.B * p.Hq);
+      const int q0 = (p.blocks_per_bh - 1 - x.item / (p.B * p.Hq)) * (kQTiles * kBM);
+      const int bt = bh / p.Hq, hq = bh % p.Hq, hk = hq / p.G;
+      if (!wait_all(bar_q_empty, (q_loads & 1) ^ 1)) {
+        ok = false;
+        break;
+      }
+      if (leader) {
+        mbar_arrive_expect_tx(bar_q_full, kQTiles * L::kTileBytes);
+        for (int i = 0; i < kQTiles; ++i)
+#pragma unroll
+          for (int bx = 0; bx < L::kBoxes; ++bx)
+            tma_load_4d(sQ + i * L::kTileBytes + bx * L::kBoxBytes, &tm_q, bar_q_full, bx * 64, q0 + i * kBM, hq, bt);
+      }
+      __syncwarp();
+      ++q_loads;
+      for (int j = b - 1; j >= a && ok; --j) {
+        for (int t = 0; t < 2; ++t) {
+          const int s = idx % kStages;
+          if (!wait_all(bar_kv_empty0 + 8 * s, ((idx / kStages) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          if (leader) {
+            const uint32_t full = bar_kv_full0 + 8 * s;
+            mbar_arrive_expect_tx(full, L::kTileBytes);
+#pragma unroll
+            for (int bx = 0; bx < L::kBoxes; ++bx)
+              tma_load_4d(sRing + s * L::kTileBytes + bx * L::kBoxBytes, t ? &tm_v : &tm_k, full, bx * 64, j * kBN, hk,
+                          bt);
+          }
+          __syncwarp();
+          ++idx;
+        }
+      }
+    }
+    // Every copy issued has landed before the CTA exits (where nothing went
+    // wrong, the MMA warp has waited for each of them already).
+    if (!ok) {
+      if (q_loads > 0) mbar_wait(bar_q_full, (q_loads - 1) & 1, nullptr, p.status, kStatusTimeout, lim);
+      for (int s = 0; s < kStages && s < idx; ++s) {
+        const int cnt = (idx - s + kStages - 1) / kStages;
+        mbar_wait(bar_kv_full0 + 8 * s, (cnt - 1) & 1, nullptr, p.status, kStatusTimeout, lim);
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    setmaxnreg_dec<kControlRegs>();
+    // ----------------------------------------------------------- MMA issue
+    const bool leader = elect_one();
+    constexpr uint32_t kIdS = idesc_bf16(128, kBN, false, false);
+    constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true);
+    constexpr uint64_t kTileDesc = L::kTileBytes >> 4;
+    const uint32_t tO0 = tmem + 2 * kBN;
+    const uint64_t dQ = sdesc_k_sw128(sQ);
+    const uint64_t dK = sdesc_k_sw128(sRing);
+    const uint64_t dV = sdesc_mn_sw128(sRing, L::kBoxBytes);
+    auto issue_qk = [&](int i, int slot) {
+      const uint64_t dq = dQ + i * kTileDesc, dk = dK + slot * kTileDesc;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint64_t off = static_cast<uint64_t>(((kk / 4) * L::kBoxBytes + (kk % 4) * 32) >> 4);
+        umma_ss(tmem + i * kBN, dq + off, dk + off, kIdS, kk > 0);
+      }
+    };
+    auto issue_pv = [&](int i, int slot, bool acc, int part) {
+      const uint64_t dv = dV + slot * kTileDesc;
+      constexpr int kPer = kBN / 16 / kPParts;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        const int kk = part * kPer + u;
+        umma_ts(tO0 + i * D, tmem + i * kBN + kk * 8, dv + static_cast<uint64_t>(kk * 128), kIdPV,
+                (acc || kk > 0) ? 1u : 0u);
+      }
+    };
+    bool ok = true;
+    int idx = 0;           // ring position (over all items)
+    int g0 = 0, g1 = 0;    // key tiles of each query tile over all items: phases of the P barriers
+    int q_used = 0;
+    ItemSlot x;
+    for (int it = 0; ok && next_item(it, x, ok); ++it) {
+      int a, b;
+      hull(x, a, b);
+      if (a >= b) continue;
+      auto in = [&](int i, int j) { return j >= first_of(x, i) && j < last_of(x, i); };
+      if (!wait_all(bar_q_full, q_used & 1) ||
+          !wait_all(bar_kv_full0 + 8 * (idx % kStages), (idx / kStages) & 1)) {
+        ok = false;
+        break;
+      }
+      ++q_used;
+      tc_fence_after();
+      if (leader) {
+        for (int i = 0; i < 2; ++i)
+          if (in(i, b - 1)) {
+            issue_qk(i, idx % kStages);
+            umma_commit(bar_s_full0 + 8 * i);
+          }
+        umma_commit(bar_kv_empty0 + 8 * (idx % kStages));
+        if (b - 1 == a) umma_commit(bar_q_empty);
+      }
+      __syncwarp();
+      ++idx;
+      for (int j = b - 1; j >= a && ok; --j) {
+        const int sv = idx % kStages;
+        if (!wait_all(bar_kv_full0 + 8 * sv, (idx / kStages) & 1)) {
+          ok = false;
+          break;
+        }
+        ++idx;
+        const bool more = j > a;
+        int sk = 0;
+        for (int i = 0; i < 2 && ok; ++i) {
+          if (in(i, j)) {
+            const bool acc = j < last_of(x, i) - 1;
+            const uint32_t ph = (i ? g1 : g0) & 1;
+            if (!wait_all(bar_p_part0 + 8 * i, ph)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            if (leader) issue_pv(i, sv, acc, 0);
+            __syncwarp();
+            if (!wait_all(bar_p_full0 + 8 * i, ph)) {
+              ok = false;
+              break;
+            }
+            i ? ++g1 : ++g0;
+            tc_fence_after();
+            if (leader) {
+              issue_pv(i, sv, true, 1);
+              if (j == first_of(x, i)) umma_commit(bar_o_full0 + 8 * i);
+            }
+            __syncwarp();
+          }
+          if (leader && i == 1) umma_commit(bar_kv_empty0 + 8 * sv);
+          __syncwarp();
+          if (more) {
+            if (i == 0) {
+              sk = idx % kStages;
+              if (!wait_all(bar_kv_full0 + 8 * sk, (idx / kStages) & 1)) {
+                ok = false;
+                break;
+              }
+              ++idx;
+              tc_fence_after();
+            }
+            if (leader) {
+              if (in(i, j - 1)) {
+                issue_qk(i, sk);
+                umma_commit(bar_s_full0 + 8 * i);
+              }
+              if (i == 1) {
+                umma_commit(bar_kv_empty0 + 8 * sk);
+                if (j - 1 == a) umma_commit(bar_q_empty);  // the item's last Q K^T
+              }
+            }
+            __syncwarp();
+          }
+        }
+      }
+    }
+    // Every MMA issued completes before tensor memory is freed.
+    if (leader) umma_commit(bar_drain);
+    __syncwarp();
+    mbar_wait(bar_drain, 0, nullptr, p.status, kStatusTimeout, lim);
+    __syncwarp();
+  } else {
+    setmaxnreg_inc<kSoftmaxRegs>();
+    // ------------------------------------------------------------- softmax
+    const int i = warp / 4;
+    const uint32_t lane_off = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const uint32_t tS = tmem + i * kBN + lane_off;
+    const uint32_t tO = tmem + 2 * kBN + i * D + lane_off;
+    bool ok = true;
+    int g = 0;    // key tiles over all items: phases of the S barrier
+    int n_o = 0;  // items with key tiles: phase of the O barrier
+    ItemSlot x;
+    for (int it = 0; ok && next_item(it, x, ok); ++it) {
+      const int bh = x.item % (p.B * p.Hq);
+      const int bt = bh / p.Hq, hq = bh % p.Hq;
+      const int row = (p.blocks_per_bh - 1 - x.item / (p.B * p.Hq)) * (kQTiles * kBM) + threadIdx.x;
+      const int pos = row + p.q_offset;
+      float slope2 = 0.f;
+      if constexpr (kBias) slope2 = __ldg(p.sm.slopes + hq) * 1.4426950408889634f;
+      // Rows past Nq are computed like any other (their Q is zeros) and not
+      // stored; they count as seeing everything, so that they mask nothing.
+      int2 seen = make_int2(0, 0x7fffffff);
+      if (row < p.Nq) {
+        int t = 0;
+        if (p.docs != nullptr)
+          t = find_doc(p.docs + static_cast<long long>(bt) * (p.n_docs + 1), pos, x.doc0, x.doc1);
+        seen = row_interval(p, bt, pos, t);
+      }
+      float m_ref = -INFINITY, l = 0.f;
+      const int first = first_of(x, i), last = last_of(x, i);
+      for (int j = last - 1; j >= first; --j, ++g) {
+        const bool got =
+            mbar_wait_hint(bar_s_full0 + 8 * i, g & 1, abort_word, p.status, kStatusTimeout, lim, kSuspendHintNs);
+        if (__any_sync(0xffffffffu, !got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int k0 = j * kBN;
+        softmax_tile<D, kCap, kBias>(tS, tO, seen.x - k0, seen.y - k0, static_cast<float>(pos - k0), slope2, p.sm,
+                                     j < last - 1, m_ref, l, bar_p_part0 + 8 * i, bar_p_full0 + 8 * i, lane);
+      }
+      if (!ok) break;
+      if (first < last) {
+        const bool got = mbar_wait(bar_o_full0 + 8 * i, n_o & 1, abort_word, p.status, kStatusTimeout, lim);
+        if (__any_sync(0xffffffffu, !got)) {
+          ok = false;
+          break;
+        }
+        ++n_o;
+        tc_fence_after();
+      }
+      const int wrow = row - lane;  // first row of this warp
+      if (wrow >= p.Nq) continue;
+      const bool empty = m_ref == -INFINITY;
+      const float inv = empty ? 0.f : 1.f / l;
+      __nv_bfloat16* o = p.o + bt * p.o_s[0] + hq * p.o_s[1] + wrow * p.o_s[2];
+      const bool bad = store_rows<D>(tO, base + L::kStageOff + warp * L::kStageWarpBytes, o, nullptr, p.o_s[2],
+                                     p.Nq - wrow, inv);
+      if (row < p.Nq)
+        p.lse[static_cast<size_t>(bh) * p.Nq + row] =
+            empty ? -INFINITY : (m_ref + lg2_approx(l)) * 0.69314718055994531f;
+      // A value row that is not finite: leave hidden keys out by recomputing.
+      unsigned redo = __ballot_sync(0xffffffffu, bad && !empty && row < p.Nq && l <= FLT_MAX);
+      while (redo != 0u) {
+        const int r = __ffs(redo) - 1;
+        redo &= redo - 1;
+        __syncwarp();
+        const int j0 = __shfl_sync(0xffffffffu, seen.x, r), j1 = __shfl_sync(0xffffffffu, seen.y, r);
+        const float mr = __shfl_sync(0xffffffffu, m_ref, r), iv = __shfl_sync(0xffffffffu, inv, r);
+        const int hk = hq / p.G;
+        repair_row<D>(p.q + bt * p.q_s[0] + hq * p.q_s[1] + (wrow + r) * p.q_s[2],
+                      p.k + bt * p.k_s[0] + hk * p.k_s[1], p.v + bt * p.v_s[0] + hk * p.v_s[1], p.k_s[2], p.v_s[2], j0,
+                      j1, wrow + r + p.q_offset, mr, iv, slope2, p.sm, kCap, kBias, o + r * p.o_s[2], nullptr);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace mod
+}  // namespace pa

@@ -11,8 +11,10 @@
 #include <algorithm>
 #include <atomic>
 #include <mutex>
+#include <type_traits>
 
 #include "attn_fwd.cuh"
+#include "attn_mod.cuh"
 #include "quantize.cuh"
 #include "fwd_common.cuh"
 #include "lse_merge.cuh"
@@ -75,6 +77,7 @@ struct DeviceState {
   int* status = nullptr;  // device address of pa::g_status
   unsigned char* noalloc_scratch = nullptr;  // device address of pa::g_noalloc_scratch
   bool fwd_attr[5] = {};  // d = 64, d = 128, e4m3 d = 128, accumulate d = 64, accumulate d = 128
+  bool mod_attr[8] = {};  // modified scores: 4 * (d = 128) + 2 * capped + biased
 };
 
 
@@ -382,9 +385,229 @@ int check_chunk_args(const void* q, const void* const* k_chunks, const void* con
   return device_checks(ptrs, names, n, st);
 }
 
+// ------------------------------------------------- modified-score attention
+
+// One strided operand [B, H, N, d]: element strides of its first three
+// dimensions (the last is contiguous).
+struct Operand {
+  const void* ptr;
+  const char* name;
+  int B, H, N, d;
+  long long s[3];
+};
+
+constexpr long long kMaxStride = 1ll << 38;  // elements; TMA strides end at 2^40 bytes
+
+Operand operand(const void* ptr, const char* name, int B, int H, int N, int d, const long long* strides) {
+  Operand x{ptr, name, B, H, N, d, {static_cast<long long>(H) * N * d, static_cast<long long>(N) * d, d}};
+  if (strides)
+    for (int i = 0; i < 3; ++i) x.s[i] = strides[i];
+  // The stride of a dimension of one entry is never used: any legal one does.
+  if (B == 1) x.s[0] = d;
+  if (H == 1) x.s[1] = d;
+  if (N == 1) x.s[2] = d;
+  return x;
+}
+
+// Bytes from the first element to the end of the last row.
+uint64_t extent(const Operand& x) {
+  return static_cast<uint64_t>((x.B - 1) * x.s[0] + (x.H - 1) * x.s[1] + (x.N - 1) * x.s[2] + x.d) * 2;
+}
+
+int check_operand(const Operand& x, bool written) {
+  if (!x.ptr) return fail(PA_ERR_INVALID_ARG, "null pointer argument (%s)", x.name);
+  if (!aligned(x.ptr, 16)) return fail(PA_ERR_MISALIGNED, "%s must be 16-byte aligned", x.name);
+  for (int i = 0; i < 3; ++i) {
+    if (x.s[i] < 1 || x.s[i] > kMaxStride) return fail(PA_ERR_INVALID_ARG, "%s: stride %d out of range", x.name, i);
+    if (x.s[i] % 8) return fail(PA_ERR_MISALIGNED, "%s: strides must be multiples of 8 elements", x.name);
+  }
+  if (written) {
+    // Rows that are written must not share memory: with the dimensions ordered
+    // by stride, each one must step over all of the smaller ones.
+    const int n[3] = {x.B, x.H, x.N};
+    int order[3] = {0, 1, 2};
+    std::sort(order, order + 3, [&](int a, int b) { return x.s[a] < x.s[b]; });
+    long long span = x.d;
+    for (int i : order) {
+      if (n[i] <= 1) continue;
+      if (x.s[i] < span) return fail(PA_ERR_INVALID_ARG, "%s: strides make its rows overlap", x.name);
+      span = x.s[i] * n[i];
+    }
+  }
+  return PA_OK;
+}
+
+// 4-D map (d, N, H, B) with 128-byte swizzled boxes of 64 elements x box_rows
+// rows x 1 x box_batch.
+int encode_map4(CUtensorMap* map, const Operand& x, int box_rows, int box_batch = 1) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(x.d), static_cast<cuuint64_t>(x.N), static_cast<cuuint64_t>(x.H),
+                        static_cast<cuuint64_t>(x.B)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(x.s[2]) * 2, static_cast<cuuint64_t>(x.s[1]) * 2,
+                           static_cast<cuuint64_t>(x.s[0]) * 2};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, static_cast<cuuint32_t>(box_batch)};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(x.ptr), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(PA_ERR_CUDA, "cuTensorMapEncodeTiled failed for %s (CUresult %d)", x.name, int(r));
+  return PA_OK;
+}
+
+// Shared memory of a kernel with a register split, set once per device, and the
+// check that it was built with the register count the split assumes.
+template <typename Kern>
+int ready_kernel(Kern kern, bool* done, int smem_bytes, int regs, const char* what) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (*done) return PA_OK;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaFuncGetAttributes");
+  if (fa.numRegs != regs)
+    return fail(PA_ERR_UNSUPPORTED, "%s kernel built with %d registers per thread, the register split needs %d", what,
+                fa.numRegs, regs);
+  *done = true;
+  return PA_OK;
+}
+
+// Checks shared by the two modified-score entry points.
+int check_scores(int B, int Hq, int Hkv, int Nq, int d, float scale, float softcap, const float* slopes) {
+  if (B < 1 || Hq < 1 || Hkv < 1) return fail(PA_ERR_INVALID_ARG, "B, Hq and Hkv must be >= 1");
+  if (Hq % Hkv) return fail(PA_ERR_INVALID_ARG, "Hq must be a multiple of Hkv (got %d, %d)", Hq, Hkv);
+  if (Nq < 0) return fail(PA_ERR_INVALID_ARG, "Nq must be >= 0 (got %d)", Nq);
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(PA_ERR_INVALID_ARG, "scale must be finite and > 0");
+  if (!std::isfinite(softcap) || softcap < 0.f)
+    return fail(PA_ERR_INVALID_ARG, "softcap must be finite and >= 0 (0: no cap)");
+  if (d != 64 && d != 128) return fail(PA_ERR_UNSUPPORTED, "d must be 64 or 128 (got %d)", d);
+  if (static_cast<long long>(B) * Hq > 65535) return fail(PA_ERR_UNSUPPORTED, "B*Hq must be <= 65535");
+  if (slopes && !aligned(slopes, 4)) return fail(PA_ERR_MISALIGNED, "slopes must be 4-byte aligned");
+  return PA_OK;
+}
+
+pa::mod::ScoreMod score_mod(float scale, float softcap, const float* slopes) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  pa::mod::ScoreMod m;
+  m.scale_log2 = scale * kLog2e;
+  m.cap_k = softcap > 0.f ? 2.f * kLog2e * scale / softcap : 0.f;
+  m.cap_log2 = softcap * kLog2e;
+  m.slopes = slopes;
+  return m;
+}
+
+template <int D, bool kCap, bool kBias>
+int launch_mod(DeviceState* st, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+               const pa::mod::FwdModParams& prm, cudaStream_t stream) {
+  using L = pa::mod::Layout<D>;
+  auto kern = pa::mod::attn_mod_kernel<D, kCap, kBias>;
+  const int rc = ready_kernel(kern, &st->mod_attr[4 * (D == 128) + 2 * kCap + kBias], L::kAllocBytes,
+                              pa::mod::kLaunchRegs, "modified-score forward");
+  if (rc != PA_OK) return rc;
+  const unsigned grid = static_cast<unsigned>(std::min(prm.items, st->sm_count));
+  kern<<<grid, pa::mod::kThreads, L::kAllocBytes, stream>>>(tq, tk, tv, prm);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "attn_mod launch");
+  return PA_OK;
+}
+
+// Calls f with (head dim, capped, biased) as compile-time constants.
+template <typename F>
+int by_mod(int d, bool cap, bool bias, F f) {
+  using std::false_type;
+  using std::true_type;
+  auto with_d = [&](auto dd) {
+    if (cap) return bias ? f(dd, true_type{}, true_type{}) : f(dd, true_type{}, false_type{});
+    return bias ? f(dd, false_type{}, true_type{}) : f(dd, false_type{}, false_type{});
+  };
+  return d == 64 ? with_d(std::integral_constant<int, 64>{}) : with_d(std::integral_constant<int, 128>{});
+}
+
 }  // namespace
 
 extern "C" {
+
+int pa_attn_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Nq,
+                    int Nk, int d, const long long* strides, float scale, const pa_score_mod* mod, void* stream) {
+  g_err[0] = '\0';
+  if (!mod) return fail(PA_ERR_INVALID_ARG, "null pointer argument (mod)");
+  int rc = check_scores(B, Hq, Hkv, Nq, d, scale, mod->softcap, mod->slopes);
+  if (rc != PA_OK) return rc;
+  constexpr int kMaxRows = 1 << 30;
+  if (Nk < 1) return fail(PA_ERR_INVALID_ARG, "Nk must be >= 1 (got %d)", Nk);
+  if (Nk > kMaxRows || Nq > kMaxRows || mod->q_offset > kMaxRows || mod->q_offset < -kMaxRows)
+    return fail(PA_ERR_UNSUPPORTED, "Nq, Nk and |q_offset| must be <= 2^30");
+  if (mod->prefix_lens && !mod->causal) return fail(PA_ERR_INVALID_ARG, "prefix_lens needs the causal mask");
+  if (mod->doc_offsets && mod->n_docs < 1) return fail(PA_ERR_INVALID_ARG, "doc_offsets needs n_docs >= 1");
+  if ((mod->prefix_lens && !aligned(mod->prefix_lens, 4)) || (mod->doc_offsets && !aligned(mod->doc_offsets, 4)))
+    return fail(PA_ERR_MISALIGNED, "prefix_lens and doc_offsets must be 4-byte aligned");
+  if (Nq == 0) return PA_OK;  // an empty tensor may have no address
+  if (!lse) return fail(PA_ERR_INVALID_ARG, "null pointer argument (lse)");
+  if (!aligned(lse, 4)) return fail(PA_ERR_MISALIGNED, "lse must be 4-byte aligned");
+  const Operand oq = operand(q, "q", B, Hq, Nq, d, strides), ok = operand(k, "k", B, Hkv, Nk, d, strides ? strides + 3 : nullptr),
+                ov = operand(v, "v", B, Hkv, Nk, d, strides ? strides + 6 : nullptr),
+                oo = operand(o, "o", B, Hq, Nq, d, strides ? strides + 9 : nullptr);
+  for (const Operand* x : {&oq, &ok, &ov, &oo})
+    if ((rc = check_operand(*x, x == &oo)) != PA_OK) return rc;
+  const uint64_t lse_bytes = static_cast<uint64_t>(B) * Hq * Nq * 4;
+  const int n_docs = mod->doc_offsets ? mod->n_docs : 0;
+  const void* ins[6] = {q, k, v, mod->slopes, mod->prefix_lens, mod->doc_offsets};
+  const uint64_t in_bytes[6] = {extent(oq), extent(ok), extent(ov), static_cast<uint64_t>(Hq) * 4,
+                                static_cast<uint64_t>(B) * std::max(n_docs, 1) * 4,
+                                static_cast<uint64_t>(B) * (n_docs + 1) * 4};
+  for (int i = 0; i < 6; ++i)
+    if (ins[i] && (overlap(ins[i], in_bytes[i], o, extent(oo)) || overlap(ins[i], in_bytes[i], lse, lse_bytes)))
+      return fail(PA_ERR_INVALID_ARG, "outputs overlap an input");
+  if (overlap(o, extent(oo), lse, lse_bytes)) return fail(PA_ERR_INVALID_ARG, "o and lse overlap");
+
+  const void* ptrs[8] = {q, k, v, o, lse};
+  const char* names[8] = {"q", "k", "v", "o", "lse"};
+  int np = 5;
+  if (mod->slopes) ptrs[np] = mod->slopes, names[np++] = "slopes";
+  if (mod->prefix_lens) ptrs[np] = mod->prefix_lens, names[np++] = "prefix_lens";
+  if (mod->doc_offsets) ptrs[np] = mod->doc_offsets, names[np++] = "doc_offsets";
+  DeviceState* st = nullptr;
+  if ((rc = device_checks(ptrs, names, np, &st)) != PA_OK) return rc;
+
+  CUtensorMap tq, tk, tv;
+  if ((rc = encode_map4(&tq, oq, pa::kBM)) != PA_OK || (rc = encode_map4(&tk, ok, pa::kBN)) != PA_OK ||
+      (rc = encode_map4(&tv, ov, pa::kBN)) != PA_OK)
+    return rc;
+  pa::mod::FwdModParams prm;
+  prm.o = static_cast<__nv_bfloat16*>(o);
+  prm.lse = lse;
+  prm.q = static_cast<const __nv_bfloat16*>(q);
+  prm.k = static_cast<const __nv_bfloat16*>(k);
+  prm.v = static_cast<const __nv_bfloat16*>(v);
+  for (int i = 0; i < 3; ++i) {
+    prm.q_s[i] = oq.s[i];
+    prm.k_s[i] = ok.s[i];
+    prm.v_s[i] = ov.s[i];
+    prm.o_s[i] = oo.s[i];
+  }
+  prm.B = B;
+  prm.Hq = Hq;
+  prm.G = Hq / Hkv;
+  prm.Nq = Nq;
+  prm.Nk = Nk;
+  prm.blocks_per_bh = (Nq + pa::kQTiles * pa::kBM - 1) / (pa::kQTiles * pa::kBM);
+  const long long items = static_cast<long long>(prm.blocks_per_bh) * B * Hq;
+  if (items > 0x3fffffffLL) return fail(PA_ERR_UNSUPPORTED, "too many query blocks");
+  prm.items = static_cast<int>(items);
+  prm.q_offset = mod->q_offset;
+  prm.causal = mod->causal != 0;
+  prm.prefix = mod->prefix_lens;
+  prm.docs = mod->doc_offsets;
+  prm.n_docs = n_docs;
+  prm.sm = score_mod(scale, mod->softcap, mod->slopes);
+  prm.status = st->status;
+  prm.timeout_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  return by_mod(d, mod->softcap > 0.f, mod->slopes != nullptr, [&](auto dd, auto cap, auto bias) {
+    return launch_mod<decltype(dd)::value, decltype(cap)::value, decltype(bias)::value>(
+        st, tq, tk, tv, prm, static_cast<cudaStream_t>(stream));
+  });
+}
 
 int pa_attn_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Nq,
                 int Nk, int d, float scale, void* stream) {

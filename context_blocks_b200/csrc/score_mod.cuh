@@ -1,0 +1,318 @@
+// Attention with modified scores: the arithmetic shared by the prefill kernel
+// (attn_mod.cuh) and the shared-prefix decoding kernel (attn_shared.cuh).
+//
+//     s_ij = scale * q_i . k_j
+//     capped:  s_ij <- c * tanh(s_ij / c)
+//     biased:  s_ij <- s_ij - slope_h * |p_i - j|      (p_i: the row's position)
+//     hidden keys:  s_ij <- -inf, chosen by comparison, never added, so that a
+//                   NaN or Inf score of a hidden key does not reach the softmax
+//
+// Everything is kept in log2 units (x = s * log2 e), fp32.  tanh is taken as
+// 1 - 2 / (2^(2 u log2 e) + 1): ex2 and rcp of the special-function unit, whose
+// errors (2^-22 relative) become at most c * 2^-21 in the capped score.  The
+// unit's own tanh has a relative error of 2^-11, which at c = 50 would be 0.02
+// in the exponent.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cfloat>
+#include <cstdint>
+
+#include "fwd_common.cuh"
+
+namespace pa {
+namespace mod {
+
+constexpr int kPParts = 2;                     // P is handed to the MMA warp in two halves
+constexpr uint32_t kSuspendHintNs = 1000000;   // see attn_fwd.cuh; the waits stay bounded
+// Share of the exponentials on the FMA pipe in tiles without hidden keys: 1 in
+// 4 pairs, as in attn_fwd.cuh.  Tiles with hidden keys take all of them on the
+// special-function unit, which gives exactly 0 for -inf (the polynomial gives
+// 2^-126, and a hidden value row may be as large as 2^127).
+constexpr uint32_t kPolyPairs = 0x8888u;
+
+__device__ __forceinline__ uint64_t f2_mul(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Scalars of the score modification, set by the host.
+struct ScoreMod {
+  float scale_log2;     // scale * log2(e)
+  float cap_k;          // 2 * scale * log2(e) / c
+  float cap_log2;       // c * log2(e)
+  const float* slopes;  // [Hq], natural units; read where the kernel is built for a bias
+};
+
+// A row's constants in one tile: dist0 = p_i - (first key of the tile).
+__device__ __forceinline__ float mod_one(float s, const ScoreMod& m, bool cap, bool bias, float slope2, float dist) {
+  float x;
+  if (cap)
+    x = fmaf(rcp_approx(ex2_approx(s * m.cap_k) + 1.f), -2.f * m.cap_log2, m.cap_log2);
+  else
+    x = s * m.scale_log2;
+  if (bias) x = fmaf(-slope2, fabsf(dist), x);
+  return x;
+}
+
+// One 128-key tile of one row a thread: S from tensor memory at tS, P (bf16
+// pairs) written back over it and handed over in two halves.  The row sees
+// keys [a, b) of the tile.  m_ref, l: the row's running reference maximum and
+// sum; tO: its O accumulator, rescaled when the maximum moves (`have_o`: it
+// holds something).  A row that has seen nothing keeps m_ref = -inf and l = 0.
+template <int D, bool kCap, bool kBias>
+__device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int a, int b, float dist0, float slope2,
+                                             const ScoreMod& sm, bool have_o, float& m_ref, float& l,
+                                             uint32_t bar_part, uint32_t bar_full, int lane) {
+  constexpr bool kMod = kCap || kBias;
+  uint32_t sr[kBN];
+  tmem_ld_x128(tS, sr);
+  float s[kBN];
+#pragma unroll
+  for (int e = 0; e < kBN; ++e) s[e] = __uint_as_float(sr[e]);
+  const float c = sm.scale_log2;
+  if constexpr (kMod) {
+    // The distance is linear in the key on either side of the row's own
+    // position, so a tile that does not hold it needs one packed FMA a pair.
+    float sl = slope2;
+    bool linear = true;
+    if constexpr (kBias) {
+      if (dist0 <= 0.f) sl = -slope2;
+      linear = __all_sync(0xffffffffu, dist0 <= 0.f || dist0 >= static_cast<float>(kBN - 1));
+    }
+    const uint64_t c2 = f2(c, c), ck2 = f2(sm.cap_k, sm.cap_k);
+    const uint64_t cl2 = f2(sm.cap_log2, sm.cap_log2), m2cl2 = f2(-2.f * sm.cap_log2, -2.f * sm.cap_log2);
+    const uint64_t one2 = f2(1.f, 1.f);
+    const uint64_t sl2 = f2(sl, sl), b02 = f2(-sl * dist0, -sl * dist0);
+#pragma unroll
+    for (int e = 0; e < kBN; e += 2) {
+      uint64_t x;
+      if constexpr (kCap) {
+        float u0, u1;
+        f2_split(f2_mul(f2(s[e], s[e + 1]), ck2), u0, u1);
+        f2_split(f2_add(f2(ex2_approx(u0), ex2_approx(u1)), one2), u0, u1);
+        x = f2_fma(f2(rcp_approx(u0), rcp_approx(u1)), m2cl2, cl2);
+        if constexpr (kBias)
+          if (linear) x = f2_add(x, f2_fma(sl2, f2(static_cast<float>(e), static_cast<float>(e + 1)), b02));
+      } else {
+        x = linear ? f2_fma(f2(s[e], s[e + 1]), c2,
+                            f2_fma(sl2, f2(static_cast<float>(e), static_cast<float>(e + 1)), b02))
+                   : f2_mul(f2(s[e], s[e + 1]), c2);
+      }
+      f2_split(x, s[e], s[e + 1]);
+    }
+    if (kBias && !linear) {
+#pragma unroll
+      for (int e = 0; e < kBN; ++e) s[e] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(e)), s[e]);
+    }
+  }
+  const bool edge = __any_sync(0xffffffffu, a > 0 || b < kBN);
+  if (edge) {
+#pragma unroll
+    for (int e = 0; e < kBN; ++e)
+      if (e < a || e >= b) s[e] = -INFINITY;
+  }
+  float m8[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) m8[k] = fmaxf(s[k], s[k + 8]);
+#pragma unroll
+  for (int e = 16; e < kBN; e += 16)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m8[k] = max3f(m8[k], s[e + k], s[e + 8 + k]);
+  float mx = fmaxf(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], max3f(m8[5], m8[6], m8[7])));
+  if constexpr (!kMod) mx *= c;
+  float alpha = 1.f;
+  bool rescale = false;
+  if (mx > m_ref + kRescaleLog2) {
+    alpha = ex2_approx(m_ref - mx);  // 0 when the row was empty (m_ref = -inf)
+    l *= alpha;
+    m_ref = mx;
+    rescale = have_o;
+  }
+  if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+    for (int ch = 0; ch < D / 32; ++ch) {
+      uint32_t orr[32];
+      tmem_ld_x32(tO + ch * 32, orr);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+      tmem_st_x32(tO + ch * 32, orr);
+    }
+  }
+  // x - m_ref stays -inf (not NaN) where the row has seen nothing so far.
+  const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
+  const float mul = kMod ? 1.f : c;
+  const uint64_t mul2 = f2(mul, mul), nm2 = f2(neg_m, neg_m);
+  uint64_t l4[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+  auto pass = [&](auto with_poly) {
+#pragma unroll
+    for (int ch = 0; ch < kBN / 32; ++ch) {
+      uint32_t pk[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const uint64_t s2 = f2(s[ch * 32 + 2 * e], s[ch * 32 + 2 * e + 1]);
+        const uint64_t x2 = kMod ? f2_add(s2, nm2) : f2_fma(s2, mul2, nm2);
+        float p0, p1;
+        if (with_poly() && ((kPolyPairs >> e) & 1)) {
+          f2_split(exp2_poly3_x2(x2), p0, p1);
+        } else {
+          float x0, x1;
+          f2_split(x2, x0, x1);
+          p0 = ex2_approx(x0);
+          p1 = ex2_approx(x1);
+        }
+        l4[e & 3] = f2_add(l4[e & 3], f2(p0, p1));
+        pk[e] = pack_bf16x2(p0, p1);
+      }
+      tmem_st_x16(tS + ch * 16, pk);
+      constexpr int kChPerPart = (kBN / 32) / kPParts;
+      if ((ch + 1) % kChPerPart == 0 && ch + 1 < kBN / 32) {
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_part);
+      }
+    }
+  };
+  if (edge)
+    pass([] { return false; });
+  else
+    pass([] { return true; });
+  const uint64_t sum = f2_add(f2_add(l4[0], l4[1]), f2_add(l4[2], l4[3]));
+  float s0, s1;
+  f2_split(sum, s0, s1);
+  l += s0 + s1;
+  tmem_st_wait();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar_full);
+}
+
+// Scale a thread's O row (TMEM columns [tO, tO + D)) by `inv` and store it,
+// through the warp's 4 KB staging area (see attn_fwd.cuh), as bf16 or, where
+// o_bf16 is null, as fp32.  Row r of the warp is at dst0 + r * row_stride
+// elements; rows r >= rows_left are not written.  inv = 0 stores zeros
+// whatever the accumulator holds.  Returns whether this thread's row has a
+// value that is not finite.
+template <int D>
+__device__ __noinline__ bool store_rows(uint32_t tO, uint32_t stg, __nv_bfloat16* o_bf16, float* o_f32,
+                                        long long row_stride, int rows_left, float inv) {
+  const int lane = threadIdx.x % 32;
+  const int r0 = lane >> 3, c = lane & 7;
+  float bad = 0.f;  // x * 0 is NaN where x is not finite
+  auto value = [&](uint32_t w) {
+    const float x = __uint_as_float(w);
+    bad = fmaf(x, 0.f, bad);
+    return inv == 0.f ? 0.f : x * inv;
+  };
+  auto stage4 = [&](int c0, const uint32_t (&w)[16]) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      st_shared_v4(stg + lane * 128 + (((c0 + u) ^ (lane & 7)) << 4), w[4 * u], w[4 * u + 1], w[4 * u + 2],
+                   w[4 * u + 3]);
+  };
+  auto drain = [&](uint8_t* dst, long long row_bytes) {
+    dst += r0 * row_bytes + c * 16;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = 4 * k + r0;
+      const uint4 x = ld_shared_v4(stg + r * 128 + ((c ^ (r & 7)) << 4));
+      if (r < rows_left) *reinterpret_cast<uint4*>(dst + k * 4 * row_bytes) = x;
+    }
+  };
+  if (o_bf16 != nullptr) {
+#pragma unroll 1
+    for (int h = 0; h < D / 64; ++h) {
+      __syncwarp();
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        uint32_t orr[32], pk[16];
+        tmem_ld_x32(tO + h * 64 + hh * 32, orr);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(value(orr[2 * e]), value(orr[2 * e + 1]));
+        stage4(4 * hh, pk);
+      }
+      __syncwarp();
+      drain(reinterpret_cast<uint8_t*>(o_bf16 + h * 64), row_stride * 2);
+    }
+  } else {
+#pragma unroll 1
+    for (int ch = 0; ch < D / 32; ++ch) {
+      uint32_t orr[32];
+      tmem_ld_x32(tO + ch * 32, orr);
+      __syncwarp();
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(value(orr[16 * hh + e]));
+        stage4(4 * hh, w);
+      }
+      __syncwarp();
+      drain(reinterpret_cast<uint8_t*>(o_f32 + ch * 32), row_stride * 4);
+    }
+  }
+  return !(bad == 0.f);
+}
+
+// Recompute one output row with the whole warp, reading only the keys [j0, j1)
+// the row sees.  The tensor cores multiply the zero weight of a hidden key with
+// its value row, so a hidden value that is NaN or Inf would reach the row; a
+// row whose accumulator is not finite is therefore done again here, with the
+// maximum m and sum the softmax found (hidden scores never entered those).
+// Rare and slow (about 40 instructions a key); q, k, v: the row's query, and
+// key and value row 0 of its head.  pos: the row's position among the keys.
+template <int D>
+__device__ __noinline__ void repair_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
+                                        long long k_stride, long long v_stride, int j0, int j1, int pos, float m,
+                                        float inv, float slope2, ScoreMod sm, bool cap, bool bias,
+                                        __nv_bfloat16* o_bf16, float* o_f32) {
+  constexpr int kCols = D / 32;
+  const int lane = threadIdx.x % 32;
+  float qv[kCols], acc[kCols];
+#pragma unroll
+  for (int u = 0; u < kCols; ++u) {
+    qv[u] = __bfloat162float(q[lane * kCols + u]);
+    acc[u] = 0.f;
+  }
+  for (int j = j0; j < j1; ++j) {
+    const __nv_bfloat16* kr = k + j * k_stride + lane * kCols;
+    const __nv_bfloat16* vr = v + j * v_stride + lane * kCols;
+    float dot = 0.f;
+#pragma unroll
+    for (int u = 0; u < kCols; ++u) dot = fmaf(qv[u], __bfloat162float(kr[u]), dot);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    const float p = ex2_approx(mod_one(dot, sm, cap, bias, slope2, static_cast<float>(pos - j)) - m);
+#pragma unroll
+    for (int u = 0; u < kCols; ++u) acc[u] = fmaf(p, __bfloat162float(vr[u]), acc[u]);
+  }
+#pragma unroll
+  for (int u = 0; u < kCols; ++u) {
+    if (o_bf16 != nullptr)
+      o_bf16[lane * kCols + u] = __float2bfloat16(acc[u] * inv);
+    else
+      o_f32[lane * kCols + u] = acc[u] * inv;
+  }
+}
+
+// 4-D tiled load (coordinates innermost first); c0 * element size must be a
+// multiple of 16 bytes.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                            int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+
+}  // namespace mod
+}  // namespace pa

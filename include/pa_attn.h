@@ -249,6 +249,56 @@ int pa_attn_merge(const void* o_parts, const float* lse_parts, int n_parts, void
                   int B, int H, int N, int d, void* stream);
 
 /*
+ * Modification of the attention scores and the mask (pa_attn_fwd_mod).  A zeroed
+ * structure is plain, unmasked attention.
+ */
+typedef struct pa_score_mod {
+  float softcap;          /* c > 0: s <- c * tanh(s / c); 0: no cap */
+  int causal;             /* non-zero: a row sees no key behind its own position,
+                             those of its prefix apart */
+  const float* slopes;    /* [Hq] fp32, device, finite: s <- s - slopes[h] * |p_i - j|; or NULL */
+  const int* prefix_lens; /* [B] (or [B, n_docs] with documents), device: with causal, the
+                             first so many keys (of the document) are seen by all rows
+                             (of the document); or NULL */
+  const int* doc_offsets; /* [B, n_docs + 1], device, non-decreasing in each row: document t of
+                             batch b holds the keys doc_offsets[b][t] <= j < doc_offsets[b][t+1];
+                             a row sees the keys of its own document only; or NULL */
+  int n_docs;             /* >= 1 with doc_offsets, ignored without */
+  int q_offset;           /* row i stands at position p_i = i + q_offset among the keys */
+} pa_score_mod;
+
+/*
+ * pa_attn_fwd_mod - attention with capped and biased scores and interval masks.
+ *
+ * For each b < B, h < Hq and query row i < Nq, with h' = h / (Hq / Hkv):
+ *     s_ij  = scale * sum_c q[b,h,i,c] k[b,h',j,c], capped, then biased as
+ *             pa_score_mod says
+ *     lse[i] = ln sum_j exp(s_ij),  o[i,:] = sum_j exp(s_ij - lse[i]) v[b,h',j,:]
+ * over the keys j that row i sees.  A row that sees none (its mask leaves
+ * nothing, or its position lies in no document) gets o = 0 and lse = -inf,
+ * which pa_attn_merge takes as a part of no weight.  Keys that a row does not
+ * see do not reach it, whatever they hold (NaN and Inf included).  Offsets and
+ * prefix lengths are read on the device; values out of range are clamped to
+ * the keys, and offsets that decrease give undefined results, never a fault.
+ *
+ * q, o   [B,Hq,Nq,d] bf16      k, v  [B,Hkv,Nk,d] bf16, Hq a multiple of Hkv
+ * lse    [B,Hq,Nq] fp32, contiguous
+ * strides  host array of 12: element strides of the batch, head and row
+ *        dimensions of q, k, v and o, in this order; or NULL where all four are
+ *        contiguous.  Positive multiples of 8 (that of a dimension of one entry
+ *        is ignored); the last dimension is contiguous.  o's rows must not
+ *        overlap one another, nor the range of o that of an input.
+ * B*Hq <= 65535; Nq >= 0 (0 is a no-op); Nk >= 1; Nq, Nk, |q_offset| <= 2^30
+ *        (distances are exact up to 2^24)
+ * d      64 or 128;  scale  finite and > 0
+ *
+ * Errors: as pa_attn_fwd; PA_ERR_INVALID_ARG for a bad cap, prefix_lens without
+ * causal, bad strides and overlapping buffers.
+ */
+int pa_attn_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Nq,
+                    int Nk, int d, const long long* strides, float scale, const pa_score_mod* mod, void* stream);
+
+/*
  * pa_residual_diff - First Block Cache's residual difference.
  *
  * diffusers "ParaAttention" guide, section "First Block Cache": the change of
