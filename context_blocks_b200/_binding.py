@@ -41,6 +41,8 @@ SIGNATURES = {
     "pa_attn_merge": (_I, [_VP, _VP, _I, _VP, _VP, _I, _I, _I, _I, _VP]),
     "pa_attn_chunks_noalloc": (_I, [_VP, _VP, _VP, _VP, _I, _VP, _VP, _I, _I, _I, _I, _F, _VP]),
     "pa_attn_fwd_mod": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _VP, _F, _VP, _VP]),
+    "pa_attn_shared_prefix": (_I, [_VP] * 8 + [_I] * 7 + [_VP, _F, _F, _VP, _VP, ctypes.c_size_t, _VP]),
+    "pa_attn_shared_prefix_workspace": (ctypes.c_size_t, [_I] * 7),
     "pa_residual_diff": (_I, [_VP, _VP, ctypes.c_longlong, _VP, _VP]),
     "pa_status_string": (ctypes.c_char_p, [_I]),
     "pa_last_error": (ctypes.c_char_p, []),
@@ -392,6 +394,66 @@ def attn_fwd_mod(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, s
                                          Hq, Hkv, Nq, Nk, d, strides, float(scale), ctypes.byref(mod),
                                          _stream_handle(stream, q.device))
     _check(rc, "pa_attn_fwd_mod", check)
+    return out, lse
+
+
+def shared_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Np: int, Nt: int, d: int) -> int:
+    """Bytes of workspace ``attn_shared_prefix`` needs for these sizes."""
+    return int(load_library().pa_attn_shared_prefix_workspace(B, Hq, Hkv, Nq, Np, Nt, d))
+
+
+def attn_shared_prefix(q, k_prefix, v_prefix, k_tail, v_tail, tail_lens, scale: Optional[float] = None,
+                       softcap: float = 0.0, slopes=None, out=None, lse=None, workspace=None, stream=None,
+                       check: bool = False):
+    """A decoding step of B requests that share a prefix
+    (``pa_attn_shared_prefix``): q [B,Hq,Nq,d] (contiguous) against the prefix
+    k_prefix, v_prefix [Hkv,Np,d], read once for all requests, and each
+    request's own k_tail, v_tail [B,Hkv,Nt,d] up to tail_lens [B] int32, the
+    new tokens' own keys being the last Nq of them.  ``softcap`` and ``slopes``
+    as in ``attn_fwd_mod``.  ``workspace`` (uint8, at least
+    ``shared_prefix_workspace_bytes``) is allocated when not given; two calls
+    that may overlap on the GPU need one each.  Returns (o, lse).
+    """
+    import torch
+    _check_bf16("q", q, 4)
+    _check_rows("k_prefix", k_prefix, 3, q.device)
+    _check_rows("v_prefix", v_prefix, 3, q.device)
+    _check_rows("k_tail", k_tail, 4, q.device)
+    _check_rows("v_tail", v_tail, 4, q.device)
+    B, Hq, Nq, d = q.shape
+    Hkv, Np = k_prefix.shape[:2]
+    Nt = k_tail.shape[2]
+    if (k_prefix.shape[2] != d or v_prefix.shape != k_prefix.shape or tuple(k_tail.shape) != (B, Hkv, Nt, d)
+            or v_tail.shape != k_tail.shape or Hkv < 1 or Hq % Hkv):
+        raise ValueError(f"shape mismatch: q {tuple(q.shape)}, prefix {tuple(k_prefix.shape)} and "
+                         f"{tuple(v_prefix.shape)}, tail {tuple(k_tail.shape)} and {tuple(v_tail.shape)}")
+    lens = _check_vector("tail_lens", tail_lens, torch.int32, (B,), q.device)
+    sl = _check_vector("slopes", slopes, torch.float32, (Hq,), q.device)
+    lib = load_library()
+    need = int(lib.pa_attn_shared_prefix_workspace(B, Hq, Hkv, Nq, Np, Nt, d))
+    with _allocating_for(stream, q.device):
+        if out is None:
+            out = torch.empty((B, Hq, Nq, d), dtype=torch.bfloat16, device=q.device)
+        lse = _lse_out(lse, (B, Hq, Nq), q.device)
+        if workspace is None:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    _check_bf16("out", out, 4)
+    if out.shape != q.shape or out.device != q.device:
+        raise ValueError("out must have q's shape and device")
+    if not isinstance(workspace, torch.Tensor) or workspace.device != q.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    strides = None
+    if not (k_prefix.is_contiguous() and v_prefix.is_contiguous() and k_tail.is_contiguous()
+            and v_tail.is_contiguous()):
+        strides = (ctypes.c_longlong * 10)(*k_prefix.stride()[:2], *v_prefix.stride()[:2], *k_tail.stride()[:3],
+                                           *v_tail.stride()[:3])
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    rc = lib.pa_attn_shared_prefix(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_tail.data_ptr(),
+                                   v_tail.data_ptr(), lens, out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, Np, Nt, d,
+                                   strides, float(scale), float(softcap), sl, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream_handle(stream, q.device))
+    _check(rc, "pa_attn_shared_prefix", check)
     return out, lse
 
 

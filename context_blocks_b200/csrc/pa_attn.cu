@@ -15,6 +15,7 @@
 
 #include "attn_fwd.cuh"
 #include "attn_mod.cuh"
+#include "attn_shared.cuh"
 #include "quantize.cuh"
 #include "fwd_common.cuh"
 #include "lse_merge.cuh"
@@ -78,6 +79,7 @@ struct DeviceState {
   unsigned char* noalloc_scratch = nullptr;  // device address of pa::g_noalloc_scratch
   bool fwd_attr[5] = {};  // d = 64, d = 128, e4m3 d = 128, accumulate d = 64, accumulate d = 128
   bool mod_attr[8] = {};  // modified scores: 4 * (d = 128) + 2 * capped + biased
+  bool shared_attr[8] = {};  // shared prefix: the same
 };
 
 
@@ -524,9 +526,166 @@ int by_mod(int d, bool cap, bool bias, F f) {
   return d == 64 ? with_d(std::integral_constant<int, 64>{}) : with_d(std::integral_constant<int, 128>{});
 }
 
+// Shapes of a shared-prefix call; false where the rows of one request under one
+// K/V head do not fit a row tile.
+bool shared_plan(int B, int Hq, int Hkv, int Nq, int Np, int Nt, int ctas, pa::shared::Plan* plan) {
+  const long long rows = static_cast<long long>(Hq / Hkv) * Nq;
+  if (rows < 1 || rows > pa::kBM) return false;
+  plan->B = B;
+  plan->Hq = Hq;
+  plan->Hkv = Hkv;
+  plan->G = Hq / Hkv;
+  plan->Nq = Nq;
+  plan->rows = static_cast<int>(rows);
+  plan->tile_reqs = std::min(B, pa::kBM / plan->rows);
+  plan->row_tiles = (B + plan->tile_reqs - 1) / plan->tile_reqs;
+  plan->pairs = (plan->row_tiles + 1) / 2;
+  plan->Np = Np;
+  plan->Nt = Nt;
+  plan->prefix_tiles = (Np + pa::kBN - 1) / pa::kBN;
+  plan->prefix_segs = Np > 0 ? Hkv * plan->pairs : 0;
+  plan->ctas = ctas;
+  plan->tail_lens = nullptr;
+  return true;
+}
+
+// Byte offsets of the four parts of a shared-prefix workspace (each on a
+// 256-byte boundary), and their end.
+struct SharedWorkspace {
+  uint64_t prefix_o, prefix_lse, tail_o, tail_lse, end;
+};
+
+SharedWorkspace shared_workspace(const pa::shared::Plan& plan, int d) {
+  auto up = [](uint64_t n) { return (n + 255) & ~255ull; };
+  const uint64_t pre =
+      plan.prefix_segs ? 2ull * (plan.prefix_segs + pa::shared::kMaxCtas) * plan.tile_reqs * plan.rows : 0;
+  const uint64_t tail =
+      plan.Nt > 0 ? 2ull * (static_cast<uint64_t>(plan.B) * plan.Hkv + pa::shared::kMaxCtas) * plan.rows : 0;
+  SharedWorkspace w;
+  w.prefix_o = 0;
+  w.prefix_lse = up(pre * d * 4);
+  w.tail_o = w.prefix_lse + up(pre * 4);
+  w.tail_lse = w.tail_o + up(tail * d * 4);
+  w.end = w.tail_lse + up(tail * 4);
+  return w;
+}
+
+template <int D, bool kCap, bool kBias>
+int launch_shared(DeviceState* st, const CUtensorMap (&maps)[6], const pa::shared::Params& prm, void* o, float* lse,
+                  cudaStream_t stream) {
+  using L = pa::shared::SharedLayout<D>;
+  auto kern = pa::shared::attn_shared_kernel<D, kCap, kBias>;
+  const int rc = ready_kernel(kern, &st->shared_attr[4 * (D == 128) + 2 * kCap + kBias], L::kAllocBytes,
+                              pa::mod::kLaunchRegs, "shared-prefix");
+  if (rc != PA_OK) return rc;
+  if (prm.plan.Np > 0 || prm.plan.Nt > 0)
+    kern<<<prm.plan.ctas, pa::mod::kThreads, L::kAllocBytes, stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4],
+                                                                       maps[5], prm);
+  pa::shared::shared_merge_kernel<D><<<prm.plan.B * prm.plan.Hkv, pa::shared::kMergeWarps * 32, 0, stream>>>(
+      prm, static_cast<__nv_bfloat16*>(o), lse);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "attn_shared launch");
+  return PA_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t pa_attn_shared_prefix_workspace(int B, int Hq, int Hkv, int Nq, int Np, int Nt, int d) {
+  pa::shared::Plan plan;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Nq < 1 || Np < 0 || Nt < 0 || (d != 64 && d != 128) ||
+      static_cast<long long>(B) * Hq > 65535 || !shared_plan(B, Hq, Hkv, Nq, Np, Nt, 1, &plan))
+    return 0;
+  return static_cast<size_t>(shared_workspace(plan, d).end);
+}
+
+int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k_tail,
+                          const void* v_tail, const int* tail_lens, void* o, float* lse, int B, int Hq, int Hkv, int Nq,
+                          int Np, int Nt, int d, const long long* strides, float scale, float softcap,
+                          const float* slopes, void* workspace, size_t workspace_bytes, void* stream) {
+  g_err[0] = '\0';
+  int rc = check_scores(B, Hq, Hkv, Nq, d, scale, softcap, slopes);
+  if (rc != PA_OK) return rc;
+  constexpr int kMaxRows = 1 << 30;
+  if (Np < 0 || Nt < 0) return fail(PA_ERR_INVALID_ARG, "Np and Nt must be >= 0 (got %d, %d)", Np, Nt);
+  if (Np > kMaxRows || Nt > kMaxRows - Np) return fail(PA_ERR_UNSUPPORTED, "Np + Nt must be <= 2^30");
+  if (Nq == 0) return PA_OK;
+  pa::shared::Plan plan;
+  if (!shared_plan(B, Hq, Hkv, Nq, Np, Nt, 1, &plan))
+    return fail(PA_ERR_UNSUPPORTED, "(Hq / Hkv) * Nq must be <= %d", pa::kBM);
+  if (!tail_lens || !lse) return fail(PA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(tail_lens, 4) || !aligned(lse, 4))
+    return fail(PA_ERR_MISALIGNED, "tail_lens and lse must be 4-byte aligned");
+  // A part of no keys has no address; what stands for it is never read.
+  const long long ps[4] = {strides ? strides[0] : 0, strides ? strides[1] : 0, strides ? strides[2] : 0,
+                           strides ? strides[3] : 0};
+  const long long kp_s[3] = {d, ps[0], ps[1]}, vp_s[3] = {d, ps[2], ps[3]};
+  const Operand oq = operand(q, "q", B, Hkv, plan.rows, d, nullptr), oo = operand(o, "o", B, Hq, Nq, d, nullptr);
+  const Operand kp = Np ? operand(k_prefix, "k_prefix", 1, Hkv, Np, d, strides ? kp_s : nullptr) : oq;
+  const Operand vp = Np ? operand(v_prefix, "v_prefix", 1, Hkv, Np, d, strides ? vp_s : nullptr) : oq;
+  const Operand kt = Nt ? operand(k_tail, "k_tail", B, Hkv, Nt, d, strides ? strides + 4 : nullptr) : oq;
+  const Operand vt = Nt ? operand(v_tail, "v_tail", B, Hkv, Nt, d, strides ? strides + 7 : nullptr) : oq;
+  for (const Operand* x : {&oq, &oo, &kp, &vp, &kt, &vt})
+    if ((rc = check_operand(*x, false)) != PA_OK) return rc;
+  const SharedWorkspace ws = shared_workspace(plan, d);
+  if (ws.end > 0) {
+    if (!workspace) return fail(PA_ERR_INVALID_ARG, "null pointer argument (workspace)");
+    if (!aligned(workspace, 16)) return fail(PA_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    if (workspace_bytes < ws.end)
+      return fail(PA_ERR_INVALID_ARG, "the workspace needs %llu bytes (got %llu)", static_cast<unsigned long long>(ws.end),
+                  static_cast<unsigned long long>(workspace_bytes));
+  }
+  const uint64_t lse_bytes = static_cast<uint64_t>(B) * Hq * Nq * 4;
+  const void* ins[7] = {q, kp.ptr, vp.ptr, kt.ptr, vt.ptr, tail_lens, slopes};
+  const uint64_t in_bytes[7] = {extent(oq), extent(kp), extent(vp), extent(kt), extent(vt),
+                                static_cast<uint64_t>(B) * 4, static_cast<uint64_t>(Hq) * 4};
+  for (int i = 0; i < 7; ++i)
+    if (ins[i] && (overlap(ins[i], in_bytes[i], o, extent(oo)) || overlap(ins[i], in_bytes[i], lse, lse_bytes) ||
+                   (ws.end && overlap(ins[i], in_bytes[i], workspace, ws.end))))
+      return fail(PA_ERR_INVALID_ARG, "outputs or workspace overlap an input");
+  if (overlap(o, extent(oo), lse, lse_bytes) ||
+      (ws.end && (overlap(o, extent(oo), workspace, ws.end) || overlap(lse, lse_bytes, workspace, ws.end))))
+    return fail(PA_ERR_INVALID_ARG, "o, lse and workspace overlap");
+
+  const void* ptrs[10] = {q, kp.ptr, vp.ptr, kt.ptr, vt.ptr, tail_lens, o, lse};
+  const char* names[10] = {"q", "k_prefix", "v_prefix", "k_tail", "v_tail", "tail_lens", "o", "lse"};
+  int np = 8;
+  if (slopes) ptrs[np] = slopes, names[np++] = "slopes";
+  if (ws.end) ptrs[np] = workspace, names[np++] = "workspace";
+  DeviceState* st = nullptr;
+  if ((rc = device_checks(ptrs, names, np, &st)) != PA_OK) return rc;
+  plan.ctas = std::min(st->sm_count, pa::shared::kMaxCtas);
+  plan.tail_lens = tail_lens;
+
+  CUtensorMap maps[6];
+  if ((rc = encode_map4(&maps[0], oq, plan.rows, plan.tile_reqs)) != PA_OK ||
+      (rc = encode_map4(&maps[1], oq, plan.rows, 1)) != PA_OK || (rc = encode_map4(&maps[2], kp, pa::kBN)) != PA_OK ||
+      (rc = encode_map4(&maps[3], vp, pa::kBN)) != PA_OK || (rc = encode_map4(&maps[4], kt, pa::kBN)) != PA_OK ||
+      (rc = encode_map4(&maps[5], vt, pa::kBN)) != PA_OK)
+    return rc;
+  pa::shared::Params prm;
+  prm.plan = plan;
+  prm.q = static_cast<const __nv_bfloat16*>(q);
+  prm.kt = static_cast<const __nv_bfloat16*>(kt.ptr);
+  prm.vt = static_cast<const __nv_bfloat16*>(vt.ptr);
+  for (int i = 0; i < 3; ++i) {
+    prm.kt_s[i] = kt.s[i];
+    prm.vt_s[i] = vt.s[i];
+  }
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  prm.prefix_o = reinterpret_cast<float*>(w + ws.prefix_o);
+  prm.prefix_lse = reinterpret_cast<float*>(w + ws.prefix_lse);
+  prm.tail_o = reinterpret_cast<float*>(w + ws.tail_o);
+  prm.tail_lse = reinterpret_cast<float*>(w + ws.tail_lse);
+  prm.sm = score_mod(scale, softcap, slopes);
+  prm.status = st->status;
+  prm.timeout_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  return by_mod(d, softcap > 0.f, slopes != nullptr, [&](auto dd, auto cap, auto bias) {
+    return launch_shared<decltype(dd)::value, decltype(cap)::value, decltype(bias)::value>(
+        st, maps, prm, o, lse, static_cast<cudaStream_t>(stream));
+  });
+}
 
 int pa_attn_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Nq,
                     int Nk, int d, const long long* strides, float scale, const pa_score_mod* mod, void* stream) {

@@ -52,6 +52,8 @@
 #ifndef PA_ATTN_H_
 #define PA_ATTN_H_
 
+#include <stddef.h>
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -297,6 +299,49 @@ typedef struct pa_score_mod {
  */
 int pa_attn_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Nq,
                     int Nk, int d, const long long* strides, float scale, const pa_score_mod* mod, void* stream);
+
+/*
+ * pa_attn_shared_prefix - a decoding step of B requests that share a prefix.
+ *
+ * Request b has the Np keys of the prefix, held once for all requests, and
+ * len_b = tail_lens[b] keys of its own, of which the last Nq are its new
+ * tokens' (their K and V already in the tail).  Token t of request b stands at
+ * position Np + len_b - Nq + t and sees the whole prefix and the tail keys
+ * j <= len_b - Nq + t; the tail's keys stand at Np + j.  Scores are scaled,
+ * capped and biased as in pa_attn_fwd_mod:
+ *     lse = ln sum exp(s),  o = sum exp(s - lse) v     over the keys it sees.
+ * A token that sees none (no prefix and an empty tail) gets o = 0 and
+ * lse = -inf.  Tail entries at len_b and behind it are not read into any
+ * result, whatever they hold.
+ *
+ * q, o       [B,Hq,Nq,d] bf16, contiguous;  lse [B,Hq,Nq] fp32
+ * k_prefix, v_prefix  [Hkv,Np,d] bf16  (not read with Np = 0, may be NULL)
+ * k_tail, v_tail      [B,Hkv,Nt,d] bf16  (not read with Nt = 0, may be NULL)
+ * tail_lens  [B] int32, device, 0 <= tail_lens[b] <= Nt; read on the device,
+ *            where a value outside is clamped and raises PA_ERR_BAD_INPUT in
+ *            the device status word
+ * strides    host array of 10: element strides of k_prefix (head, row), v_prefix
+ *            (head, row), k_tail (batch, head, row), v_tail (batch, head, row);
+ *            or NULL where all are contiguous.  Positive multiples of 8.
+ * slopes     [Hq] fp32, device, or NULL;  softcap 0: no cap
+ * workspace  device, 16-byte aligned, at least
+ *            pa_attn_shared_prefix_workspace() bytes: the partial results of
+ *            the call.  It needs no clearing; calls that overlap on the GPU
+ *            need one each.
+ * Hq a multiple of Hkv; (Hq / Hkv) * Nq <= 128; B*Hq <= 65535; Nq >= 0 (0 is a
+ * no-op); Np + Nt <= 2^30; d 64 or 128.
+ *
+ * Two launches on `stream`.  Errors: as pa_attn_fwd_mod; PA_ERR_INVALID_ARG for
+ * a missing or small workspace.
+ */
+int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k_tail,
+                          const void* v_tail, const int* tail_lens, void* o, float* lse, int B, int Hq, int Hkv, int Nq,
+                          int Np, int Nt, int d, const long long* strides, float scale, float softcap,
+                          const float* slopes, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that pa_attn_shared_prefix needs for these sizes (a host
+ * computation); 0 where it needs none or the sizes are not supported. */
+size_t pa_attn_shared_prefix_workspace(int B, int Hq, int Hkv, int Nq, int Np, int Nt, int d);
 
 /*
  * pa_residual_diff - First Block Cache's residual difference.
