@@ -43,6 +43,7 @@ SIGNATURES = {
     "pa_attn_fwd_mod": (_I, [_VP, _VP, _VP, _VP, _VP, _I, _I, _I, _I, _I, _I, _VP, _F, _VP, _VP]),
     "pa_attn_shared_prefix": (_I, [_VP] * 8 + [_I] * 7 + [_VP, _F, _F, _VP, _VP, ctypes.c_size_t, _VP]),
     "pa_attn_shared_prefix_workspace": (ctypes.c_size_t, [_I] * 7),
+    "pa_gate_residual_norm": (_I, [_VP, _VP, _VP, _VP, _I, _I, _I, _I, _VP, _VP]),
     "pa_residual_diff": (_I, [_VP, _VP, ctypes.c_longlong, _VP, _VP]),
     "pa_status_string": (ctypes.c_char_p, [_I]),
     "pa_last_error": (ctypes.c_char_p, []),
@@ -58,6 +59,17 @@ class ScoreMod(ctypes.Structure):
 
     _fields_ = [("softcap", _F), ("causal", _I), ("slopes", _VP), ("prefix_lens", _VP), ("doc_offsets", _VP),
                 ("n_docs", _I), ("q_offset", _I)]
+
+
+class BlockNorm(ctypes.Structure):
+    """``pa_block_norm`` of include/pa_attn.h."""
+
+    _fields_ = [("post", _I), ("norm", _I), ("post_weight", _VP), ("norm_weight", _VP), ("gate", _VP), ("scale", _VP),
+                ("shift", _VP), ("gate_stride", ctypes.c_longlong), ("scale_stride", ctypes.c_longlong),
+                ("shift_stride", ctypes.c_longlong), ("residual_scale", _F), ("eps", _F)]
+
+
+PA_NORM = {"none": 0, "rms": 1, "layer": 2}
 
 
 class PaError(RuntimeError):
@@ -455,6 +467,60 @@ def attn_shared_prefix(q, k_prefix, v_prefix, k_tail, v_tail, tail_lens, scale: 
                                    workspace.numel() * workspace.element_size(), _stream_handle(stream, q.device))
     _check(rc, "pa_attn_shared_prefix", check)
     return out, lse
+
+
+def gate_residual_norm(y, x, gate=None, post: str = "none", post_weight=None, norm: str = "rms", norm_weight=None,
+                       scale=None, shift=None, residual_scale: float = 1.0, eps: float = 1e-6, x_out=None, out=None,
+                       stream=None, check: bool = False):
+    """A block's gated residual update with the norms around it
+    (``pa_gate_residual_norm``), in one pass over the data:
+
+        x_new = residual_scale * x + gate * post(y) * post_weight
+        h = norm(x_new) * norm_weight * (1 + scale) + shift
+
+    y [B,N,D] bf16, x [B,N,D] bf16 or float32 (the residual stream), gate,
+    scale, shift [B,D] bf16 (slices of one wider modulation tensor are taken as
+    they are), weights [D] bf16; ``post`` and ``norm`` are "none", "rms" or
+    "layer".  Returns (x_new, h); x_new has x's type and goes to ``x_out``, which
+    may be x itself, h (bf16, None with norm="none") to ``out``."""
+    import torch
+    _check_bf16("y", y, 3)
+    B, N, D = y.shape
+    if (not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32) or x.shape != y.shape
+            or not x.is_contiguous() or x.device != y.device):
+        raise ValueError("x must be a contiguous bfloat16 or float32 tensor of y's shape on its device")
+    if post not in PA_NORM or norm not in PA_NORM:
+        raise ValueError(f"post and norm must be one of {sorted(PA_NORM)} (got {post!r}, {norm!r})")
+    cfg = BlockNorm(PA_NORM[post], PA_NORM[norm], _check_vector("post_weight", post_weight, torch.bfloat16, (D,), y.device),
+                    _check_vector("norm_weight", norm_weight, torch.bfloat16, (D,), y.device),
+                    residual_scale=float(residual_scale), eps=float(eps))
+    for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
+        if t is None:
+            continue
+        _check_rows(name, t, 2, y.device)
+        if tuple(t.shape) != (B, D):
+            raise ValueError(f"{name} must be [B, D] = {(B, D)} (got {tuple(t.shape)})")
+        setattr(cfg, name, t.data_ptr())
+        setattr(cfg, name + "_stride", t.stride(0))
+    if norm == "none" and out is not None:
+        raise ValueError("out is written only with a norm")
+    with _allocating_for(stream, y.device):
+        if x_out is None:
+            x_out = torch.empty_like(x)
+        if out is None and norm != "none":
+            out = torch.empty_like(y)
+    if x_out.dtype != x.dtype or x_out.shape != x.shape or not x_out.is_contiguous() or x_out.device != y.device:
+        raise ValueError("x_out must be a contiguous tensor of x's type and shape on its device")
+    if out is not None:
+        _check_bf16("out", out, 3)
+        if out.shape != y.shape or out.device != y.device:
+            raise ValueError("out must have y's shape and device")
+    rc = load_library().pa_gate_residual_norm(y.data_ptr(), x.data_ptr(), x_out.data_ptr(),
+                                               None if out is None else out.data_ptr(), B, N, D,
+                                               1 if x.dtype == torch.float32 else 0, ctypes.byref(cfg),
+                                               _stream_handle(stream, y.device))
+    _check(rc, "pa_gate_residual_norm", check)
+    return x_out, out
 
 
 def attn_merge(o_parts, lse_parts, out=None, lse=None, stream=None, check: bool = False):

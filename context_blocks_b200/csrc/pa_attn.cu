@@ -16,6 +16,7 @@
 #include "attn_fwd.cuh"
 #include "attn_mod.cuh"
 #include "attn_shared.cuh"
+#include "block_norm.cuh"
 #include "quantize.cuh"
 #include "fwd_common.cuh"
 #include "lse_merge.cuh"
@@ -526,6 +527,36 @@ int by_mod(int d, bool cap, bool bias, F f) {
   return d == 64 ? with_d(std::integral_constant<int, 64>{}) : with_d(std::integral_constant<int, 128>{});
 }
 
+// ------------------------------------------------------ gated residual norm
+
+template <bool kX32, int kVecs, int kWarps>
+int launch_block_norm(const pa::norm::Params& prm, cudaStream_t stream) {
+  constexpr int kRows = pa::norm::kThreads / 32 / kWarps;
+  const long long blocks = (prm.rows + kRows - 1) / kRows;
+  if (blocks > 0x7fffffffLL) return fail(PA_ERR_UNSUPPORTED, "too many rows");
+  pa::norm::gate_residual_norm_kernel<kX32, kVecs, kWarps>
+      <<<static_cast<unsigned>(blocks), pa::norm::kThreads, 0, stream>>>(prm);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "gate_residual_norm launch");
+  return PA_OK;
+}
+
+// The fewest warps a row that hold it in four vectors a thread (eight above 8192).
+template <bool kX32>
+int launch_block_norm_x(const pa::norm::Params& prm, cudaStream_t stream) {
+  if (prm.D <= 256) return launch_block_norm<kX32, 1, 1>(prm, stream);
+  if (prm.D <= 512) return launch_block_norm<kX32, 2, 1>(prm, stream);
+  if (prm.D <= 1024) return launch_block_norm<kX32, 4, 1>(prm, stream);
+  if (prm.D <= 2048) return launch_block_norm<kX32, 4, 2>(prm, stream);
+  if (prm.D <= 4096) return launch_block_norm<kX32, 4, 4>(prm, stream);
+  if (prm.D <= 8192) return launch_block_norm<kX32, 4, 8>(prm, stream);
+  return launch_block_norm<kX32, 8, 8>(prm, stream);
+}
+
+int launch_block_norm(const pa::norm::Params& prm, bool x32, cudaStream_t stream) {
+  return x32 ? launch_block_norm_x<true>(prm, stream) : launch_block_norm_x<false>(prm, stream);
+}
+
 // Shapes of a shared-prefix call; false where the rows of one request under one
 // K/V head do not fit a row tile.
 bool shared_plan(int B, int Hq, int Hkv, int Nq, int Np, int Nt, int ctas, pa::shared::Plan* plan) {
@@ -941,6 +972,79 @@ int pa_residual_diff(const void* cur, const void* prev, long long n, float* out,
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "residual_diff launch");
   return PA_OK;
+}
+
+int pa_gate_residual_norm(const void* y, const void* x, void* x_out, void* h, int B, int N, int D, int x_f32,
+                          const pa_block_norm* cfg, void* stream) {
+  g_err[0] = '\0';
+  if (!cfg) return fail(PA_ERR_INVALID_ARG, "null pointer argument (cfg)");
+  if (B < 1) return fail(PA_ERR_INVALID_ARG, "B must be >= 1 (got %d)", B);
+  if (N < 0) return fail(PA_ERR_INVALID_ARG, "N must be >= 0 (got %d)", N);
+  if (D < 8 || D % 8) return fail(PA_ERR_UNSUPPORTED, "D must be a positive multiple of 8 (got %d)", D);
+  if (D > 16384) return fail(PA_ERR_UNSUPPORTED, "D must be <= 16384 (got %d)", D);
+  for (int kind : {cfg->post, cfg->norm})
+    if (kind != PA_NORM_NONE && kind != PA_NORM_RMS && kind != PA_NORM_LAYER)
+      return fail(PA_ERR_INVALID_ARG, "unknown norm %d", kind);
+  if (cfg->norm == PA_NORM_NONE && (cfg->norm_weight || cfg->scale || cfg->shift))
+    return fail(PA_ERR_INVALID_ARG, "norm_weight, scale and shift need a norm");
+  if (!std::isfinite(cfg->eps) || cfg->eps < 0.f) return fail(PA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!std::isfinite(cfg->residual_scale)) return fail(PA_ERR_INVALID_ARG, "residual_scale must be finite");
+  if (N == 0) return PA_OK;  // an empty tensor may have no address
+  if (!y || !x || !x_out) return fail(PA_ERR_INVALID_ARG, "null pointer argument");
+  if ((h != nullptr) != (cfg->norm != PA_NORM_NONE))
+    return fail(PA_ERR_INVALID_ARG, "h is given with a norm and only with one");
+  const void* ptrs[9] = {y, x, x_out, h, cfg->post_weight, cfg->norm_weight, cfg->gate, cfg->scale, cfg->shift};
+  const char* names[9] = {"y", "x", "x_out", "h", "post_weight", "norm_weight", "gate", "scale", "shift"};
+  for (int i = 0; i < 9; ++i)
+    if (ptrs[i] && !aligned(ptrs[i], 16)) return fail(PA_ERR_MISALIGNED, "%s must be 16-byte aligned", names[i]);
+  const long long strides[3] = {cfg->gate_stride, cfg->scale_stride, cfg->shift_stride};
+  for (int i = 0; i < 3; ++i) {
+    if (!ptrs[6 + i] || B == 1) continue;
+    if (strides[i] < 0 || strides[i] > kMaxStride)
+      return fail(PA_ERR_INVALID_ARG, "%s: stride out of range", names[6 + i]);
+    if (strides[i] % 8) return fail(PA_ERR_MISALIGNED, "%s: stride must be a multiple of 8 elements", names[6 + i]);
+  }
+  const uint64_t n = static_cast<uint64_t>(B) * N * D, vec = static_cast<uint64_t>(D) * 2;
+  auto table = [&](int i) { return (B > 1 ? static_cast<uint64_t>(B - 1) * strides[i] * 2 : 0) + vec; };
+  const uint64_t bytes[9] = {n * 2, n * (x_f32 ? 4 : 2), n * (x_f32 ? 4 : 2), n * 2, vec, vec,
+                             ptrs[6] ? table(0) : 0, ptrs[7] ? table(1) : 0, ptrs[8] ? table(2) : 0};
+  for (int o = 2; o < 4; ++o)
+    for (int i = 0; i < 9; ++i) {
+      // x_out may be x itself: every element is read and written by one thread.
+      if (i == o || !ptrs[o] || !ptrs[i] || (o == 2 && i == 1 && x == x_out)) continue;
+      if (overlap(ptrs[o], bytes[o], ptrs[i], bytes[i]))
+        return fail(PA_ERR_INVALID_ARG, "%s overlaps %s", names[o], names[i]);
+    }
+  const void* given[9];
+  const char* given_names[9];
+  int ng = 0;
+  for (int i = 0; i < 9; ++i)
+    if (ptrs[i]) given[ng] = ptrs[i], given_names[ng++] = names[i];
+  DeviceState* st = nullptr;
+  int rc;
+  if ((rc = device_checks(given, given_names, ng, &st)) != PA_OK) return rc;
+
+  pa::norm::Params prm;
+  prm.y = static_cast<const __nv_bfloat16*>(y);
+  prm.x = x;
+  prm.x_out = x_out;
+  prm.h = static_cast<__nv_bfloat16*>(h);
+  prm.post_weight = static_cast<const __nv_bfloat16*>(cfg->post_weight);
+  prm.norm_weight = static_cast<const __nv_bfloat16*>(cfg->norm_weight);
+  prm.gate = static_cast<const __nv_bfloat16*>(cfg->gate);
+  prm.scale = static_cast<const __nv_bfloat16*>(cfg->scale);
+  prm.shift = static_cast<const __nv_bfloat16*>(cfg->shift);
+  prm.gate_stride = cfg->gate_stride;
+  prm.scale_stride = cfg->scale_stride;
+  prm.shift_stride = cfg->shift_stride;
+  prm.rows = static_cast<long long>(B) * N;
+  prm.rows_per_batch = N;
+  prm.D = D;
+  prm.post = cfg->post;
+  prm.norm = cfg->norm;
+  prm.residual_scale = cfg->residual_scale;
+  prm.eps = cfg->eps;
+  return launch_block_norm(prm, x_f32 != 0, static_cast<cudaStream_t>(stream));
 }
 
 int pa_attn_chunks_noalloc(const void* q, const void* const* k_chunks, const void* const* v_chunks,

@@ -371,6 +371,46 @@ size_t pa_attn_shared_prefix_workspace(int B, int Hq, int Hkv, int Nq, int Np, i
  */
 int pa_residual_diff(const void* cur, const void* prev, long long n, float* out, void* stream);
 
+/* Norms of pa_block_norm. */
+#define PA_NORM_NONE 0
+#define PA_NORM_RMS 1   /* v / sqrt(mean(v^2) + eps) */
+#define PA_NORM_LAYER 2 /* (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) */
+
+/* The norms, gate and modulation of pa_gate_residual_norm.  Tensors are bf16,
+ * device, 16-byte aligned, or NULL for none. */
+typedef struct pa_block_norm {
+  int post;                /* PA_NORM_*: norm of the block's output */
+  int norm;                /* PA_NORM_*: norm of the new residual; NONE: no h */
+  const void* post_weight; /* [D] */
+  const void* norm_weight; /* [D] */
+  const void* gate;        /* [B, D], gate_stride elements between batch entries */
+  const void* scale;       /* [B, D] */
+  const void* shift;       /* [B, D] */
+  long long gate_stride, scale_stride, shift_stride; /* multiples of 8, >= 0; ignored with B = 1 */
+  float residual_scale;    /* a */
+  float eps;               /* >= 0 */
+} pa_block_norm;
+
+/*
+ * pa_gate_residual_norm - a block's gated residual update, with the norm of its
+ * output before it and the next block's input norm behind it, in one pass:
+ *     t     = post(y) * post_weight
+ *     x_out = a * x + gate[b] * t
+ *     h     = norm(a * x + gate[b] * t) * norm_weight * (1 + scale[b]) + shift[b]
+ * computed in fp32 and rounded once (h is taken from the unrounded residual).
+ *
+ * y, h      [B,N,D] bf16, contiguous, 16-byte aligned (h NULL without a norm)
+ * x, x_out  [B,N,D] bf16, or fp32 with x_f32 non-zero; x_out may be x (an update
+ *           in place), otherwise outputs overlap nothing
+ * D         a multiple of 8, 8 .. 16384;  B >= 1;  N >= 0 (0 is a no-op)
+ *
+ * One launch on `stream`.  Errors: PA_ERR_INVALID_ARG (null pointers, unknown
+ * norms, h without a norm or the other way round, overlap), PA_ERR_UNSUPPORTED
+ * (D), PA_ERR_MISALIGNED, PA_ERR_CUDA.
+ */
+int pa_gate_residual_norm(const void* y, const void* x, void* x_out, void* h, int B, int N, int D, int x_f32,
+                          const pa_block_norm* cfg, void* stream);
+
 /*
  * pa_attn_chunks_noalloc - attention of Q over several K/V chunks, allocating
  * nothing.
