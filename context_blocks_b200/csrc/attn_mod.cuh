@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int hk = hq / p.G;
         repair_row<D>(p.q + bt * p.q_s[0] + hq * p.q_s[1] + (wrow + r) * p.q_s[2],
                       p.k + bt * p.k_s[0] + hk * p.k_s[1], p.v + bt * p.v_s[0] + hk * p.v_s[1], p.k_s[2], p.v_s[2], j0,
-                      j1, wrow + r + p.q_offset, mr, iv, slope2, p.sm, kCap, kBias, o + r * p.o_s[2], nullptr);
+                      j1, 1, 1, 0, wrow + r + p.q_offset, mr, iv, slope2, p.sm, kCap, kBias, o + r * p.o_s[2], nullptr);
       }
     }
   }

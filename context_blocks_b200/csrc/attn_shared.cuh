@@ -7,25 +7,34 @@
 // the rows of all of them (Nq tokens x G query heads a K/V head) are stacked
 // into tiles of up to 128 rows.
 //
-// Work is a line of key tiles (128 keys): first every prefix segment (K/V head x
-// pair of row tiles), then every tail segment (request x K/V head).  CTA c of C
-// takes the tiles whose place on the line falls in its C-th part, so every SM
-// gets the same share whatever the lengths are, without counters or host
-// knowledge of them.  The part of a segment that falls to one CTA is a piece;
-// segment s and CTA c name it (s + c is different for every piece, since both
-// only grow along the line), and with it the place of its partial results:
-// normalised fp32 O and LSE rows in the caller's workspace, which
-// shared_merge_kernel joins, one row a group of warps, from the same arithmetic.
+// Work.  A segment is the keys one row tile has to go over: the prefix under one
+// K/V head, or one request's tail under one K/V head.  Two row tiles over the
+// same prefix make a pair, which shares its K and V tiles; what is left (the
+// prefix under an odd row tile, and the tails) is single.  Pairs and singles
+// each form a line of key tiles (128 keys), cut into equal parts: a pair part
+// for each CTA of the first kind, a single part for each of the two streams (a
+// softmax warpgroup, its MMA and its load warp) of the others, so that every SM
+// gets the same share whatever the lengths are, without counters and without
+// host knowledge of them.  The part of a segment that falls to one part of the
+// line is a piece; segment + part is another number for every piece, since both
+// only grow along the line, and names the place of its partial results in the
+// caller's workspace: normalised fp32 O rows and their LSE (base 2).
+// shared_merge_kernel joins them, finding them by the same arithmetic.
 //
-// A piece runs two streams, one a softmax warpgroup, so that one stream's tensor
-// work overlaps the other's softmax: with a pair of row tiles each stream takes
-// one tile over the same keys; with a single row tile (tails, and the prefix of
-// few requests) each stream takes half of the piece's keys and leaves partial
-// results of its own.  Warps as in attn_mod.cuh.
+// The streams of a single CTA run independently, so that one stream's loads,
+// tensor work and softmax fill the other's waits.  Row tiles of few rows (32 or
+// less; 64 or less) hold their rows four times (twice): every copy lies in the
+// tensor-memory lanes of a warp of its own, which takes its quarter (half) of
+// the tile's keys, with zero weights for the rest.  One warp working through 128
+// keys a row took longer than the tile's loads: 4.5 TB/s where this reaches 5.6
+// (24 heads, 119056 keys, 21 rows).  The copies' results are joined like those of different pieces.
+//
+// Warps: 0-3, 4-7 softmax of stream 0 and 1 (208 registers); 8, 11 MMA issue of
+// stream 0 and 1 (8 issues for both in a pair CTA); 9, 10 pieces and TMA loads
+// of stream 0 and 1 (9 for both in a pair CTA).
 //
 // Bound: HBM (64 KB of K and V a tile at d = 128) as long as few rows share a
-// tile; with several row-tile pairs the prefix becomes tensor and special-
-// function work and its re-reads come from L2.
+// tile; pairs are tensor and special-function work, their re-reads come from L2.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -40,28 +49,49 @@ namespace shared {
 using namespace mod;
 
 constexpr int kMaxCtas = 160;  // sizes the workspace; the grid is one CTA an SM, at most this many
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 4;
+constexpr int kLoadWarp = 9;   // + stream
+// Cost of a pair's key tile over a single's, in quarters: how the CTAs are
+// dealt to the two kinds.
+constexpr int kPairCost4 = 4;
 
-// The decomposition of the line, computed alike by the kernel and the merge.
+// A line of n units cut into `parts` parts, none empty, sizes differing by one.
+struct Cut {
+  int n, parts, q, r;
+  __device__ Cut(int n_, int most) : n(n_), parts(max(min(n_, most), 1)), q(n_ / parts), r(n_ - q * parts) {}
+  __device__ int begin(int c) const { return c * q + min(c, r); }
+  __device__ int holder(int u) const { return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q; }
+};
+
+// Shapes of a call.
 struct Plan {
   int B, Hq, Hkv, G, Nq;
   int rows;          // rows of one request under one K/V head: G * Nq
   int tile_reqs;     // requests in a row tile: 128 / rows, at most B
-  int row_tiles;     // ceil(B / tile_reqs)
-  int pairs;         // ceil(row_tiles / 2)
+  int row_tiles;     // ceil(B / tile_reqs); 0 without a prefix
   int Np, Nt;
   int prefix_tiles;  // key tiles of the prefix
-  int prefix_segs;   // Hkv * pairs, 0 without a prefix
   int ctas;
   const int* tail_lens;
 
-  __host__ __device__ long long prefix_units() const { return static_cast<long long>(prefix_segs) * prefix_tiles; }
+  __host__ __device__ int tile_rows() const { return tile_reqs * rows; }
+  __host__ __device__ int pairs() const { return row_tiles / 2; }
+  __host__ __device__ bool odd() const { return (row_tiles & 1) != 0; }
+  __host__ __device__ int pair_units() const { return Hkv * pairs() * prefix_tiles; }
+  __host__ __device__ int odd_units() const { return odd() ? Hkv * prefix_tiles : 0; }
+  // Copies of a row tile's rows.
+  __host__ __device__ static int copies(int n) { return n <= 32 ? 4 : n <= 64 ? 2 : 1; }
   __device__ int len(int b) const { return min(max(__ldg(tail_lens + b), 0), Nt); }
   __device__ static int tiles_of(int keys) { return (keys + kBN - 1) / kBN; }
-  // First unit of CTA c's part of a line of `total` units.
-  __device__ long long part(long long total, int c) const { return total * c / ctas; }
-  // Whether row tile pair `pr` is a single tile (the last one of an odd number).
-  __host__ __device__ bool single(int pr) const { return 2 * pr + 1 >= row_tiles; }
+  // CTAs that take pairs, given the tail tiles (under one K/V head) of all
+  // requests.
+  __device__ int pair_ctas(int tails) const {
+    const long long p = static_cast<long long>(pair_units()) * kPairCost4;
+    const long long s = (odd_units() + static_cast<long long>(tails) * Hkv) * 4;
+    if (p == 0) return 0;
+    if (s == 0) return ctas;
+    return static_cast<int>(min(max((ctas * p + (p + s) / 2) / (p + s), 1ll), ctas - 1ll));
+  }
 };
 
 struct Params {
@@ -70,28 +100,32 @@ struct Params {
   const __nv_bfloat16* kt;
   const __nv_bfloat16* vt;
   long long kt_s[3], vt_s[3];  // tail strides: batch, head, row (elements)
-  float* prefix_o;             // [2 * (prefix_segs + ctas)][tile_reqs * rows][D]
-  float* prefix_lse;
-  float* tail_o;               // [2 * (B * Hkv + ctas)][rows][D]
+  float* pair_o;               // [(Hkv * pairs + ctas) * 2][tile_rows][D]
+  float* pair_lse;
+  float* odd_o;                // [(Hkv + 2 * ctas) * copies][tile_rows][D]
+  float* odd_lse;
+  float* tail_o;               // [(B * Hkv + 2 * ctas) * copies][rows][D]
   float* tail_lse;
   ScoreMod sm;
   int* status;
   unsigned long long timeout_ns;
 };
 
-// A piece as the scheduler hands it out.
+constexpr int kEnd = -1, kTail = 0, kOdd = 1, kPair = 2;
+
+// A piece as its load warp hands it out.
 struct Piece {
-  int kind;   // -1: no more; 0: tail; 1: prefix, one row tile; 2: prefix, two row tiles
+  int kind;
   int hk;
-  int req;    // tail: the request; prefix: the first row tile
-  int t0, t1; // its key tiles
-  int slot;   // segment + CTA
-  int keys;   // keys of the segment
+  int req;     // a tail's request, or the first request of the row tile (of the first one of a pair)
+  int t0, t1;  // its key tiles
+  int slot;    // segment + part
+  int keys;    // keys of the segment
 };
 
 template <int D>
 struct SharedLayout {
-  static constexpr int kStages = D == 64 ? 8 : 4;  // 128 KB of K and V in flight
+  static constexpr int kStages = D == 64 ? 8 : 4;  // 128 KB of K and V; half of them a stream's own in a single CTA
   static constexpr int kBoxBytes = 128 * 128;
   static constexpr int kBoxes = D / 64;
   static constexpr int kTileBytes = kBoxes * kBoxBytes;
@@ -100,14 +134,119 @@ struct SharedLayout {
   static constexpr int kStageOff = kRingOff + kStages * kTileBytes;
   static constexpr int kStageWarpBytes = 32 * 128;
   static constexpr int kBarOff = kStageOff + 8 * kStageWarpBytes;
-  static constexpr int kNumBars = 2 + 2 * kStages + 8 + 1 + 4;
+  // q_full[2], q_empty[2], kv_full[S], kv_empty[S], s_full[2], p_part[2],
+  // p_full[2], o_full[2], drain[2], piece_full[2][2], piece_empty[2][2]
+  static constexpr int kNumBars = 4 + 2 * kStages + 8 + 2 + 8;
   static constexpr int kPieceOff = kBarOff + kNumBars * 8;
-  static constexpr int kTmemSlotOff = kPieceOff + 2 * static_cast<int>(sizeof(Piece));
+  static constexpr int kTmemSlotOff = kPieceOff + 4 * static_cast<int>(sizeof(Piece));
   static constexpr int kAbortOff = kTmemSlotOff + 4;
   static constexpr int kBytes = kAbortOff + 4;
   static constexpr int kMinOneCtaPerSm = 120 * 1024;
   static constexpr int kAllocBytes = (kBytes + 1024 > kMinOneCtaPerSm) ? (kBytes + 1024) : kMinOneCtaPerSm;
 };
+
+// softmax_tile for a warp that takes kKeys keys of the tile, those from kq *
+// kKeys on, of rows that have a copy in its tensor-memory lanes; the weights of
+// the tile's other keys are zero in this copy.  The row sees keys j < b of the
+// tile.  All exponentials on the special-function unit: a warp has few enough.
+template <int D, bool kCap, bool kBias, int kKeys>
+__device__ __forceinline__ void softmax_share(uint32_t tS, uint32_t tO, int kq, int b, float dist0, float slope2,
+                                              const ScoreMod& sm, bool have_o, float& m_ref, float& l,
+                                              uint32_t bar_part, uint32_t bar_full, int lane) {
+  uint32_t sr[kKeys];
+  if constexpr (kKeys == 32)
+    tmem_ld_x32(tS + kq * kKeys, sr);
+  else
+    tmem_ld_x64(tS + kq * kKeys, sr);
+  const int e0 = kq * kKeys;
+  const float d0 = dist0 - static_cast<float>(e0);
+  float x[kKeys];
+#pragma unroll
+  for (int e = 0; e < kKeys; ++e) {
+    x[e] = mod_one(__uint_as_float(sr[e]), sm, kCap, kBias, slope2, d0 - static_cast<float>(e));
+    if (e >= b - e0) x[e] = -INFINITY;
+  }
+  float m4[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m4[k] = fmaxf(x[k], x[k + 4]);
+#pragma unroll
+  for (int e = 8; e < kKeys; e += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m4[k] = max3f(m4[k], x[e + k], x[e + 4 + k]);
+  const float mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
+  float alpha = 1.f;
+  bool rescale = false;
+  if (mx > m_ref + kRescaleLog2) {
+    alpha = ex2_approx(m_ref - mx);
+    l *= alpha;
+    m_ref = mx;
+    rescale = have_o;
+  }
+  if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+    for (int ch = 0; ch < D / 32; ++ch) {
+      uint32_t orr[32];
+      tmem_ld_x32(tO + ch * 32, orr);
+#pragma unroll
+      for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+      tmem_st_x32(tO + ch * 32, orr);
+    }
+  }
+  const float neg_m = (m_ref == -INFINITY) ? 0.f : -m_ref;
+  uint32_t zero[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) zero[e] = 0u;
+  float l2[2] = {0.f, 0.f};
+  constexpr int kParts = kKeys / 32;
+#pragma unroll
+  for (int ch = 0; ch < kParts; ++ch) {
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float p0 = ex2_approx(x[ch * 32 + 2 * e] + neg_m), p1 = ex2_approx(x[ch * 32 + 2 * e + 1] + neg_m);
+      l2[0] += p0;
+      l2[1] += p1;
+      pk[e] = pack_bf16x2(p0, p1);
+    }
+    tmem_st_x16(tS + (kq * kParts + ch) * 16, pk);
+  }
+#pragma unroll
+  for (int u = kParts; u < 4; ++u) tmem_st_x16(tS + ((kq * kParts + u) & 3) * 16, zero);
+  l += l2[0] + l2[1];
+  tmem_st_wait();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) {
+    mbar_arrive(bar_part);
+    mbar_arrive(bar_full);
+  }
+}
+
+// Scale a thread's O row by inv and store it as fp32 at dst, where `write`.
+// For a warp with few rows: no staging.  inv = 0 stores zeros.  Returns whether
+// the row has a value that is not finite.
+template <int D>
+__device__ __noinline__ bool store_row_f32(uint32_t tO, float* dst, bool write, float inv) {
+  float bad = 0.f;
+#pragma unroll 1
+  for (int ch = 0; ch < D / 32; ++ch) {
+    uint32_t orr[32];
+    tmem_ld_x32(tO + ch * 32, orr);
+    float v[32];
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float x = __uint_as_float(orr[e]);
+      bad = fmaf(x, 0.f, bad);
+      v[e] = inv == 0.f ? 0.f : x * inv;
+    }
+    if (write) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        reinterpret_cast<float4*>(dst + ch * 32)[u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+    }
+  }
+  return !(bad == 0.f);
+}
 
 template <int D, bool kCap, bool kBias>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -117,6 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                        const __grid_constant__ Params p) {
   using L = SharedLayout<D>;
   constexpr int kStages = L::kStages;
+  constexpr int kHalf = kStages / 2;  // ring slots of a stream in a single CTA
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -125,16 +265,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sQ = base + L::kQOff;
   const uint32_t sRing = base + L::kRingOff;
   const uint32_t bars = base + L::kBarOff;
-  const uint32_t bar_q_full = bars, bar_q_empty = bars + 8;
-  const uint32_t bar_kv_full0 = bars + 8 * 2;
-  const uint32_t bar_kv_empty0 = bars + 8 * (2 + kStages);
-  const uint32_t bar_s_full0 = bars + 8 * (2 + 2 * kStages);
-  const uint32_t bar_p_part0 = bars + 8 * (4 + 2 * kStages);
-  const uint32_t bar_p_full0 = bars + 8 * (6 + 2 * kStages);
-  const uint32_t bar_o_full0 = bars + 8 * (8 + 2 * kStages);
-  const uint32_t bar_drain = bars + 8 * (10 + 2 * kStages);
-  const uint32_t bar_piece_full0 = bars + 8 * (11 + 2 * kStages);
-  const uint32_t bar_piece_empty0 = bars + 8 * (13 + 2 * kStages);
+  const uint32_t bar_q_full0 = bars, bar_q_empty0 = bars + 8 * 2;
+  const uint32_t bar_kv_full0 = bars + 8 * 4;
+  const uint32_t bar_kv_empty0 = bars + 8 * (4 + kStages);
+  const uint32_t bar_s_full0 = bars + 8 * (4 + 2 * kStages);
+  const uint32_t bar_p_part0 = bars + 8 * (6 + 2 * kStages);
+  const uint32_t bar_p_full0 = bars + 8 * (8 + 2 * kStages);
+  const uint32_t bar_o_full0 = bars + 8 * (10 + 2 * kStages);
+  const uint32_t bar_drain0 = bars + 8 * (12 + 2 * kStages);
+  const uint32_t bar_piece_full0 = bars + 8 * (14 + 2 * kStages);   // + 8 * (2 * stream + slot)
+  const uint32_t bar_piece_empty0 = bars + 8 * (18 + 2 * kStages);
   volatile Piece* slots = reinterpret_cast<volatile Piece*>(gbase + L::kPieceOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kTmemSlotOff);
   volatile int* abort_word = reinterpret_cast<volatile int*>(gbase + L::kAbortOff);
@@ -145,29 +285,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Plan& plan = p.plan;
 
   if (threadIdx.x == 0) {
-    mbar_init(bar_q_full, 1);
-    mbar_init(bar_q_empty, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar_kv_full0 + 8 * s, 1);
       mbar_init(bar_kv_empty0 + 8 * s, 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(bar_q_full0 + 8 * i, 1);
+      mbar_init(bar_q_empty0 + 8 * i, 1);
       mbar_init(bar_s_full0 + 8 * i, 1);
       mbar_init(bar_p_part0 + 8 * i, 4);  // one arrival per softmax warp
       mbar_init(bar_p_full0 + 8 * i, 4);
       mbar_init(bar_o_full0 + 8 * i, 1);
-      mbar_init(bar_piece_full0 + 8 * i, 1);
-      mbar_init(bar_piece_empty0 + 8 * i, 10);  // 8 softmax warps, MMA, TMA
+      mbar_init(bar_drain0 + 8 * i, 1);
     }
-    mbar_init(bar_drain, 1);
+    for (int u = 0; u < 4; ++u) {
+      mbar_init(bar_piece_full0 + 8 * u, 1);
+      mbar_init(bar_piece_empty0 + 8 * u, 5);  // 4 softmax warps and the MMA warp of the stream
+    }
     *abort_word = 0;
     fence_barrier_init();
   }
-  if (warp == kTmaWarp && lane == 0) {
+  if (warp == kLoadWarp && lane == 0) {
     prefetch_tensormap(&tm_qp);
-    prefetch_tensormap(&tm_qt);
     prefetch_tensormap(&tm_kp);
     prefetch_tensormap(&tm_vp);
+  }
+  if (warp == kLoadWarp + 1 && lane == 0) {
+    prefetch_tensormap(&tm_qt);
     prefetch_tensormap(&tm_kt);
     prefetch_tensormap(&tm_vt);
   }
@@ -184,170 +328,180 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool got = mbar_wait_hint(bar, parity, abort_word, p.status, kStatusTimeout, lim, kSuspendHintNs);
     return __all_sync(0xffffffffu, got);
   };
-  auto next_piece = [&](int it, Piece& x, bool& ok) {
-    const int s = it & 1;
-    if (!wait_all(bar_piece_full0 + 8 * s, (it >> 1) & 1)) {
+  // The it-th piece of a stream, copied out of its slot; false at the end (or
+  // where a wait gave up, with `ok` cleared).
+  auto next_piece = [&](int i, int it, Piece& x, bool& ok) {
+    const int u = 2 * i + (it & 1);
+    if (!wait_all(bar_piece_full0 + 8 * u, (it >> 1) & 1)) {
       ok = false;
       return false;
     }
-    x.kind = slots[s].kind;
-    x.hk = slots[s].hk;
-    x.req = slots[s].req;
-    x.t0 = slots[s].t0, x.t1 = slots[s].t1;
-    x.slot = slots[s].slot;
-    x.keys = slots[s].keys;
+    x.kind = slots[u].kind;
+    x.hk = slots[u].hk;
+    x.req = slots[u].req;
+    x.t0 = slots[u].t0, x.t1 = slots[u].t1;
+    x.slot = slots[u].slot;
+    x.keys = slots[u].keys;
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar_piece_empty0 + 8 * s);
-    return x.kind >= 0;
+    if (lane == 0) mbar_arrive(bar_piece_empty0 + 8 * u);
+    return x.kind != kEnd;
   };
-  // Key tiles [a, b) of stream i of a piece: all of them with two row tiles,
-  // the lower or the upper half with one.
-  auto first_of = [](const Piece& x, int i) { return x.kind == 2 || i == 0 ? x.t0 : x.t0 + (x.t1 - x.t0 + 1) / 2; };
-  auto last_of = [](const Piece& x, int i) { return x.kind == 2 || i == 1 ? x.t1 : x.t0 + (x.t1 - x.t0 + 1) / 2; };
 
-  if (warp > kSchedWarp) {
+  if (warp == kLoadWarp || warp == kLoadWarp + 1) {
     setmaxnreg_dec<kControlRegs>();
-  } else if (warp == kSchedWarp) {
-    setmaxnreg_dec<kControlRegs>();
-    // ----------------------------------------------------------- scheduler
-    int it = 0;
+    // --------------------------------------------------- pieces and loads
+    const int i = warp - kLoadWarp;
+    const bool leader = elect_one();
     bool ok = true;
-    auto emit = [&](int kind, int hk, int req, int t0, int t1, int slot, int keys) {
-      const int s = it & 1;
-      if (!wait_all(bar_piece_empty0 + 8 * s, ((it >> 1) & 1) ^ 1)) {
+    int it = 0;   // pieces handed out
+    int idx = 0;  // ring loads issued so far
+    // Ring slots this warp fills: all of them in a pair CTA, else its half.
+    int slot0 = i * kHalf, n_slots = kHalf;
+    // Hands a piece to the warps of its stream (of both, for a pair).
+    auto publish = [&](int kind, int hk, int req, int t0, int t1, int slot, int keys, bool both) {
+      for (int s = both ? 0 : i; s <= (both ? 1 : i) && ok; ++s) {
+        const int u = 2 * s + (it & 1);
+        if (!wait_all(bar_piece_empty0 + 8 * u, ((it >> 1) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          slots[u].kind = kind;
+          slots[u].hk = hk;
+          slots[u].req = req;
+          slots[u].t0 = t0;
+          slots[u].t1 = t1;
+          slots[u].slot = slot;
+          slots[u].keys = keys;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_piece_full0 + 8 * u);
+      }
+      ++it;
+    };
+    // A piece: its Q rows, then K and V tiles from the last to the first, in
+    // the order the MMA warp takes them.
+    int q_loads = 0;
+    auto run = [&](int kind, int hk, int req, int t0, int t1, int slot, int keys) {
+      publish(kind, hk, req, t0, t1, slot, keys, kind == kPair);
+      if (!ok || !wait_all(bar_q_empty0 + 8 * i, (q_loads & 1) ^ 1)) {
         ok = false;
         return;
       }
-      if (lane == 0) {
-        slots[s].kind = kind;
-        slots[s].hk = hk;
-        slots[s].req = req;
-        slots[s].t0 = t0;
-        slots[s].t1 = t1;
-        slots[s].slot = slot;
-        slots[s].keys = keys;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar_piece_full0 + 8 * s);
-      ++it;
-    };
-    const int c = blockIdx.x;
-    // All tail tiles under one K/V head.
-    long long tails = 0;
-    for (int b = lane; b < plan.B; b += 32) tails += Plan::tiles_of(plan.len(b));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) tails += __shfl_xor_sync(0xffffffffu, tails, off);
-    const long long pre = plan.prefix_units();
-    const long long total = pre + tails * plan.Hkv;
-    const long long u0 = plan.part(total, c), u1 = plan.part(total, c + 1);
-    if (u0 < pre) {
-      for (int s = static_cast<int>(u0 / plan.prefix_tiles); s < plan.prefix_segs && ok; ++s) {
-        const long long at = static_cast<long long>(s) * plan.prefix_tiles;
-        if (at >= u1) break;
-        const int t0 = static_cast<int>(max(u0 - at, 0ll));
-        const int t1 = static_cast<int>(min(u1 - at, static_cast<long long>(plan.prefix_tiles)));
-        if (t0 < t1)
-          emit(plan.single(s % plan.pairs) ? 1 : 2, s / plan.pairs, 2 * (s % plan.pairs), t0, t1, s + c, plan.Np);
-      }
-    }
-    long long at = pre;  // place of request b0's first tile
-    for (int b0 = 0; b0 < plan.B && at < u1 && ok; b0 += 32) {
-      const int n = b0 + lane < plan.B ? plan.len(b0 + lane) : 0;
-      const int nt = Plan::tiles_of(n);
-      int upto = nt;  // inclusive scan
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, upto, off);
-        if (lane >= off) upto += y;
-      }
-      const long long all = static_cast<long long>(__shfl_sync(0xffffffffu, upto, 31)) * plan.Hkv;
-      // Requests of these 32 that have a tile in this CTA's part.
-      const long long mine0 = at + static_cast<long long>(upto - nt) * plan.Hkv;
-      const long long mine1 = mine0 + static_cast<long long>(nt) * plan.Hkv;
-      unsigned todo = __ballot_sync(0xffffffffu, nt > 0 && mine0 < u1 && mine1 > u0);
-      while (todo != 0u && ok) {
-        const int k = __ffs(todo) - 1;
-        todo &= todo - 1;
-        const long long a0 = __shfl_sync(0xffffffffu, mine0, k);
-        const int kn = __shfl_sync(0xffffffffu, n, k), knt = __shfl_sync(0xffffffffu, nt, k);
-        for (int hk = static_cast<int>(max(u0 - a0, 0ll) / knt); hk < plan.Hkv && ok; ++hk) {
-          const long long a = a0 + static_cast<long long>(hk) * knt;
-          if (a >= u1) break;
-          const int t0 = static_cast<int>(max(u0 - a, 0ll));
-          const int t1 = static_cast<int>(min(u1 - a, static_cast<long long>(knt)));
-          if (t0 < t1) emit(0, hk, b0 + k, t0, t1, (b0 + k) * plan.Hkv + hk + c, kn);
-        }
-      }
-      at += all;
-    }
-    if (ok) emit(-1, 0, 0, 0, 0, 0, 0);
-  } else if (warp == kTmaWarp) {
-    setmaxnreg_dec<kControlRegs>();
-    // ------------------------------------------------------------ producer
-    const bool leader = elect_one();
-    bool ok = true;
-    int idx = 0;      // ring loads issued so far (over all pieces)
-    int q_loads = 0;  // pieces whose Q was issued
-    Piece x;
-    for (int it = 0; ok && next_piece(it, x, ok); ++it) {
-      if (!wait_all(bar_q_empty, (q_loads & 1) ^ 1)) {
-        ok = false;
-        break;
-      }
+      const int q_rows = kind == kTail ? plan.rows : plan.tile_rows();
+      const int copies = kind == kPair ? 2 : Plan::copies(q_rows);
       if (leader) {
-        const int tiles = x.kind == 2 ? 2 : 1;
-        const int box_rows = x.kind == 0 ? plan.rows : plan.rows * plan.tile_reqs;
-        mbar_arrive_expect_tx(bar_q_full, tiles * L::kBoxes * box_rows * 128);
-        for (int i = 0; i < tiles; ++i)
+        mbar_arrive_expect_tx(bar_q_full0 + 8 * i, copies * L::kBoxes * q_rows * 128);
+        // Two row tiles, or the rows of one at every 128 / copies rows.
+        for (int u = 0; u < copies; ++u)
 #pragma unroll
           for (int bx = 0; bx < L::kBoxes; ++bx)
-            tma_load_4d(sQ + i * L::kTileBytes + bx * L::kBoxBytes, x.kind == 0 ? &tm_qt : &tm_qp, bar_q_full, bx * 64,
-                        0, x.hk, x.kind == 0 ? x.req : (x.req + i) * plan.tile_reqs);
+            tma_load_4d(kind == kPair ? sQ + u * L::kTileBytes + bx * L::kBoxBytes
+                                      : sQ + i * L::kTileBytes + bx * L::kBoxBytes + u * (128 / copies) * 128,
+                        kind == kTail ? &tm_qt : &tm_qp, bar_q_full0 + 8 * i, bx * 64, 0, hk,
+                        kind == kPair ? req + u * plan.tile_reqs : req);
       }
       __syncwarp();
       ++q_loads;
-      // One K or V tile into the next ring slot.
-      auto load = [&](bool is_v, int t) {
-        const int s = idx % kStages;
-        if (!wait_all(bar_kv_empty0 + 8 * s, ((idx / kStages) & 1) ^ 1)) {
-          ok = false;
-          return;
-        }
-        if (leader) {
-          const uint32_t full = bar_kv_full0 + 8 * s;
-          mbar_arrive_expect_tx(full, L::kTileBytes);
-          const CUtensorMap* map = x.kind == 0 ? (is_v ? &tm_vt : &tm_kt) : (is_v ? &tm_vp : &tm_kp);
+      for (int t = t1 - 1; t >= t0; --t)
+        for (int v = 0; v < 2; ++v) {
+          const int s = slot0 + idx % n_slots;
+          if (!wait_all(bar_kv_empty0 + 8 * s, ((idx / n_slots) & 1) ^ 1)) {
+            ok = false;
+            return;
+          }
+          if (leader) {
+            const uint32_t full = bar_kv_full0 + 8 * s;
+            mbar_arrive_expect_tx(full, L::kTileBytes);
+            const CUtensorMap* map = kind == kTail ? (v ? &tm_vt : &tm_kt) : (v ? &tm_vp : &tm_kp);
 #pragma unroll
-          for (int bx = 0; bx < L::kBoxes; ++bx)
-            tma_load_4d(sRing + s * L::kTileBytes + bx * L::kBoxBytes, map, full, bx * 64, t * kBN, x.hk,
-                        x.kind == 0 ? x.req : 0);
+            for (int bx = 0; bx < L::kBoxes; ++bx)
+              tma_load_4d(sRing + s * L::kTileBytes + bx * L::kBoxBytes, map, full, bx * 64, t * kBN, hk,
+                          kind == kTail ? req : 0);
+          }
+          __syncwarp();
+          ++idx;
         }
-        __syncwarp();
-        ++idx;
-      };
-      // In the order the MMA warp takes them.
-      const int streams = x.kind == 2 ? 1 : 2;
-      const int n = last_of(x, 0) - first_of(x, 0);
-      for (int i = 0; i < streams && ok; ++i)
-        if (first_of(x, i) < last_of(x, i)) load(false, last_of(x, i) - 1);
-      for (int j = 0; j < n && ok; ++j)
-        for (int i = 0; i < streams && ok; ++i) {
-          const int t = last_of(x, i) - 1 - j;
-          if (t >= first_of(x, i)) load(true, t);
-          if (ok && t - 1 >= first_of(x, i)) load(false, t - 1);
+    };
+    // All tail tiles under one K/V head.
+    int tails = 0;
+    for (int b0 = 0; b0 < plan.B; b0 += 128) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int b = b0 + u * 32 + lane;
+        if (b < plan.B) tails += Plan::tiles_of(plan.len(b));
+      }
+    }
+    tails = __reduce_add_sync(0xffffffffu, tails);
+    const int pair_ctas = plan.pair_ctas(tails);
+    if (static_cast<int>(blockIdx.x) < pair_ctas) {
+      if (i == 0) {
+        slot0 = 0, n_slots = kStages;
+        const Cut cut(plan.pair_units(), pair_ctas);
+        const int c = blockIdx.x;
+        const int u0 = c < cut.parts ? cut.begin(c) : 0, u1 = c < cut.parts ? cut.begin(c + 1) : 0;
+        for (int u = u0; u < u1 && ok;) {
+          const int s = u / plan.prefix_tiles, t0 = u - s * plan.prefix_tiles;
+          const int t1 = min(plan.prefix_tiles, t0 + u1 - u);
+          run(kPair, s / plan.pairs(), 2 * (s % plan.pairs()) * plan.tile_reqs, t0, t1, s + c, plan.Np);
+          u += t1 - t0;
         }
+        if (ok) publish(kEnd, 0, 0, 0, 0, 0, 0, true);
+      }
+    } else {
+      const int singles = plan.ctas - pair_ctas;
+      const Cut cut(plan.odd_units() + tails * plan.Hkv, 2 * singles);
+      // Streams of different CTAs are neighbours on the line, so that few units
+      // go to many SMs.
+      const int c = i * singles + static_cast<int>(blockIdx.x) - pair_ctas;
+      const int u0 = c < cut.parts ? cut.begin(c) : 0, u1 = c < cut.parts ? cut.begin(c + 1) : 0;
+      int u = u0;
+      for (; u < min(u1, plan.odd_units()) && ok;) {
+        const int s = u / plan.prefix_tiles, t0 = u - s * plan.prefix_tiles;
+        const int t1 = min(plan.prefix_tiles, t0 + u1 - u);
+        run(kOdd, s, (plan.row_tiles - 1) * plan.tile_reqs, t0, t1, s + c, plan.Np);
+        u += t1 - t0;
+      }
+      int at = plan.odd_units();  // place of request b0's first tile
+      for (int b0 = 0; b0 < plan.B && at < u1 && ok; b0 += 32) {
+        const int n = b0 + lane < plan.B ? plan.len(b0 + lane) : 0;
+        const int nt = Plan::tiles_of(n);
+        int upto = nt;  // inclusive scan
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, off);
+          if (lane >= off) upto += y;
+        }
+        const int mine0 = at + (upto - nt) * plan.Hkv, mine1 = at + upto * plan.Hkv;
+        at += __shfl_sync(0xffffffffu, upto, 31) * plan.Hkv;
+        // Requests of these 32 that have a tile in this part.
+        unsigned todo = __ballot_sync(0xffffffffu, nt > 0 && mine0 < u1 && mine1 > u0);
+        while (todo != 0u && ok) {
+          const int k = __ffs(todo) - 1;
+          todo &= todo - 1;
+          const int a0 = __shfl_sync(0xffffffffu, mine0, k);
+          const int kn = __shfl_sync(0xffffffffu, n, k), knt = __shfl_sync(0xffffffffu, nt, k);
+          for (int hk = max(u0 - a0, 0) / knt; hk < plan.Hkv && ok; ++hk) {
+            const int a = a0 + hk * knt;
+            if (a >= u1) break;
+            run(kTail, hk, b0 + k, max(u0 - a, 0), min(u1 - a, knt), (b0 + k) * plan.Hkv + hk + c, kn);
+          }
+        }
+      }
+      if (ok) publish(kEnd, 0, 0, 0, 0, 0, 0, false);
     }
     if (!ok) {  // every copy issued has landed before the CTA exits
-      if (q_loads > 0) mbar_wait(bar_q_full, (q_loads - 1) & 1, nullptr, p.status, kStatusTimeout, lim);
-      for (int s = 0; s < kStages && s < idx; ++s) {
-        const int cnt = (idx - s + kStages - 1) / kStages;
-        mbar_wait(bar_kv_full0 + 8 * s, (cnt - 1) & 1, nullptr, p.status, kStatusTimeout, lim);
+      if (q_loads > 0) mbar_wait(bar_q_full0 + 8 * i, (q_loads - 1) & 1, nullptr, p.status, kStatusTimeout, lim);
+      for (int s = 0; s < n_slots && s < idx; ++s) {
+        const int cnt = (idx - s + n_slots - 1) / n_slots;
+        mbar_wait(bar_kv_full0 + 8 * (slot0 + s), (cnt - 1) & 1, nullptr, p.status, kStatusTimeout, lim);
       }
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
+  } else if (warp >= kMmaWarp) {
     setmaxnreg_dec<kControlRegs>();
     // ----------------------------------------------------------- MMA issue
+    const int me = warp == kMmaWarp ? 0 : 1;  // stream
     const bool leader = elect_one();
     constexpr uint32_t kIdS = idesc_bf16(128, kBN, false, false);
     constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true);
@@ -356,13 +510,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dQ = sdesc_k_sw128(sQ);
     const uint64_t dK = sdesc_k_sw128(sRing);
     const uint64_t dV = sdesc_mn_sw128(sRing, L::kBoxBytes);
-    auto issue_qk = [&](int i, int q_tile, int slot) {
-      const uint64_t dq = dQ + q_tile * kTileDesc, dk = dK + slot * kTileDesc;
+    auto issue_qk = [&](int i, int slot) {
+      const uint64_t dq = dQ + i * kTileDesc, dk = dK + slot * kTileDesc;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint64_t off = static_cast<uint64_t>(((kk / 4) * L::kBoxBytes + (kk % 4) * 32) >> 4);
         umma_ss(tmem + i * kBN, dq + off, dk + off, kIdS, kk > 0);
       }
+      umma_commit(bar_s_full0 + 8 * i);
     };
     auto issue_pv = [&](int i, int slot, bool acc, int part, int steps) {
       const uint64_t dv = dV + slot * kTileDesc;
@@ -376,125 +531,112 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     bool ok = true;
-    int idx = 0;  // ring position (over all pieces)
-    int g0 = 0, g1 = 0;
+    int idx = 0;  // ring position
+    int g = 0;    // key tiles so far: phase of the P barriers (the same for both streams of a pair CTA)
     int q_used = 0;
     Piece x;
-    for (int it = 0; ok && next_piece(it, x, ok); ++it) {
-      const bool both = x.kind == 2;  // both streams take the same keys
-      int qk_left = (last_of(x, 0) - first_of(x, 0)) + (last_of(x, 1) - first_of(x, 1));
-      if (!wait_all(bar_q_full, q_used & 1)) break;
-      ++q_used;
-      // S of stream i from the K tile in `slot`; the last of the piece frees Q.
-      auto qk = [&](int i, int slot) {
-        --qk_left;
-        if (leader) {
-          issue_qk(i, both ? i : 0, slot);
-          umma_commit(bar_s_full0 + 8 * i);
-          if (!both || i == 1) umma_commit(bar_kv_empty0 + 8 * slot);
-          if (qk_left == 0) umma_commit(bar_q_empty);
-        }
-        __syncwarp();
+    for (int it = 0; ok && next_piece(me, it, x, ok); ++it) {
+      const bool both = x.kind == kPair;
+      if (both && me == 1) continue;  // warp 8 issues for both streams
+      const int slot0 = both ? 0 : me * kHalf, n_slots = both ? kStages : kHalf;
+      const int i0 = both ? 0 : me, i1 = both ? 2 : me + 1;
+      auto take = [&](int& slot) {
+        slot = slot0 + idx % n_slots;
+        if (!wait_all(bar_kv_full0 + 8 * slot, (idx / n_slots) & 1)) return false;
+        ++idx;
+        tc_fence_after();
+        return true;
       };
       int slot_k = 0, slot_v = 0;
-      for (int i = 0; i < 2 && ok; ++i) {
-        if (first_of(x, i) >= last_of(x, i)) continue;
-        if (!both || i == 0) {
-          slot_k = idx % kStages;
-          if (!wait_all(bar_kv_full0 + 8 * slot_k, (idx / kStages) & 1)) {
-            ok = false;
-            break;
-          }
-          ++idx;
-          tc_fence_after();
-        }
-        qk(i, slot_k);
+      if (!wait_all(bar_q_full0 + 8 * me, q_used & 1) || !take(slot_k)) break;
+      ++q_used;
+      tc_fence_after();
+      if (leader) {
+        for (int i = i0; i < i1; ++i) issue_qk(i, slot_k);
+        umma_commit(bar_kv_empty0 + 8 * slot_k);
+        if (x.t1 - 1 == x.t0) umma_commit(bar_q_empty0 + 8 * me);
       }
-      const int n = last_of(x, 0) - first_of(x, 0);
-      for (int j = 0; j < n && ok; ++j)
-        for (int i = 0; i < 2 && ok; ++i) {
-          const int t = last_of(x, i) - 1 - j;
-          if (t < first_of(x, i)) continue;
-          if (!both || i == 0) {
-            slot_v = idx % kStages;
-            if (!wait_all(bar_kv_full0 + 8 * slot_v, (idx / kStages) & 1)) {
-              ok = false;
-              break;
-            }
-            ++idx;
-          }
-          // Keys past the request's length: their weights are 0, but a value
-          // left in the cache may be NaN or Inf, so the rows an instruction
-          // (16 keys) would still read are cleared, and the rest left out.
-          int steps = kBN / 16;
-          const int valid = x.keys - t * kBN;
-          if (x.kind == 0 && valid < kBN) {
-            steps = (valid + 15) / 16;
-            const uint32_t v0 = sRing + slot_v * L::kTileBytes;
-            const int rows = steps * 16 - valid;
-            for (int e = lane; e < rows * 8 * L::kBoxes; e += 32)
-              st_shared_v4(v0 + (e / (rows * 8)) * L::kBoxBytes + (valid + (e / 8) % rows) * 128 + (e % 8) * 16, 0u, 0u,
-                           0u, 0u);
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-          }
-          const uint32_t ph = (i ? g1 : g0) & 1;
-          if (!wait_all(bar_p_part0 + 8 * i, ph)) {
+      __syncwarp();
+      for (int t = x.t1 - 1; t >= x.t0 && ok; --t, ++g) {
+        if (!take(slot_v)) {
+          ok = false;
+          break;
+        }
+        // Keys past a request's length: their weights are 0, but a value left
+        // in the cache may be NaN or Inf, so the rows an instruction (16 keys)
+        // would still read are cleared, and the rest left out.
+        int steps = kBN / 16;
+        const int valid = x.keys - t * kBN;
+        if (x.kind == kTail && valid < kBN) {
+          steps = (valid + 15) / 16;
+          const uint32_t v0 = sRing + slot_v * L::kTileBytes;
+          const int rows = steps * 16 - valid;
+          for (int e = lane; e < rows * 8 * L::kBoxes; e += 32)
+            st_shared_v4(v0 + (e / (rows * 8)) * L::kBoxBytes + (valid + (e / 8) % rows) * 128 + (e % 8) * 16, 0u, 0u,
+                         0u, 0u);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        for (int i = i0; i < i1 && ok; ++i) {
+          if (!wait_all(bar_p_part0 + 8 * i, g & 1)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          if (leader) issue_pv(i, slot_v, j > 0, 0, steps);
+          if (leader) issue_pv(i, slot_v, t < x.t1 - 1, 0, steps);
           __syncwarp();
-          if (!wait_all(bar_p_full0 + 8 * i, ph)) {
+          if (!wait_all(bar_p_full0 + 8 * i, g & 1)) {
             ok = false;
             break;
           }
-          i ? ++g1 : ++g0;
           tc_fence_after();
           if (leader) {
             issue_pv(i, slot_v, true, 1, steps);
-            if (t == first_of(x, i)) umma_commit(bar_o_full0 + 8 * i);
-            if (!both || i == 1) umma_commit(bar_kv_empty0 + 8 * slot_v);
+            if (t == x.t0) umma_commit(bar_o_full0 + 8 * i);
+            if (i == i1 - 1) umma_commit(bar_kv_empty0 + 8 * slot_v);
           }
           __syncwarp();
-          if (t > first_of(x, i)) {
-            if (!both || i == 0) {
-              slot_k = idx % kStages;
-              if (!wait_all(bar_kv_full0 + 8 * slot_k, (idx / kStages) & 1)) {
-                ok = false;
-                break;
-              }
-              ++idx;
-              tc_fence_after();
+          if (t > x.t0) {
+            if (i == i0 && !take(slot_k)) {
+              ok = false;
+              break;
             }
-            qk(i, slot_k);
+            if (leader) {
+              issue_qk(i, slot_k);
+              if (i == i1 - 1) {
+                umma_commit(bar_kv_empty0 + 8 * slot_k);
+                if (t - 1 == x.t0) umma_commit(bar_q_empty0 + 8 * me);  // the piece's last Q K^T
+              }
+            }
+            __syncwarp();
           }
         }
+      }
     }
     // Every MMA issued completes before tensor memory is freed.
-    if (leader) umma_commit(bar_drain);
+    if (leader) umma_commit(bar_drain0 + 8 * me);
     __syncwarp();
-    mbar_wait(bar_drain, 0, nullptr, p.status, kStatusTimeout, lim);
+    mbar_wait(bar_drain0 + 8 * me, 0, nullptr, p.status, kStatusTimeout, lim);
     __syncwarp();
   } else {
     setmaxnreg_inc<kSoftmaxRegs>();
     // ------------------------------------------------------------- softmax
     const int i = warp / 4;
-    const int r = threadIdx.x % 128;  // row of the row tile
-    const int wr = r - lane;          // first row of this warp
-    const uint32_t lane_off = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const int w4 = warp % 4;
+    const uint32_t lane_off = static_cast<uint32_t>(w4 * 32) << 16;
     const uint32_t tS = tmem + i * kBN + lane_off;
     const uint32_t tO = tmem + 2 * kBN + i * D + lane_off;
     bool ok = true;
-    int g = 0;    // key tiles over all pieces: phases of the S barrier
-    int n_o = 0;  // pieces with key tiles of this stream: phase of the O barrier
+    int g = 0;  // key tiles so far: phase of the S barrier
     Piece x;
-    for (int it = 0; ok && next_piece(it, x, ok); ++it) {
-      const int first = first_of(x, i), last = last_of(x, i);
-      if (first >= last) continue;
-      const int req0 = x.kind == 0 ? x.req : (x.req + (x.kind == 2 ? i : 0)) * plan.tile_reqs;
-      const int rows = x.kind == 0 ? plan.rows : min(plan.tile_reqs, plan.B - req0) * plan.rows;
+    int it = 0;  // pieces so far: phase of the O barrier
+    for (; ok && next_piece(i, it, x, ok); ++it) {
+      const int req0 = x.kind == kPair ? x.req + i * plan.tile_reqs : x.req;
+      const int rows = x.kind == kTail ? plan.rows : min(plan.tile_reqs, plan.B - req0) * plan.rows;
+      const int copies = x.kind == kPair ? 1 : Plan::copies(x.kind == kTail ? plan.rows : plan.tile_rows());
+      // This warp's rows of the row tile and, with copies, its share of the keys.
+      const int per = 4 / copies;  // warps a copy
+      const int wr = (w4 % per) * 32, r = wr + lane, kq = w4 / per;
       const bool active = wr < rows, mine = r < rows;
       // The row's request, head and token, its position (in a tail: counted
       // from the tail's start) and the keys it sees.  Rows of the tile that
@@ -505,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (mine) {
         const int rr = r % plan.rows, req = req0 + r / plan.rows;
         m_ref = -INFINITY;
-        if (x.kind == 0) {
+        if (x.kind == kTail) {
           pos = x.keys - plan.Nq + rr % plan.Nq;
           seen = max(pos + 1, 0);
         } else {
@@ -514,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if constexpr (kBias) slope2 = __ldg(p.sm.slopes + x.hk * plan.G + rr / plan.Nq) * 1.4426950408889634f;
       }
-      for (int t = last - 1; t >= first; --t, ++g) {
+      for (int t = x.t1 - 1; t >= x.t0; --t, ++g) {
         const bool got =
             mbar_wait_hint(bar_s_full0 + 8 * i, g & 1, abort_word, p.status, kStatusTimeout, lim, kSuspendHintNs);
         if (__any_sync(0xffffffffu, !got)) {
@@ -529,48 +671,58 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         tc_fence_after();
-        const int k0 = t * kBN;
-        softmax_tile<D, kCap, kBias>(tS, tO, 0, seen - k0, static_cast<float>(pos - k0), slope2, p.sm, t < last - 1,
-                                     m_ref, l, bar_p_part0 + 8 * i, bar_p_full0 + 8 * i, lane);
+        const int b = seen - t * kBN;
+        const float dist0 = static_cast<float>(pos - t * kBN);
+        const bool have_o = t < x.t1 - 1;
+        if (copies == 4)
+          softmax_share<D, kCap, kBias, 32>(tS, tO, kq, b, dist0, slope2, p.sm, have_o, m_ref, l, bar_p_part0 + 8 * i,
+                                            bar_p_full0 + 8 * i, lane);
+        else if (copies == 2)
+          softmax_share<D, kCap, kBias, 64>(tS, tO, kq, b, dist0, slope2, p.sm, have_o, m_ref, l, bar_p_part0 + 8 * i,
+                                            bar_p_full0 + 8 * i, lane);
+        else
+          softmax_tile<D, kCap, kBias>(tS, tO, 0, b, dist0, slope2, p.sm, have_o, m_ref, l, bar_p_part0 + 8 * i,
+                                       bar_p_full0 + 8 * i, lane);
       }
       if (!ok) break;
       {
-        const bool got = mbar_wait(bar_o_full0 + 8 * i, n_o & 1, abort_word, p.status, kStatusTimeout, lim);
+        const bool got = mbar_wait(bar_o_full0 + 8 * i, it & 1, abort_word, p.status, kStatusTimeout, lim);
         if (__any_sync(0xffffffffu, !got)) {
           ok = false;
           break;
         }
-        ++n_o;
         tc_fence_after();
       }
       if (!active) continue;
       const bool empty = !mine || m_ref == -INFINITY;
       const float inv = empty ? 0.f : 1.f / l;
-      const size_t row0 = x.kind == 0 ? static_cast<size_t>(2 * x.slot + i) * plan.rows
-                                      : static_cast<size_t>(2 * x.slot + i) * (plan.tile_reqs * plan.rows);
-      float* o = (x.kind == 0 ? p.tail_o : p.prefix_o) + (row0 + wr) * D;
-      const bool bad =
-          store_rows<D>(tO, base + L::kStageOff + warp * L::kStageWarpBytes, nullptr, o, D, rows - wr, inv);
+      const size_t row0 = x.kind == kPair ? static_cast<size_t>(2 * x.slot + i) * plan.tile_rows()
+                                          : static_cast<size_t>(x.slot * copies + kq) *
+                                                (x.kind == kOdd ? plan.tile_rows() : plan.rows);
+      float* o = (x.kind == kPair ? p.pair_o : x.kind == kOdd ? p.odd_o : p.tail_o) + (row0 + wr) * D;
+      const bool bad = copies > 1 ? store_row_f32<D>(tO, o + lane * D, mine, inv)
+                                  : store_rows<D>(tO, base + L::kStageOff + warp * L::kStageWarpBytes, nullptr, o, D,
+                                                  rows - wr, inv);
       if (mine)
-        (x.kind == 0 ? p.tail_lse : p.prefix_lse)[row0 + r] =
-            empty ? -INFINITY : (m_ref + lg2_approx(l)) * 0.69314718055994531f;
+        (x.kind == kPair ? p.pair_lse : x.kind == kOdd ? p.odd_lse : p.tail_lse)[row0 + r] =
+            empty ? -INFINITY : m_ref + lg2_approx(l);
       // A value row that is not finite among the new tokens of a request does
       // not reach the tokens before it (see repair_row).
-      if (x.kind == 0 && plan.Nq > 1) {
+      if (x.kind == kTail && plan.Nq > 1) {
         unsigned redo = __ballot_sync(0xffffffffu, bad && !empty && l <= FLT_MAX);
         while (redo != 0u) {
           const int k = __ffs(redo) - 1;
           redo &= redo - 1;
           __syncwarp();
-          const int j0 = first * kBN, j1 = min(__shfl_sync(0xffffffffu, seen, k), last * kBN);
-          const int ps = __shfl_sync(0xffffffffu, pos, k);
+          const int ps = __shfl_sync(0xffffffffu, pos, k), sn = __shfl_sync(0xffffffffu, seen, k);
           const float mr = __shfl_sync(0xffffffffu, m_ref, k), iv = __shfl_sync(0xffffffffu, inv, k);
           const float sl = __shfl_sync(0xffffffffu, slope2, k);
           const size_t q_row =
               (static_cast<size_t>(x.req) * plan.Hq + x.hk * plan.G) * plan.Nq + wr + k;  // rows of a K/V head are adjacent
           repair_row<D>(p.q + q_row * D, p.kt + x.req * p.kt_s[0] + x.hk * p.kt_s[1],
-                        p.vt + x.req * p.vt_s[0] + x.hk * p.vt_s[1], p.kt_s[2], p.vt_s[2], j0, j1, ps, mr, iv, sl, p.sm,
-                        kCap, kBias, nullptr, o + k * D);
+                        p.vt + x.req * p.vt_s[0] + x.hk * p.vt_s[1], p.kt_s[2], p.vt_s[2], x.t0 * kBN,
+                        min(sn, x.t1 * kBN), kBN / copies, kBN, kq, ps, mr, iv, sl, p.sm, kCap, kBias, nullptr,
+                        o + k * D);
         }
       }
     }
@@ -585,15 +737,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partial results of every row, as pa_attn_merge defines it:
-//     M = max_p lse_p,  w_p = exp(lse_p - M),  o = sum w_p o_p / sum w_p
+//     M = max_p lse_p,  w_p = 2^(lse_p - M),  o = sum w_p o_p / sum w_p
 // One block a (request, K/V head); its rows are dealt to groups of warps, the
 // partials of a row to the warps of its group.  The partials lie where the
-// kernel above put them: the same line is cut into the same parts.
+// kernel above put them: the same lines are cut into the same parts.
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __grid_constant__ Params p,
                                                                         __nv_bfloat16* o, float* lse) {
   constexpr int kCols = D / 32;
-  __shared__ long long sums[2][kMergeWarps];
+  __shared__ int sums[2][kMergeWarps];
   __shared__ float part_m[kMergeWarps], part_l[kMergeWarps];
   __shared__ float part_o[kMergeWarps][D];
   const Plan& plan = p.plan;
@@ -601,46 +753,45 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
   const int req = blockIdx.x / plan.Hkv, hk = blockIdx.x % plan.Hkv;
 
   // Tail tiles (under one K/V head) of all requests, and of those before req.
-  long long all = 0, before = 0;
+  int all = 0, before = 0;
   for (int b = threadIdx.x; b < plan.B; b += kMergeWarps * 32) {
     const int n = Plan::tiles_of(plan.len(b));
     all += n;
     if (b < req) before += n;
     if (blockIdx.x == 0 && __ldg(plan.tail_lens + b) != plan.len(b)) atomicCAS(p.status, 0, kStatusBadInput);
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, off);
-    before += __shfl_xor_sync(0xffffffffu, before, off);
-  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
   if (lane == 0) sums[0][warp] = all, sums[1][warp] = before;
   __syncthreads();
   all = before = 0;
+#pragma unroll
   for (int w = 0; w < kMergeWarps; ++w) all += sums[0][w], before += sums[1][w];
 
+  // Parts [p0, p1) of the pairs' or the singles' line hold the prefix under this
+  // row tile, [t0, t1) of the singles' the tail.
   const int n_tail = Plan::tiles_of(plan.len(req));
-  const long long total = plan.prefix_units() + all * plan.Hkv;
+  const int pair_ctas = plan.pair_ctas(all);
   const int mt = req / plan.tile_reqs;
-  const int seg_p = hk * plan.pairs + mt / 2, seg_t = req * plan.Hkv + hk;
-  const bool single = plan.single(mt / 2);
-  const long long at_p = static_cast<long long>(seg_p) * plan.prefix_tiles;
-  const long long at_t = plan.prefix_units() + before * plan.Hkv + static_cast<long long>(hk) * n_tail;
-  // CTAs that hold the units [at, at + n) of the line: [c0, c1).
-  auto holders = [&](long long at, long long n, int& c0, int& c1) {
-    auto holder = [&](long long u) {
-      int c = static_cast<int>(u * plan.ctas / total);
-      while (plan.part(total, c + 1) <= u) ++c;
-      while (plan.part(total, c) > u) --c;
-      return c;
-    };
-    c0 = c1 = 0;
-    if (n > 0) c0 = holder(at), c1 = holder(at + n - 1) + 1;
-  };
-  int p0, p1, t0, t1;
-  holders(at_p, plan.prefix_segs ? plan.prefix_tiles : 0, p0, p1);
-  holders(at_t, n_tail, t0, t1);
-  const int streams_p = single ? 2 : 1;
-  const int n_p = (p1 - p0) * streams_p, n_parts = n_p + (t1 - t0) * 2;
+  const bool pair = mt < 2 * plan.pairs();
+  const int copies_p = pair ? 1 : Plan::copies(plan.tile_rows()), copies_t = Plan::copies(plan.rows);
+  const int seg_p = pair ? hk * plan.pairs() + mt / 2 : hk, seg_t = req * plan.Hkv + hk;
+  const Cut singles(plan.odd_units() + all * plan.Hkv, 2 * (plan.ctas - pair_ctas));
+  int p0 = 0, p1 = 0, t0 = 0, t1 = 0;
+  if (plan.row_tiles > 0) {
+    const Cut pairs(plan.pair_units(), pair_ctas);
+    const Cut& cut = pair ? pairs : singles;
+    p0 = cut.holder(seg_p * plan.prefix_tiles);
+    p1 = cut.holder((seg_p + 1) * plan.prefix_tiles - 1) + 1;
+  }
+  if (n_tail > 0) {
+    const int at = plan.odd_units() + before * plan.Hkv + hk * n_tail;
+    t0 = singles.holder(at);
+    t1 = singles.holder(at + n_tail - 1) + 1;
+  }
+  const int n_p = (p1 - p0) * copies_p, n_parts = n_p + (t1 - t0) * copies_t;
+  const float* const p_o = pair ? p.pair_o : p.odd_o;
+  const float* const p_lse = pair ? p.pair_lse : p.odd_lse;
 
   int group = kMergeWarps;  // warps a row
   while (group > 1 && group * plan.rows > kMergeWarps) group /= 2;
@@ -656,22 +807,15 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
       const float* src = nullptr;
       float my = -INFINITY;
       if (k < n_parts) {
-        const bool pre = k < n_p;
-        const int q = pre ? k : k - n_p, st = pre ? streams_p : 2;
-        const int c = (pre ? p0 : t0) + q / st;
-        const long long at = pre ? at_p : at_t;
-        const int n_seg = pre ? plan.prefix_tiles : n_tail;
-        // The piece's tiles; its second stream has the smaller half.
-        const long long a = max(plan.part(total, c) - at, 0ll);
-        const long long b = min(plan.part(total, c + 1) - at, static_cast<long long>(n_seg));
-        const int i = pre && !single ? (mt & 1) : q % st;
-        const long long n = pre && !single ? b - a : (i == 0 ? (b - a + 1) / 2 : (b - a) / 2);
-        if (n > 0) {
-          const size_t row = pre ? static_cast<size_t>(2 * (seg_p + c) + i) * (plan.tile_reqs * plan.rows) +
-                                       (req % plan.tile_reqs) * plan.rows + rr
-                                 : static_cast<size_t>(2 * (seg_t + c) + i) * plan.rows + rr;
-          my = __ldcg((pre ? p.prefix_lse : p.tail_lse) + row);
-          src = (pre ? p.prefix_o : p.tail_o) + row * D;
+        if (k < n_p) {
+          const int slot = pair ? 2 * (seg_p + p0 + k) + (mt & 1) : (seg_p + p0) * copies_p + k;
+          const size_t row = static_cast<size_t>(slot) * plan.tile_rows() + (req % plan.tile_reqs) * plan.rows + rr;
+          my = __ldcg(p_lse + row);
+          src = p_o + row * D;
+        } else {
+          const size_t row = static_cast<size_t>((seg_t + t0) * copies_t + k - n_p) * plan.rows + rr;
+          my = __ldcg(p.tail_lse + row);
+          src = p.tail_o + row * D;
         }
       }
       float mx = my;
@@ -679,8 +823,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
       for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       const float nm = fmaxf(m, mx);
       if (nm == -INFINITY && !__any_sync(0xffffffffu, my != my)) continue;
-      const float w = (my == -INFINITY) ? 0.f : expf(my - nm);
-      const float keep = (m == -INFINITY) ? 0.f : expf(m - nm);
+      const float w = (my == -INFINITY) ? 0.f : exp2f(my - nm);
+      const float keep = (m == -INFINITY) ? 0.f : exp2f(m - nm);
       m = nm;
       float lw = w;
 #pragma unroll
@@ -689,7 +833,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
 #pragma unroll
       for (int u = 0; u < kCols; ++u) acc[u] *= keep;
       const int cnt = min(32, (n_parts - k0 - wi + group - 1) / group);
-#pragma unroll 4
+#pragma unroll 8
       for (int e = 0; e < cnt; ++e) {
         const float we = __shfl_sync(0xffffffffu, w, e);
         const float* s = reinterpret_cast<const float*>(
@@ -719,13 +863,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
       if (wi == 0) {
         float nm = m;
         for (int w = 1; w < group; ++w) nm = fmaxf(nm, part_m[warp + w]);
-        const float base = (nm == -INFINITY) ? 0.f : nm;
-        const float keep = expf(m - base);
+        const float ref = (nm == -INFINITY) ? 0.f : nm;
+        const float keep = exp2f(m - ref);
         l *= keep;
 #pragma unroll
         for (int u = 0; u < kCols; ++u) acc[u] *= keep;
         for (int w = 1; w < group; ++w) {
-          const float f = expf(part_m[warp + w] - base);
+          const float f = exp2f(part_m[warp + w] - ref);
           l = fmaf(f, part_l[warp + w], l);
 #pragma unroll
           for (int u = 0; u < kCols; ++u) acc[u] = fmaf(f, part_o[warp + w][lane * kCols + u], acc[u]);
@@ -745,7 +889,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
       } else {
         *reinterpret_cast<uint32_t*>(o + row * D + lane * kCols) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
       }
-      if (lane == 0) lse[row] = none ? -INFINITY : m + logf(l);
+      if (lane == 0) lse[row] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
     }
   }
 }

@@ -558,7 +558,7 @@ int launch_block_norm(const pa::norm::Params& prm, bool x32, cudaStream_t stream
 }
 
 // Shapes of a shared-prefix call; false where the rows of one request under one
-// K/V head do not fit a row tile.
+// K/V head do not fit a row tile, or the key tiles a 32-bit count.
 bool shared_plan(int B, int Hq, int Hkv, int Nq, int Np, int Nt, int ctas, pa::shared::Plan* plan) {
   const long long rows = static_cast<long long>(Hq / Hkv) * Nq;
   if (rows < 1 || rows > pa::kBM) return false;
@@ -569,33 +569,38 @@ bool shared_plan(int B, int Hq, int Hkv, int Nq, int Np, int Nt, int ctas, pa::s
   plan->Nq = Nq;
   plan->rows = static_cast<int>(rows);
   plan->tile_reqs = std::min(B, pa::kBM / plan->rows);
-  plan->row_tiles = (B + plan->tile_reqs - 1) / plan->tile_reqs;
-  plan->pairs = (plan->row_tiles + 1) / 2;
+  plan->row_tiles = Np > 0 ? (B + plan->tile_reqs - 1) / plan->tile_reqs : 0;
   plan->Np = Np;
   plan->Nt = Nt;
   plan->prefix_tiles = (Np + pa::kBN - 1) / pa::kBN;
-  plan->prefix_segs = Np > 0 ? Hkv * plan->pairs : 0;
   plan->ctas = ctas;
   plan->tail_lens = nullptr;
-  return true;
+  // The kernels count key tiles in 32 bits.
+  const long long units = static_cast<long long>(Hkv) * (static_cast<long long>(plan->prefix_tiles) * plan->row_tiles +
+                                                         static_cast<long long>(B) * ((Nt + pa::kBN - 1) / pa::kBN));
+  return units < (1ll << 30);
 }
 
-// Byte offsets of the four parts of a shared-prefix workspace (each on a
-// 256-byte boundary), and their end.
+// Byte offsets of the parts of a shared-prefix workspace (each on a 256-byte
+// boundary), and their end.
 struct SharedWorkspace {
-  uint64_t prefix_o, prefix_lse, tail_o, tail_lse, end;
+  uint64_t pair_o, pair_lse, odd_o, odd_lse, tail_o, tail_lse, end;
 };
 
 SharedWorkspace shared_workspace(const pa::shared::Plan& plan, int d) {
+  using pa::shared::kMaxCtas;
   auto up = [](uint64_t n) { return (n + 255) & ~255ull; };
-  const uint64_t pre =
-      plan.prefix_segs ? 2ull * (plan.prefix_segs + pa::shared::kMaxCtas) * plan.tile_reqs * plan.rows : 0;
+  const uint64_t rows = plan.rows, tile = plan.tile_rows();
+  const uint64_t pair = plan.pairs() > 0 ? (static_cast<uint64_t>(plan.Hkv) * plan.pairs() + kMaxCtas) * 2 * tile : 0;
+  const uint64_t odd = plan.odd() ? (plan.Hkv + 2ull * kMaxCtas) * plan.copies(plan.tile_rows()) * tile : 0;
   const uint64_t tail =
-      plan.Nt > 0 ? 2ull * (static_cast<uint64_t>(plan.B) * plan.Hkv + pa::shared::kMaxCtas) * plan.rows : 0;
+      plan.Nt > 0 ? (static_cast<uint64_t>(plan.B) * plan.Hkv + 2ull * kMaxCtas) * plan.copies(plan.rows) * rows : 0;
   SharedWorkspace w;
-  w.prefix_o = 0;
-  w.prefix_lse = up(pre * d * 4);
-  w.tail_o = w.prefix_lse + up(pre * 4);
+  w.pair_o = 0;
+  w.pair_lse = up(pair * d * 4);
+  w.odd_o = w.pair_lse + up(pair * 4);
+  w.odd_lse = w.odd_o + up(odd * d * 4);
+  w.tail_o = w.odd_lse + up(odd * 4);
   w.tail_lse = w.tail_o + up(tail * d * 4);
   w.end = w.tail_lse + up(tail * 4);
   return w;
@@ -644,7 +649,7 @@ int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_pre
   if (Nq == 0) return PA_OK;
   pa::shared::Plan plan;
   if (!shared_plan(B, Hq, Hkv, Nq, Np, Nt, 1, &plan))
-    return fail(PA_ERR_UNSUPPORTED, "(Hq / Hkv) * Nq must be <= %d", pa::kBM);
+    return fail(PA_ERR_UNSUPPORTED, "(Hq / Hkv) * Nq must be <= %d, the key tiles of all requests < 2^30", pa::kBM);
   if (!tail_lens || !lse) return fail(PA_ERR_INVALID_ARG, "null pointer argument");
   if (!aligned(tail_lens, 4) || !aligned(lse, 4))
     return fail(PA_ERR_MISALIGNED, "tail_lens and lse must be 4-byte aligned");
@@ -705,8 +710,10 @@ int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_pre
     prm.vt_s[i] = vt.s[i];
   }
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  prm.prefix_o = reinterpret_cast<float*>(w + ws.prefix_o);
-  prm.prefix_lse = reinterpret_cast<float*>(w + ws.prefix_lse);
+  prm.pair_o = reinterpret_cast<float*>(w + ws.pair_o);
+  prm.pair_lse = reinterpret_cast<float*>(w + ws.pair_lse);
+  prm.odd_o = reinterpret_cast<float*>(w + ws.odd_o);
+  prm.odd_lse = reinterpret_cast<float*>(w + ws.odd_lse);
   prm.tail_o = reinterpret_cast<float*>(w + ws.tail_o);
   prm.tail_lse = reinterpret_cast<float*>(w + ws.tail_lse);
   prm.sm = score_mod(scale, softcap, slopes);

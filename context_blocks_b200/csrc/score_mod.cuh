@@ -269,10 +269,11 @@ __device__ __noinline__ bool store_rows(uint32_t tO, uint32_t stg, __nv_bfloat16
 // maximum m and sum the softmax found (hidden scores never entered those).
 // Rare and slow (about 40 instructions a key); q, k, v: the row's query, and
 // key and value row 0 of its head.  pos: the row's position among the keys.
+// Only keys j with (j % period) / share == which count (share = period: all).
 template <int D>
 __device__ __noinline__ void repair_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
-                                        long long k_stride, long long v_stride, int j0, int j1, int pos, float m,
-                                        float inv, float slope2, ScoreMod sm, bool cap, bool bias,
+                                        long long k_stride, long long v_stride, int j0, int j1, int share, int period,
+                                        int which, int pos, float m, float inv, float slope2, ScoreMod sm, bool cap, bool bias,
                                         __nv_bfloat16* o_bf16, float* o_f32) {
   constexpr int kCols = D / 32;
   const int lane = threadIdx.x % 32;
@@ -283,6 +284,7 @@ __device__ __noinline__ void repair_row(const __nv_bfloat16* q, const __nv_bfloa
     acc[u] = 0.f;
   }
   for (int j = j0; j < j1; ++j) {
+    if ((j % period) / share != which) continue;
     const __nv_bfloat16* kr = k + j * k_stride + lane * kCols;
     const __nv_bfloat16* vr = v + j * v_stride + lane * kCols;
     float dot = 0.f;

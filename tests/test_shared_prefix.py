@@ -233,7 +233,9 @@ def test_workspace_sizes():
 
 
 def _line(total_tiles, ctas):
-    return [(total_tiles * c // ctas, total_tiles * (c + 1) // ctas) for c in range(ctas)]
+    parts = max(min(total_tiles, ctas), 1)
+    q, r = divmod(total_tiles, parts)
+    return [(c * q + min(c, r), (c + 1) * q + min(c + 1, r)) for c in range(parts)]
 
 
 @pytest.mark.parametrize("segs", [[3, 1, 4, 1, 5], [0, 0, 7, 0], [1] * 400, [1000], [37, 0, 2, 511, 1]])
