@@ -7,11 +7,15 @@
 //     hidden keys:  s_ij <- -inf, chosen by comparison, never added, so that a
 //                   NaN or Inf score of a hidden key does not reach the softmax
 //
-// Everything is kept in log2 units (x = s * log2 e), fp32.  tanh is taken as
-// 1 - 2 / (2^(2 u log2 e) + 1): ex2 and rcp of the special-function unit, whose
-// errors (2^-22 relative) become at most c * 2^-21 in the capped score.  The
-// unit's own tanh has a relative error of 2^-11, which at c = 50 would be 0.02
-// in the exponent.
+// Everything is kept in log2 units (x = s * log2 e), fp32.  tanh(u), u = s / c, is
+// u * g(u^2) with a degree-5 polynomial g (relative error 5.9e-7,
+// gen_tanh_poly.py) where all of a warp's scores of a tile have |u| <= 1, and
+// 1 - 2 / (2^(2 u log2 e) + 1) otherwise: ex2 and rcp of the special-function
+// unit, whose errors (2^-22 relative) become at most c * 2^-21 in the capped
+// score.  The polynomial takes half the special-function work of a score away,
+// which bounds the kernels: 8192 capped causal keys MEASURED_CAP.  The unit's own
+// tanh has a relative error of 2^-11, which at c = 50 would be 0.02 in the
+// exponent.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -43,11 +47,23 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// tanh(u) = u * sum_i kTanhC[i] u^(2 i) for |u| <= 1 (gen_tanh_poly.py).
+constexpr float kTanhC[6] = {9.999994040e-01f,  -3.332904279e-01f, 1.328143328e-01f,
+                             -5.160567537e-02f, 1.674311422e-02f,  -3.067060374e-03f};
+
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float r;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Scalars of the score modification, set by the host.
 struct ScoreMod {
   float scale_log2;     // scale * log2(e)
   float cap_k;          // 2 * scale * log2(e) / c
   float cap_log2;       // c * log2(e)
+  float cap_u;          // scale / c
+  float cap_g[6];       // cap_log2 * (coefficients of g)
   const float* slopes;  // [Hq], natural units; read where the kernel is built for a bias
 };
 
@@ -87,26 +103,52 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int a, in
       if (dist0 <= 0.f) sl = -slope2;
       linear = __all_sync(0xffffffffu, dist0 <= 0.f || dist0 >= static_cast<float>(kBN - 1));
     }
-    const uint64_t c2 = f2(c, c), ck2 = f2(sm.cap_k, sm.cap_k);
-    const uint64_t cl2 = f2(sm.cap_log2, sm.cap_log2), m2cl2 = f2(-2.f * sm.cap_log2, -2.f * sm.cap_log2);
-    const uint64_t one2 = f2(1.f, 1.f);
+    const uint64_t c2 = f2(c, c);
     const uint64_t sl2 = f2(sl, sl), b02 = f2(-sl * dist0, -sl * dist0);
+    auto bias2 = [&](int e) { return f2_fma(sl2, f2(static_cast<float>(e), static_cast<float>(e + 1)), b02); };
+    if constexpr (kCap) {
+      float a4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < kBN; e += 2) {
-      uint64_t x;
-      if constexpr (kCap) {
-        float u0, u1;
-        f2_split(f2_mul(f2(s[e], s[e + 1]), ck2), u0, u1);
-        f2_split(f2_add(f2(ex2_approx(u0), ex2_approx(u1)), one2), u0, u1);
-        x = f2_fma(f2(rcp_approx(u0), rcp_approx(u1)), m2cl2, cl2);
-        if constexpr (kBias)
-          if (linear) x = f2_add(x, f2_fma(sl2, f2(static_cast<float>(e), static_cast<float>(e + 1)), b02));
+      for (int e = 0; e < kBN; e += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a4[k] = max3_abs(a4[k], s[e + k], s[e + 4 + k]);
+      const float amax = max3_abs(max3_abs(a4[0], a4[1], a4[2]), a4[3], 0.f) * sm.cap_u;
+      if (__all_sync(0xffffffffu, amax <= 1.f)) {
+        const uint64_t k2 = f2(sm.cap_u, sm.cap_u);
+        uint64_t g[6];
+#pragma unroll
+        for (int u = 0; u < 6; ++u) g[u] = f2(sm.cap_g[u], sm.cap_g[u]);
+#pragma unroll
+        for (int e = 0; e < kBN; e += 2) {
+          const uint64_t v = f2_mul(f2(s[e], s[e + 1]), k2), w = f2_mul(v, v);
+          uint64_t x = f2_fma(g[5], w, g[4]);
+#pragma unroll
+          for (int u = 3; u >= 0; --u) x = f2_fma(x, w, g[u]);
+          if (kBias && linear)
+            x = f2_fma(x, v, bias2(e));
+          else
+            x = f2_mul(x, v);
+          f2_split(x, s[e], s[e + 1]);
+        }
       } else {
-        x = linear ? f2_fma(f2(s[e], s[e + 1]), c2,
-                            f2_fma(sl2, f2(static_cast<float>(e), static_cast<float>(e + 1)), b02))
-                   : f2_mul(f2(s[e], s[e + 1]), c2);
+        const uint64_t ck2 = f2(sm.cap_k, sm.cap_k), one2 = f2(1.f, 1.f);
+        const uint64_t cl2 = f2(sm.cap_log2, sm.cap_log2), m2cl2 = f2(-2.f * sm.cap_log2, -2.f * sm.cap_log2);
+#pragma unroll
+        for (int e = 0; e < kBN; e += 2) {
+          float u0, u1;
+          f2_split(f2_mul(f2(s[e], s[e + 1]), ck2), u0, u1);
+          f2_split(f2_add(f2(ex2_approx(u0), ex2_approx(u1)), one2), u0, u1);
+          uint64_t x = f2_fma(f2(rcp_approx(u0), rcp_approx(u1)), m2cl2, cl2);
+          if (kBias && linear) x = f2_add(x, bias2(e));
+          f2_split(x, s[e], s[e + 1]);
+        }
       }
-      f2_split(x, s[e], s[e + 1]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kBN; e += 2) {
+        const uint64_t s2 = f2(s[e], s[e + 1]);
+        f2_split(linear ? f2_fma(s2, c2, bias2(e)) : f2_mul(s2, c2), s[e], s[e + 1]);
+      }
     }
     if (kBias && !linear) {
 #pragma unroll

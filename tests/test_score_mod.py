@@ -252,3 +252,20 @@ def test_oracle_masks_by_hand():
     o, lse = oracle.rows(q, np.array([[3.0], [9.0]]), np.array([[5.0], [np.nan]]), np.array([[True, False]]), [1],
                          np.array([0, 1]), 0.5, softcap=2.0, slope=0.25)
     assert o[0, 0] == 5.0 and abs(lse[0] - (2.0 * math.tanh(1.5) - 0.25)) < 1e-15
+
+
+def test_tanh_polynomial_matches_its_fit_and_bound():
+    import os
+    import re
+    import sys
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "context_blocks_b200", "csrc")
+    sys.path.insert(0, csrc)
+    import gen_tanh_poly as gen
+    text = re.search(r"kTanhC\[6\] = \{([^}]*)\}", open(os.path.join(csrc, "score_mod.cuh")).read()).group(1)
+    k = np.array([float(x.strip().rstrip("f")) for x in text.split(",")], dtype=np.float32)
+    c, err = gen.fit(5)
+    assert err < 6e-7 and np.allclose(k, c.astype(np.float32), rtol=1e-6, atol=0)
+    u = np.linspace(-1.0, 1.0, 200001)
+    u = u[u != 0]
+    rel = np.abs(gen.simulate(k, u).astype(np.float64) - np.tanh(u)) / np.abs(np.tanh(u))
+    assert rel.max() < 8e-7  # the fit, and the roundings of w, p and the product: a few 2^-24
