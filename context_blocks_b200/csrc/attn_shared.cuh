@@ -153,27 +153,30 @@ template <int D, bool kCap, bool kBias, int kKeys>
 __device__ __forceinline__ void softmax_share(uint32_t tS, uint32_t tO, int kq, int b, float dist0, float slope2,
                                               const ScoreMod& sm, bool have_o, float& m_ref, float& l,
                                               uint32_t bar_part, uint32_t bar_full, int lane) {
-  uint32_t sr[kKeys];
-  if constexpr (kKeys == 32)
-    tmem_ld_x32(tS + kq * kKeys, sr);
-  else
-    tmem_ld_x64(tS + kq * kKeys, sr);
+  constexpr bool kMod = kCap || kBias;
   const int e0 = kq * kKeys;
-  const float d0 = dist0 - static_cast<float>(e0);
-  float x[kKeys];
+  uint64_t x[kKeys / 2];
+  {
+    uint32_t sr[kKeys];
+    if constexpr (kKeys == 32)
+      tmem_ld_x32(tS + e0, sr);
+    else
+      tmem_ld_x64(tS + e0, sr);
 #pragma unroll
-  for (int e = 0; e < kKeys; ++e) {
-    x[e] = mod_one(__uint_as_float(sr[e]), sm, kCap, kBias, slope2, d0 - static_cast<float>(e));
-    if (e >= b - e0) x[e] = -INFINITY;
+    for (int e = 0; e < kKeys / 2; ++e) x[e] = f2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
   }
-  float m4[4];
+  if constexpr (kCap) cap_scores<kKeys / 2>(x, sm, 0.f);
+  if constexpr (kBias) bias_scores<kKeys / 2, !kCap>(x, sm.scale_log2, slope2, dist0 - static_cast<float>(e0));
+  if (__any_sync(0xffffffffu, b < e0 + kKeys)) hide<kKeys / 2>(x, 0, b - e0);
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int k = 0; k < 4; ++k) m4[k] = fmaxf(x[k], x[k + 4]);
-#pragma unroll
-  for (int e = 8; e < kKeys; e += 8)
-#pragma unroll
-    for (int k = 0; k < 4; ++k) m4[k] = max3f(m4[k], x[e + k], x[e + 4 + k]);
-  const float mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
+  for (int e = 0; e < kKeys / 2; ++e) {
+    float x0, x1;
+    f2_split(x[e], x0, x1);
+    m4[e & 3] = max3f(m4[e & 3], x0, x1);
+  }
+  float mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
+  if constexpr (!kMod) mx *= sm.scale_log2;
   float alpha = 1.f;
   bool rescale = false;
   if (mx > m_ref + kRescaleLog2) {
@@ -203,7 +206,10 @@ __device__ __forceinline__ void softmax_share(uint32_t tS, uint32_t tO, int kq, 
     uint32_t pk[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const float p0 = ex2_approx(x[ch * 32 + 2 * e] + neg_m), p1 = ex2_approx(x[ch * 32 + 2 * e + 1] + neg_m);
+      const uint64_t nm2 = f2(neg_m, neg_m);
+      float x0, x1;
+      f2_split(kMod ? f2_add(x[ch * 16 + e], nm2) : f2_fma(x[ch * 16 + e], f2(sm.scale_log2, sm.scale_log2), nm2), x0, x1);
+      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
       l2[0] += p0;
       l2[1] += p1;
       pk[e] = pack_bf16x2(p0, p1);

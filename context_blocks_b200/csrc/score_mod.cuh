@@ -64,8 +64,19 @@ struct ScoreMod {
   float cap_log2;       // c * log2(e)
   float cap_u;          // scale / c
   float cap_g[6];       // cap_log2 * (coefficients of g)
+  float cap_ref;        // cap_log2 - kCapTop: the fixed reference maximum of capped scores
+  bool cap_fixed;       // whether the weights fit that reference (see kCapTop)
   const float* slopes;  // [Hq], natural units; read where the kernel is built for a bias
 };
+
+// Capped scores without a bias lie in [-c, c], so the softmax needs no running
+// maximum: the weights 2^(x - m) with the fixed m = c log2 e - kCapTop lie in
+// [2^(kCapTop - 2 c log2 e), 2^kCapTop], far from both ends of bf16's and
+// fp32's exponents as long as c log2 e <= kCapMax (c <= 52): a sum of 2^20
+// weights times values up to 2^66 stays finite, and values down to 2^-22 keep
+// their bits where every score of a row is -c.
+constexpr float kCapTop = 40.f;
+constexpr float kCapMax = 75.f;
 
 // A row's constants in one tile: dist0 = p_i - (first key of the tile).
 __device__ __forceinline__ float mod_one(float s, const ScoreMod& m, bool cap, bool bias, float slope2, float dist) {
@@ -78,6 +89,131 @@ __device__ __forceinline__ float mod_one(float s, const ScoreMod& m, bool cap, b
   return x;
 }
 
+// kPairs pairs of raw scores to capped scores (log2 units) plus `add`, by the
+// polynomial where the whole warp's scores allow it.  The steps go over the
+// pairs in turn, so that each has the others' latency to wait in.
+template <int kPairs>
+__device__ __forceinline__ void cap_scores(uint64_t (&x)[kPairs], const ScoreMod& sm, float add) {
+  float a4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < kPairs; ++e) {
+    float x0, x1;
+    f2_split(x[e], x0, x1);
+    a4[e & 3] = max3_abs(a4[e & 3], x0, x1);
+  }
+  const float amax = max3_abs(max3_abs(a4[0], a4[1], a4[2]), a4[3], 0.f) * sm.cap_u;
+  constexpr int kGroup = kPairs < 8 ? kPairs : 8;
+  if (__all_sync(0xffffffffu, amax <= 1.f)) {
+    const uint64_t k2 = f2(sm.cap_u, sm.cap_u), add2 = f2(add, add);
+    uint64_t g[6];
+#pragma unroll
+    for (int u = 0; u < 6; ++u) g[u] = f2(sm.cap_g[u], sm.cap_g[u]);
+#pragma unroll
+    for (int e0 = 0; e0 < kPairs; e0 += kGroup) {
+      uint64_t w[kGroup], y[kGroup];
+#pragma unroll
+      for (int e = 0; e < kGroup; ++e) x[e0 + e] = f2_mul(x[e0 + e], k2);
+#pragma unroll
+      for (int e = 0; e < kGroup; ++e) w[e] = f2_mul(x[e0 + e], x[e0 + e]);
+#pragma unroll
+      for (int e = 0; e < kGroup; ++e) y[e] = f2_fma(g[5], w[e], g[4]);
+#pragma unroll
+      for (int u = 3; u >= 0; --u)
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e) y[e] = f2_fma(y[e], w[e], g[u]);
+#pragma unroll
+      for (int e = 0; e < kGroup; ++e) x[e0 + e] = f2_fma(y[e], x[e0 + e], add2);
+    }
+  } else {
+    const uint64_t m2 = f2(-2.f * sm.cap_log2, -2.f * sm.cap_log2), t2 = f2(sm.cap_log2 + add, sm.cap_log2 + add);
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) {
+      float u0, u1;
+      f2_split(f2_mul(x[e], f2(sm.cap_k, sm.cap_k)), u0, u1);
+      f2_split(f2_add(f2(ex2_approx(u0), ex2_approx(u1)), f2(1.f, 1.f)), u0, u1);
+      x[e] = f2_fma(f2(rcp_approx(u0), rcp_approx(u1)), m2, t2);
+    }
+  }
+}
+
+// -inf where key 2 e or 2 e + 1 of the pairs is not in [a, b).
+template <int kPairs>
+__device__ __forceinline__ void hide(uint64_t (&x)[kPairs], int a, int b) {
+#pragma unroll
+  for (int e = 0; e < kPairs; ++e) {
+    float x0, x1;
+    f2_split(x[e], x0, x1);
+    x[e] = f2((2 * e < a || 2 * e >= b) ? -INFINITY : x0, (2 * e + 1 < a || 2 * e + 1 >= b) ? -INFINITY : x1);
+  }
+}
+
+// x <- x * mul - slope2 * |dist0 - key| for kPairs pairs of keys 0, 1, ..  The
+// distance is linear in the key on either side of the row's own position: away
+// from it the bias is a base for every eight keys plus one of four pairs of
+// multiples of the slope, two packed operations a pair.
+template <int kPairs, bool kMul>
+__device__ __forceinline__ void bias_scores(uint64_t (&x)[kPairs], float mul, float slope2, float dist0) {
+  if (__all_sync(0xffffffffu, dist0 <= 0.f || dist0 >= static_cast<float>(2 * kPairs - 1))) {
+    const float sl = dist0 <= 0.f ? -slope2 : slope2;
+    uint64_t step[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) step[u] = f2(sl * static_cast<float>(2 * u), sl * static_cast<float>(2 * u + 1));
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) {
+      const float at = sl * (static_cast<float>(2 * (e & ~3)) - dist0);
+      x[e] = f2_add(kMul ? f2_fma(x[e], f2(mul, mul), f2(at, at)) : f2_add(x[e], f2(at, at)), step[e & 3]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) {
+      float x0, x1;
+      f2_split(kMul ? f2_mul(x[e], f2(mul, mul)) : x[e], x0, x1);
+      x[e] = f2(fmaf(-slope2, fabsf(dist0 - static_cast<float>(2 * e)), x0),
+                fmaf(-slope2, fabsf(dist0 - static_cast<float>(2 * e + 1)), x1));
+    }
+  }
+}
+
+// softmax_tile (below) for capped scores with the fixed reference maximum: no
+// maximum, no rescaling of O, and the cap's last multiplication subtracts the
+// reference as well.
+__device__ __forceinline__ void softmax_tile_capped(uint32_t tS, int a, int b, const ScoreMod& sm, float& m_ref, float& l,
+                                                    uint32_t bar_part, uint32_t bar_full, int lane) {
+  const bool edge = __any_sync(0xffffffffu, a > 0 || b < kBN);
+  if (max(a, 0) < min(b, kBN)) m_ref = sm.cap_ref;  // stays -inf until the row sees a key
+  uint64_t l4[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+  for (int ch = 0; ch < kBN / 32; ++ch) {
+    uint32_t s[32];
+    tmem_ld_x32(tS + ch * 32, s);
+    uint64_t x[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = f2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
+    cap_scores<16>(x, sm, -sm.cap_ref);
+    if (edge) hide<16>(x, a - ch * 32, b - ch * 32);
+    uint32_t pk[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float x0, x1;
+      f2_split(x[e], x0, x1);
+      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+      l4[e & 3] = f2_add(l4[e & 3], f2(p0, p1));
+      pk[e] = pack_bf16x2(p0, p1);
+    }
+    tmem_st_x16(tS + ch * 16, pk);
+    constexpr int kChPerPart = (kBN / 32) / kPParts;
+    if ((ch + 1) % kChPerPart == 0) {
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ch + 1 < kBN / 32 ? bar_part : bar_full);
+    }
+  }
+  float s0, s1;
+  f2_split(f2_add(f2_add(l4[0], l4[1]), f2_add(l4[2], l4[3])), s0, s1);
+  l += s0 + s1;
+}
+
 // One 128-key tile of one row a thread: S from tensor memory at tS, P (bf16
 // pairs) written back over it and handed over in two halves.  The row sees
 // keys [a, b) of the tile.  m_ref, l: the row's running reference maximum and
@@ -87,75 +223,28 @@ template <int D, bool kCap, bool kBias>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int a, int b, float dist0, float slope2,
                                              const ScoreMod& sm, bool have_o, float& m_ref, float& l,
                                              uint32_t bar_part, uint32_t bar_full, int lane) {
-  constexpr bool kMod = kCap || kBias;
-  uint32_t sr[kBN];
-  tmem_ld_x128(tS, sr);
-  float s[kBN];
-#pragma unroll
-  for (int e = 0; e < kBN; ++e) s[e] = __uint_as_float(sr[e]);
-  const float c = sm.scale_log2;
-  if constexpr (kMod) {
-    // The distance is linear in the key on either side of the row's own
-    // position, so a tile that does not hold it needs one packed FMA a pair.
-    float sl = slope2;
-    bool linear = true;
-    if constexpr (kBias) {
-      if (dist0 <= 0.f) sl = -slope2;
-      linear = __all_sync(0xffffffffu, dist0 <= 0.f || dist0 >= static_cast<float>(kBN - 1));
-    }
-    const uint64_t c2 = f2(c, c);
-    const uint64_t sl2 = f2(sl, sl), b02 = f2(-sl * dist0, -sl * dist0);
-    auto bias2 = [&](int e) { return f2_fma(sl2, f2(static_cast<float>(e), static_cast<float>(e + 1)), b02); };
-    if constexpr (kCap) {
-      float a4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int e = 0; e < kBN; e += 8)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) a4[k] = max3_abs(a4[k], s[e + k], s[e + 4 + k]);
-      const float amax = max3_abs(max3_abs(a4[0], a4[1], a4[2]), a4[3], 0.f) * sm.cap_u;
-      if (__all_sync(0xffffffffu, amax <= 1.f)) {
-        const uint64_t k2 = f2(sm.cap_u, sm.cap_u);
-        uint64_t g[6];
-#pragma unroll
-        for (int u = 0; u < 6; ++u) g[u] = f2(sm.cap_g[u], sm.cap_g[u]);
-#pragma unroll
-        for (int e = 0; e < kBN; e += 2) {
-          const uint64_t v = f2_mul(f2(s[e], s[e + 1]), k2), w = f2_mul(v, v);
-          uint64_t x = f2_fma(g[5], w, g[4]);
-#pragma unroll
-          for (int u = 3; u >= 0; --u) x = f2_fma(x, w, g[u]);
-          if (kBias && linear)
-            x = f2_fma(x, v, bias2(e));
-          else
-            x = f2_mul(x, v);
-          f2_split(x, s[e], s[e + 1]);
-        }
-      } else {
-        const uint64_t ck2 = f2(sm.cap_k, sm.cap_k), one2 = f2(1.f, 1.f);
-        const uint64_t cl2 = f2(sm.cap_log2, sm.cap_log2), m2cl2 = f2(-2.f * sm.cap_log2, -2.f * sm.cap_log2);
-#pragma unroll
-        for (int e = 0; e < kBN; e += 2) {
-          float u0, u1;
-          f2_split(f2_mul(f2(s[e], s[e + 1]), ck2), u0, u1);
-          f2_split(f2_add(f2(ex2_approx(u0), ex2_approx(u1)), one2), u0, u1);
-          uint64_t x = f2_fma(f2(rcp_approx(u0), rcp_approx(u1)), m2cl2, cl2);
-          if (kBias && linear) x = f2_add(x, bias2(e));
-          f2_split(x, s[e], s[e + 1]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < kBN; e += 2) {
-        const uint64_t s2 = f2(s[e], s[e + 1]);
-        f2_split(linear ? f2_fma(s2, c2, bias2(e)) : f2_mul(s2, c2), s[e], s[e + 1]);
-      }
-    }
-    if (kBias && !linear) {
-#pragma unroll
-      for (int e = 0; e < kBN; ++e) s[e] = fmaf(-slope2, fabsf(dist0 - static_cast<float>(e)), s[e]);
-    }
+  if constexpr (kCap && !kBias) {
+    if (sm.cap_fixed) return softmax_tile_capped(tS, a, b, sm, m_ref, l, bar_part, bar_full, lane);
   }
+  constexpr bool kMod = kCap || kBias;
+  float s[kBN];
+  {
+    uint32_t sr[kBN];
+    tmem_ld_x128(tS, sr);
+#pragma unroll
+    for (int e = 0; e < kBN; ++e) s[e] = __uint_as_float(sr[e]);
+  }
+  const float c = sm.scale_log2;
   const bool edge = __any_sync(0xffffffffu, a > 0 || b < kBN);
+  if constexpr (kMod) {
+    uint64_t x[kBN / 2];
+#pragma unroll
+    for (int e = 0; e < kBN / 2; ++e) x[e] = f2(s[2 * e], s[2 * e + 1]);
+    if constexpr (kCap) cap_scores<kBN / 2>(x, sm, 0.f);
+    if constexpr (kBias) bias_scores<kBN / 2, !kCap>(x, c, slope2, dist0);
+#pragma unroll
+    for (int e = 0; e < kBN / 2; ++e) f2_split(x[e], s[2 * e], s[2 * e + 1]);
+  }
   if (edge) {
 #pragma unroll
     for (int e = 0; e < kBN; ++e)
@@ -223,7 +312,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int a, in
       }
     }
   };
-  if (edge)
+  if (edge || kCap)  // capped scores have the FMA pipe busy already
     pass([] { return false; });
   else
     pass([] { return true; });

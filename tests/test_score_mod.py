@@ -82,6 +82,31 @@ def test_small(d, Nq, Nk, kw):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cap", [0.5, 5.0, 30.0, 50.0, 52.5, 80.0, 1e4])
+@pytest.mark.parametrize("qstd", [0.1, 3.0, 20.0])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_caps(cap, qstd, slopes):
+    """Scores well inside the cap, around it and far outside; caps that take the
+    fixed reference maximum and caps that do not; rows that see nothing."""
+    _case(1, 2, 1, 260, 391, 64, seed=int(cap * 10), qstd=qstd, causal=True, softcap=cap, slopes=slopes,
+          doc_offsets=[[0, 140, 200, 380]])
+
+
+@pytest.mark.gpu
+def test_capped_scores_at_the_far_end():
+    """Every score of a row at -c: the weights are small beside the fixed
+    reference, and the result is as if they were not."""
+    q = torch.ones((1, 1, 130, 64), dtype=torch.bfloat16, device="cuda")
+    k = -100.0 * torch.ones((1, 1, 200, 64), dtype=torch.bfloat16, device="cuda")
+    for scale_v in (1.0, 1e-4, 1e6):
+        v = (scale_v * _rand((1, 1, 200, 64), 5)).bfloat16()
+        o, lse = pa.attn_fwd_mod(q, k, v, softcap=50.0, check=True)
+        want = v.double().mean(2)
+        assert (o[0, 0].double() - want[0]).abs().max() <= 2.0 ** -7 * v.double().abs().max()
+        assert (lse - (math.log(200) - 50.0)).abs().max() <= LSE_ABS
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("prefix", [0, 1, 127, 128, 129, 200, 300, 1000])
 def test_prefix(prefix):
     _case(2, 2, 1, 300, 300, 64, seed=prefix, causal=True, prefix_lens=[prefix, max(0, prefix - 3)])
