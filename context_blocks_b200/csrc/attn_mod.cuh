@@ -22,6 +22,14 @@
 // instead of moving it with every tile.
 // Tensor memory and shared memory are laid out as in attn_fwd.cuh.
 //
+// With kWide (capped scores with the fixed reference, score_mod.cuh) two
+// warpgroups share a query tile, the lower and the upper 64 keys of every tile, a
+// row a thread in both: warps 0-7 and 8-15, the others at 16-19.  Four warps a
+// scheduler instead of two keep its pipes busier: 37 heads x 4096 x 4096 capped
+// 350 us, 471 us with one warpgroup a query tile.  Without the fixed reference
+// both threads of a row would have to agree on a maximum for every tile, which
+// costs more than it gains (4096 keys, 24 heads: 207 us against 181).
+//
 // Bound: the special-function unit and the tensor pipe, as the plain forward;
 // a cap adds an ex2 and a reciprocal a score.
 #pragma once
@@ -35,14 +43,20 @@ namespace pa {
 namespace mod {
 
 constexpr int kStages = 4;
-constexpr int kMmaWarp = 8;
-constexpr int kTmaWarp = 9;
-constexpr int kSchedWarp = 10;
-constexpr int kThreads = 384;
-constexpr int kLaunchRegs = 168;
-constexpr int kSoftmaxRegs = 208;
-constexpr int kControlRegs = 88;
-static_assert(kControlRegs + 2 * kSoftmaxRegs == 3 * kLaunchRegs, "register split must sum to the launch allocation");
+// Warps and registers.  The split (see attn_fwd.cuh): three warpgroups of 168 at
+// launch, two of 208 and one of 88 then; wide, five of 96, then four of 104 and
+// one of 64.
+template <bool kWide>
+struct Roles {
+  static constexpr int kGroups = kWide ? 4 : 2;  // softmax warpgroups
+  static constexpr int kMma = 4 * kGroups, kTma = kMma + 1, kSched = kMma + 2;
+  static constexpr int kThreads = 128 * (kGroups + 1);
+  static constexpr int kLaunchRegs = kWide ? 96 : 168;
+  static constexpr int kSoftmaxRegs = kWide ? 104 : 208;
+  static constexpr int kControlRegs = kWide ? 64 : 88;
+  static_assert(kControlRegs + kGroups * kSoftmaxRegs == (kGroups + 1) * kLaunchRegs,
+                "register split must sum to the launch allocation");
+};
 
 struct FwdModParams {
   __nv_bfloat16* o;
@@ -103,7 +117,7 @@ struct ItemSlot {
   int doc0, doc1;         // documents of the item's first and last row
 };
 
-template <int D>
+template <int D, bool kWide>
 struct Layout {
   static constexpr int kBoxBytes = 128 * 128;
   static constexpr int kBoxes = D / 64;
@@ -111,11 +125,14 @@ struct Layout {
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = kQOff + kQTiles * kTileBytes;
   static constexpr int kStageOff = kRingOff + kStages * kTileBytes;
-  static constexpr int kStageWarpBytes = 32 * 128;
-  static constexpr int kBarOff = kStageOff + 8 * kStageWarpBytes;
+  static constexpr int kStageWarpBytes = kWide ? 32 * 32 : 32 * 128;
+  // Wide: what the two threads of a row tell each other at the end, the sums of
+  // their weights; [two slots in turn][query tile][key half][row].
+  static constexpr int kSumOff = kStageOff + Roles<kWide>::kGroups * 4 * kStageWarpBytes;
+  static constexpr int kBarOff = kSumOff + (kWide ? 2 * 2 * 2 * 128 * 4 : 0);
   // q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], p_part[2], p_full[2],
-  // o_full[2], drain, item_full[2], item_empty[2]
-  static constexpr int kNumBars = 2 + 2 * kStages + 8 + 1 + 4;
+  // o_full[2], drain, item_full[2], item_empty[2], swap[2][4 warps]
+  static constexpr int kNumBars = 2 + 2 * kStages + 8 + 1 + 4 + 8;
   static constexpr int kItemOff = kBarOff + kNumBars * 8;
   static constexpr int kTmemSlotOff = kItemOff + 2 * static_cast<int>(sizeof(ItemSlot));
   static constexpr int kAbortOff = kTmemSlotOff + 4;
@@ -125,11 +142,14 @@ struct Layout {
   static constexpr int kAllocBytes = (kBytes + 1024 > kMinOneCtaPerSm) ? (kBytes + 1024) : kMinOneCtaPerSm;
 };
 
-template <int D, bool kCap, bool kBias>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int D, bool kCap, bool kBias, bool kWide>
+__global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
     attn_mod_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ FwdModParams p) {
-  using L = Layout<D>;
+  static_assert(!kWide || (kCap && !kBias), "the fixed reference is for capped scores without a bias");
+  using L = Layout<D, kWide>;
+  using R = Roles<kWide>;
+  constexpr int kPOff = kWide ? 64 : 32;  // columns from a tile's first weights to those of its upper 64 keys
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -148,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_drain = bars + 8 * (10 + 2 * kStages);
   const uint32_t bar_item_full0 = bars + 8 * (11 + 2 * kStages);
   const uint32_t bar_item_empty0 = bars + 8 * (13 + 2 * kStages);
+  const uint32_t bar_swap0 = bars + 8 * (15 + 2 * kStages);  // + 8 * (4 * query tile + warp of the warpgroup)
   volatile ItemSlot* slots = reinterpret_cast<volatile ItemSlot*>(gbase + L::kItemOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kTmemSlotOff);
   volatile int* abort_word = reinterpret_cast<volatile int*>(gbase + L::kAbortOff);
@@ -169,18 +190,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_p_full0 + 8 * i, 4);
       mbar_init(bar_o_full0 + 8 * i, 1);
       mbar_init(bar_item_full0 + 8 * i, 1);
-      mbar_init(bar_item_empty0 + 8 * i, 10);  // 8 softmax warps, MMA, TMA
+      mbar_init(bar_item_empty0 + 8 * i, 4 * R::kGroups + 2);  // softmax warps, MMA, TMA
     }
     mbar_init(bar_drain, 1);
+    for (int u = 0; u < 8; ++u) mbar_init(bar_swap0 + 8 * u, 2);  // the two warps of the same rows
     *abort_word = 0;
     fence_barrier_init();
   }
-  if (warp == kTmaWarp && lane == 0) {
+  if (warp == R::kTma && lane == 0) {
     prefetch_tensormap(&tm_q);
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
-  if (warp == kMmaWarp) {
+  if (warp == R::kMma) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
@@ -218,10 +240,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     b = has0 && has1 ? max(x.last[0], x.last[1]) : has0 ? x.last[0] : x.last[1];
   };
 
-  if (warp > kSchedWarp) {
-    setmaxnreg_dec<kControlRegs>();
-  } else if (warp == kSchedWarp) {
-    setmaxnreg_dec<kControlRegs>();
+  if (warp > R::kSched) {
+    setmaxnreg_dec<R::kControlRegs>();
+  } else if (warp == R::kSched) {
+    setmaxnreg_dec<R::kControlRegs>();
     // ----------------------------------------------------------- scheduler
     int it = 0;
     for (int item = blockIdx.x;; item += gridDim.x, ++it) {
@@ -278,8 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar_item_full0 + 8 * s);
     }
-  } else if (warp == kTmaWarp) {
-    setmaxnreg_dec<kControlRegs>();
+  } else if (warp == R::kTma) {
+    setmaxnreg_dec<R::kControlRegs>();
     // ------------------------------------------------------------ producer
     const bool leader = elect_one();
     bool ok = true;
@@ -336,8 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == kMmaWarp) {
-    setmaxnreg_dec<kControlRegs>();
+  } else if (warp == R::kMma) {
+    setmaxnreg_dec<R::kControlRegs>();
     // ----------------------------------------------------------- MMA issue
     const bool leader = elect_one();
     constexpr uint32_t kIdS = idesc_bf16(128, kBN, false, false);
@@ -361,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int u = 0; u < kPer; ++u) {
         const int kk = part * kPer + u;
-        umma_ts(tO0 + i * D, tmem + i * kBN + kk * 8, dv + static_cast<uint64_t>(kk * 128), kIdPV,
+        umma_ts(tO0 + i * D, tmem + i * kBN + part * kPOff + u * 8, dv + static_cast<uint64_t>(kk * 128), kIdPV,
                 (acc || kk > 0) ? 1u : 0u);
       }
     };
@@ -458,20 +480,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait(bar_drain, 0, nullptr, p.status, kStatusTimeout, lim);
     __syncwarp();
   } else {
-    setmaxnreg_inc<kSoftmaxRegs>();
+    setmaxnreg_inc<R::kSoftmaxRegs>();
     // ------------------------------------------------------------- softmax
-    const int i = warp / 4;
+    const int i = kWide ? warp / 8 : warp / 4;      // query tile
+    const int half = kWide ? (warp / 4) % 2 : 0;      // wide: which keys, and which O columns to store
+    const int r = threadIdx.x % 128;                  // row of the tile = tensor-memory lane
+    constexpr int kCols = kWide ? D / 2 : D;
     const uint32_t lane_off = static_cast<uint32_t>((warp % 4) * 32) << 16;
-    const uint32_t tS = tmem + i * kBN + lane_off;
-    const uint32_t tO = tmem + 2 * kBN + i * D + lane_off;
+    const uint32_t tS = tmem + i * kBN + half * 64 + lane_off;
+    const uint32_t tO = tmem + 2 * kBN + i * D + half * kCols + lane_off;
     bool ok = true;
     int g = 0;    // key tiles over all items: phases of the S barrier
     int n_o = 0;  // items with key tiles: phase of the O barrier
+    auto wait_warp = [&](uint32_t bar, uint32_t parity) {
+      const bool got = mbar_wait_hint(bar, parity, abort_word, p.status, kStatusTimeout, lim, kSuspendHintNs);
+      return !__any_sync(0xffffffffu, !got);
+    };
     ItemSlot x;
     for (int it = 0; ok && next_item(it, x, ok); ++it) {
       const int bh = x.item % (p.B * p.Hq);
       const int bt = bh / p.Hq, hq = bh % p.Hq;
-      const int row = (p.blocks_per_bh - 1 - x.item / (p.B * p.Hq)) * (kQTiles * kBM) + threadIdx.x;
+      const int row = (p.blocks_per_bh - 1 - x.item / (p.B * p.Hq)) * (kQTiles * kBM) + i * kBM + r;
       const int pos = row + p.q_offset;
       float slope2 = 0.f;
       if constexpr (kBias) slope2 = __ldg(p.sm.slopes + hq) * 1.4426950408889634f;
@@ -484,24 +513,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           t = find_doc(p.docs + static_cast<long long>(bt) * (p.n_docs + 1), pos, x.doc0, x.doc1);
         seen = row_interval(p, bt, pos, t);
       }
-      float m_ref = -INFINITY, l = 0.f;
+      float m_ref = kWide ? p.sm.cap_ref : -INFINITY, l = 0.f;
       const int first = first_of(x, i), last = last_of(x, i);
       for (int j = last - 1; j >= first; --j, ++g) {
-        const bool got =
-            mbar_wait_hint(bar_s_full0 + 8 * i, g & 1, abort_word, p.status, kStatusTimeout, lim, kSuspendHintNs);
-        if (__any_sync(0xffffffffu, !got)) {
+        if (!wait_warp(bar_s_full0 + 8 * i, g & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int k0 = j * kBN;
-        softmax_tile<D, kCap, kBias>(tS, tO, seen.x - k0, seen.y - k0, static_cast<float>(pos - k0), slope2, p.sm,
-                                     j < last - 1, m_ref, l, bar_p_part0 + 8 * i, bar_p_full0 + 8 * i, lane);
+        const int k0 = j * kBN + half * 64;
+        if constexpr (kWide)
+          capped_keys(tS, tS, seen.x - k0, seen.y - k0, p.sm, l, (half ? bar_p_full0 : bar_p_part0) + 8 * i, lane);
+        else
+          softmax_tile<D, kCap, kBias>(tS, tO, seen.x - k0, seen.y - k0, static_cast<float>(pos - k0), slope2, p.sm,
+                                       j < last - 1, m_ref, l, bar_p_part0 + 8 * i, bar_p_full0 + 8 * i, lane);
       }
       if (!ok) break;
       if (first < last) {
-        const bool got = mbar_wait(bar_o_full0 + 8 * i, n_o & 1, abort_word, p.status, kStatusTimeout, lim);
-        if (__any_sync(0xffffffffu, !got)) {
+        if constexpr (kWide) {
+          // The row's sum is both threads'.  A slot is written again two items
+          // on, after a swap that the other thread enters having read it.
+          const uint32_t at = base + L::kSumOff + (n_o & 1) * 2048 + i * 1024 + r * 4;
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + half * 512), "f"(l) : "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_swap0 + 8 * (4 * i + warp % 4));
+          if (!wait_warp(bar_swap0 + 8 * (4 * i + warp % 4), n_o & 1)) {
+            ok = false;
+            break;
+          }
+          float other;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(other) : "r"(at + (1 - half) * 512) : "memory");
+          l += other;
+        }
+        if (!wait_warp(bar_o_full0 + 8 * i, n_o & 1)) {
           ok = false;
           break;
         }
@@ -510,33 +554,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int wrow = row - lane;  // first row of this warp
       if (wrow >= p.Nq) continue;
-      const bool empty = m_ref == -INFINITY;
+      const bool empty = l == 0.f;
       const float inv = empty ? 0.f : 1.f / l;
-      __nv_bfloat16* o = p.o + bt * p.o_s[0] + hq * p.o_s[1] + wrow * p.o_s[2];
-      const bool bad = store_rows<D>(tO, base + L::kStageOff + warp * L::kStageWarpBytes, o, nullptr, p.o_s[2],
-                                     p.Nq - wrow, inv);
-      if (row < p.Nq)
+      __nv_bfloat16* o = p.o + bt * p.o_s[0] + hq * p.o_s[1] + wrow * p.o_s[2] + half * kCols;
+      const uint32_t stage = base + L::kStageOff + warp * L::kStageWarpBytes;
+      bool bad;
+      if constexpr (kWide)
+        bad = store_cols_bf16<kCols>(tO, stage, o, p.o_s[2], p.Nq - wrow, inv);
+      else
+        bad = store_rows<D>(tO, stage, o, nullptr, p.o_s[2], p.Nq - wrow, inv);
+      if (half == 0 && row < p.Nq)
         p.lse[static_cast<size_t>(bh) * p.Nq + row] =
             empty ? -INFINITY : (m_ref + lg2_approx(l)) * 0.69314718055994531f;
       // A value row that is not finite: leave hidden keys out by recomputing.
       unsigned redo = __ballot_sync(0xffffffffu, bad && !empty && row < p.Nq && l <= FLT_MAX);
       while (redo != 0u) {
-        const int r = __ffs(redo) - 1;
+        const int k = __ffs(redo) - 1;
         redo &= redo - 1;
         __syncwarp();
-        const int j0 = __shfl_sync(0xffffffffu, seen.x, r), j1 = __shfl_sync(0xffffffffu, seen.y, r);
-        const float mr = __shfl_sync(0xffffffffu, m_ref, r), iv = __shfl_sync(0xffffffffu, inv, r);
+        const int j0 = __shfl_sync(0xffffffffu, seen.x, k), j1 = __shfl_sync(0xffffffffu, seen.y, k);
+        const float mr = __shfl_sync(0xffffffffu, m_ref, k), iv = __shfl_sync(0xffffffffu, inv, k);
         const int hk = hq / p.G;
-        repair_row<D>(p.q + bt * p.q_s[0] + hq * p.q_s[1] + (wrow + r) * p.q_s[2],
-                      p.k + bt * p.k_s[0] + hk * p.k_s[1], p.v + bt * p.v_s[0] + hk * p.v_s[1], p.k_s[2], p.v_s[2], j0,
-                      j1, 1, 1, 0, wrow + r + p.q_offset, mr, iv, slope2, p.sm, kCap, kBias, o + r * p.o_s[2], nullptr);
+        repair_row<D, kCols>(p.q + bt * p.q_s[0] + hq * p.q_s[1] + (wrow + k) * p.q_s[2],
+                             p.k + bt * p.k_s[0] + hk * p.k_s[1], p.v + bt * p.v_s[0] + hk * p.v_s[1] + half * kCols,
+                             p.k_s[2], p.v_s[2], j0, j1, 1, 1, 0, wrow + k + p.q_offset, mr, iv, slope2, p.sm, kCap,
+                             kBias, o + k * p.o_s[2], nullptr);
       }
     }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == R::kMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }

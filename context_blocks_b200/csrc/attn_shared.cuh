@@ -48,6 +48,8 @@ namespace shared {
 
 using namespace mod;
 
+using R = Roles<false>;  // warps and registers of the single-warpgroup kernel
+
 constexpr int kMaxCtas = 160;  // sizes the workspace; the grid is one CTA an SM, at most this many
 constexpr int kMergeWarps = 4;
 constexpr int kLoadWarp = 9;   // + stream
@@ -255,7 +257,7 @@ __device__ __noinline__ bool store_row_f32(uint32_t tO, float* dst, bool write, 
 }
 
 template <int D, bool kCap, bool kBias>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(R::kThreads, 1)
     attn_shared_kernel(const __grid_constant__ CUtensorMap tm_qp, const __grid_constant__ CUtensorMap tm_qt,
                        const __grid_constant__ CUtensorMap tm_kp, const __grid_constant__ CUtensorMap tm_vp,
                        const __grid_constant__ CUtensorMap tm_kt, const __grid_constant__ CUtensorMap tm_vt,
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&tm_kt);
     prefetch_tensormap(&tm_vt);
   }
-  if (warp == kMmaWarp) {
+  if (warp == R::kMma) {
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp == kLoadWarp || warp == kLoadWarp + 1) {
-    setmaxnreg_dec<kControlRegs>();
+    setmaxnreg_dec<R::kControlRegs>();
     // --------------------------------------------------- pieces and loads
     const int i = warp - kLoadWarp;
     const bool leader = elect_one();
@@ -504,10 +506,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp >= kMmaWarp) {
-    setmaxnreg_dec<kControlRegs>();
+  } else if (warp >= R::kMma) {
+    setmaxnreg_dec<R::kControlRegs>();
     // ----------------------------------------------------------- MMA issue
-    const int me = warp == kMmaWarp ? 0 : 1;  // stream
+    const int me = warp == R::kMma ? 0 : 1;  // stream
     const bool leader = elect_one();
     constexpr uint32_t kIdS = idesc_bf16(128, kBN, false, false);
     constexpr uint32_t kIdPV = idesc_bf16(128, D, false, true);
@@ -625,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_wait(bar_drain0 + 8 * me, 0, nullptr, p.status, kStatusTimeout, lim);
     __syncwarp();
   } else {
-    setmaxnreg_inc<kSoftmaxRegs>();
+    setmaxnreg_inc<R::kSoftmaxRegs>();
     // ------------------------------------------------------------- softmax
     const int i = warp / 4;
     const int w4 = warp % 4;
@@ -700,7 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       if (!active) continue;
-      const bool empty = !mine || m_ref == -INFINITY;
+      const bool empty = !mine || l == 0.f;
       const float inv = empty ? 0.f : 1.f / l;
       const size_t row0 = x.kind == kPair ? static_cast<size_t>(2 * x.slot + i) * plan.tile_rows()
                                           : static_cast<size_t>(x.slot * copies + kq) *
@@ -725,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float sl = __shfl_sync(0xffffffffu, slope2, k);
           const size_t q_row =
               (static_cast<size_t>(x.req) * plan.Hq + x.hk * plan.G) * plan.Nq + wr + k;  // rows of a K/V head are adjacent
-          repair_row<D>(p.q + q_row * D, p.kt + x.req * p.kt_s[0] + x.hk * p.kt_s[1],
+          repair_row<D, D>(p.q + q_row * D, p.kt + x.req * p.kt_s[0] + x.hk * p.kt_s[1],
                         p.vt + x.req * p.vt_s[0] + x.hk * p.vt_s[1], p.kt_s[2], p.vt_s[2], x.t0 * kBN,
                         min(sn, x.t1 * kBN), kBN / copies, kBN, kq, ps, mr, iv, sl, p.sm, kCap, kBias, nullptr,
                         o + k * D);
@@ -736,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == R::kMma) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
   }

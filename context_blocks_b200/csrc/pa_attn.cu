@@ -80,6 +80,7 @@ struct DeviceState {
   unsigned char* noalloc_scratch = nullptr;  // device address of pa::g_noalloc_scratch
   bool fwd_attr[5] = {};  // d = 64, d = 128, e4m3 d = 128, accumulate d = 64, accumulate d = 128
   bool mod_attr[8] = {};  // modified scores: 4 * (d = 128) + 2 * capped + biased
+  bool wide_attr[2] = {};    // capped with the fixed reference: d = 64, d = 128
   bool shared_attr[8] = {};  // shared prefix: the same
 };
 
@@ -504,16 +505,19 @@ pa::mod::ScoreMod score_mod(float scale, float softcap, const float* slopes) {
   return m;
 }
 
-template <int D, bool kCap, bool kBias>
+template <int D, bool kCap, bool kBias, bool kWide = false>
 int launch_mod(DeviceState* st, const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                const pa::mod::FwdModParams& prm, cudaStream_t stream) {
-  using L = pa::mod::Layout<D>;
-  auto kern = pa::mod::attn_mod_kernel<D, kCap, kBias>;
-  const int rc = ready_kernel(kern, &st->mod_attr[4 * (D == 128) + 2 * kCap + kBias], L::kAllocBytes,
-                              pa::mod::kLaunchRegs, "modified-score forward");
+  if constexpr (kCap && !kBias && !kWide)
+    if (prm.sm.cap_fixed) return launch_mod<D, true, false, true>(st, tq, tk, tv, prm, stream);
+  using L = pa::mod::Layout<D, kWide>;
+  using R = pa::mod::Roles<kWide>;
+  auto kern = pa::mod::attn_mod_kernel<D, kCap, kBias, kWide>;
+  bool* const ready = kWide ? &st->wide_attr[D == 128] : &st->mod_attr[4 * (D == 128) + 2 * kCap + kBias];
+  const int rc = ready_kernel(kern, ready, L::kAllocBytes, R::kLaunchRegs, "modified-score forward");
   if (rc != PA_OK) return rc;
   const unsigned grid = static_cast<unsigned>(std::min(prm.items, st->sm_count));
-  kern<<<grid, pa::mod::kThreads, L::kAllocBytes, stream>>>(tq, tk, tv, prm);
+  kern<<<grid, R::kThreads, L::kAllocBytes, stream>>>(tq, tk, tv, prm);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "attn_mod launch");
   return PA_OK;
@@ -616,10 +620,10 @@ int launch_shared(DeviceState* st, const CUtensorMap (&maps)[6], const pa::share
   using L = pa::shared::SharedLayout<D>;
   auto kern = pa::shared::attn_shared_kernel<D, kCap, kBias>;
   const int rc = ready_kernel(kern, &st->shared_attr[4 * (D == 128) + 2 * kCap + kBias], L::kAllocBytes,
-                              pa::mod::kLaunchRegs, "shared-prefix");
+                              pa::shared::R::kLaunchRegs, "shared-prefix");
   if (rc != PA_OK) return rc;
   if (prm.plan.Np > 0 || prm.plan.Nt > 0)
-    kern<<<prm.plan.ctas, pa::mod::kThreads, L::kAllocBytes, stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4],
+    kern<<<prm.plan.ctas, pa::shared::R::kThreads, L::kAllocBytes, stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4],
                                                                        maps[5], prm);
   pa::shared::shared_merge_kernel<D><<<prm.plan.B * prm.plan.Hkv, pa::shared::kMergeWarps * 32, 0, stream>>>(
       prm, static_cast<__nv_bfloat16*>(o), lse);

@@ -57,6 +57,17 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   return r;
 }
 
+// Load 16 consecutive 32-bit TMEM columns of this thread's lane; waits for completion.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // Scalars of the score modification, set by the host.
 struct ScoreMod {
   float scale_log2;     // scale * log2(e)
@@ -89,11 +100,9 @@ __device__ __forceinline__ float mod_one(float s, const ScoreMod& m, bool cap, b
   return x;
 }
 
-// kPairs pairs of raw scores to capped scores (log2 units) plus `add`, by the
-// polynomial where the whole warp's scores allow it.  The steps go over the
-// pairs in turn, so that each has the others' latency to wait in.
+// Whether all of the warp's scores lie where the polynomial holds.
 template <int kPairs>
-__device__ __forceinline__ void cap_scores(uint64_t (&x)[kPairs], const ScoreMod& sm, float add) {
+__device__ __forceinline__ bool cap_by_polynomial(const uint64_t (&x)[kPairs], const ScoreMod& sm) {
   float a4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int e = 0; e < kPairs; ++e) {
@@ -102,8 +111,16 @@ __device__ __forceinline__ void cap_scores(uint64_t (&x)[kPairs], const ScoreMod
     a4[e & 3] = max3_abs(a4[e & 3], x0, x1);
   }
   const float amax = max3_abs(max3_abs(a4[0], a4[1], a4[2]), a4[3], 0.f) * sm.cap_u;
+  return __all_sync(0xffffffffu, amax <= 1.f);
+}
+
+// kPairs pairs of raw scores to capped scores (log2 units) plus `add`, by the
+// polynomial where the whole warp's scores allow it.  The steps go over the
+// pairs in turn, so that each has the others' latency to wait in.
+template <int kPairs>
+__device__ __forceinline__ void cap_scores(uint64_t (&x)[kPairs], const ScoreMod& sm, float add) {
   constexpr int kGroup = kPairs < 8 ? kPairs : 8;
-  if (__all_sync(0xffffffffu, amax <= 1.f)) {
+  if (cap_by_polynomial<kPairs>(x, sm)) {
     const uint64_t k2 = f2(sm.cap_u, sm.cap_u), add2 = f2(add, add);
     uint64_t g[6];
 #pragma unroll
@@ -134,6 +151,49 @@ __device__ __forceinline__ void cap_scores(uint64_t (&x)[kPairs], const ScoreMod
       x[e] = f2_fma(f2(rcp_approx(u0), rcp_approx(u1)), m2, t2);
     }
   }
+}
+
+// Raw scores to packed weights against the fixed reference, polynomial only; l
+// grows by their sum.  The exponentials of eight pairs are issued among the
+// polynomial steps of the next eight, so that the special-function and the FMA
+// pipe work at the same time.
+template <int kPairs>
+__device__ __forceinline__ void capped_weights(uint64_t (&x)[kPairs], const ScoreMod& sm, uint32_t (&pk)[kPairs],
+                                               float& l) {
+  constexpr int kGroup = 8;
+  const uint64_t k2 = f2(sm.cap_u, sm.cap_u), add2 = f2(-sm.cap_ref, -sm.cap_ref);
+  uint64_t g[6], l2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+  for (int u = 0; u < 6; ++u) g[u] = f2(sm.cap_g[u], sm.cap_g[u]);
+#pragma unroll
+  for (int e0 = 0; e0 <= kPairs; e0 += kGroup) {
+    uint64_t w[kGroup], y[kGroup];
+#pragma unroll
+    for (int step = 0; step < 8; ++step) {
+      if (e0 < kPairs) {
+#pragma unroll
+        for (int e = 0; e < kGroup; ++e) {
+          uint64_t& v = x[e0 < kPairs ? e0 + e : 0];
+          if (step == 0) v = f2_mul(v, k2);
+          if (step == 1) w[e] = f2_mul(v, v);
+          if (step == 2) y[e] = f2_fma(g[5], w[e], g[4]);
+          if (step >= 3 && step < 7) y[e] = f2_fma(y[e], w[e], g[6 - step]);
+          if (step == 7) v = f2_fma(y[e], v, add2);
+        }
+      }
+      if (e0 > 0) {  // pair `step` of the eight before
+        const int e = e0 - kGroup + step;
+        float x0, x1;
+        f2_split(x[e], x0, x1);
+        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+        l2[e & 1] = f2_add(l2[e & 1], f2(p0, p1));
+        pk[e] = pack_bf16x2(p0, p1);
+      }
+    }
+  }
+  float s0, s1;
+  f2_split(f2_add(l2[0], l2[1]), s0, s1);
+  l += s0 + s1;
 }
 
 // -inf where key 2 e or 2 e + 1 of the pairs is not in [a, b).
@@ -174,44 +234,46 @@ __device__ __forceinline__ void bias_scores(uint64_t (&x)[kPairs], float mul, fl
   }
 }
 
-// softmax_tile (below) for capped scores with the fixed reference maximum: no
-// maximum, no rescaling of O, and the cap's last multiplication subtracts the
-// reference as well.
-__device__ __forceinline__ void softmax_tile_capped(uint32_t tS, int a, int b, const ScoreMod& sm, float& m_ref, float& l,
-                                                    uint32_t bar_part, uint32_t bar_full, int lane) {
-  const bool edge = __any_sync(0xffffffffu, a > 0 || b < kBN);
-  if (max(a, 0) < min(b, kBN)) m_ref = sm.cap_ref;  // stays -inf until the row sees a key
-  uint64_t l4[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+// A softmax step of one row a thread over 64 keys with the fixed reference: scores
+// at tS in tensor memory, weights (bf16 pairs, 32 columns) to tP, which may lie
+// over scores this thread has taken.  The row sees the keys [a, b) of the 64.
+// No maximum, no rescaling of O, nothing to agree on with another thread; l
+// grows by the weights' sum.
+__device__ __forceinline__ void capped_keys(uint32_t tS, uint32_t tP, int a, int b, const ScoreMod& sm, float& l,
+                                            uint32_t bar_p, int lane) {
+  constexpr int kPairs = 32;
+  const bool edge = __any_sync(0xffffffffu, a > 0 || b < 2 * kPairs);
+  uint64_t x[kPairs];
+  {
+    uint32_t sr[2 * kPairs];
+    tmem_ld_x64(tS, sr);
 #pragma unroll
-  for (int ch = 0; ch < kBN / 32; ++ch) {
-    uint32_t s[32];
-    tmem_ld_x32(tS + ch * 32, s);
-    uint64_t x[16];
+    for (int e = 0; e < kPairs; ++e) x[e] = f2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+  }
+  uint32_t pk[kPairs];
+  if (!edge && cap_by_polynomial<kPairs>(x, sm)) {
+    capped_weights<kPairs>(x, sm, pk, l);
+  } else {
+    cap_scores<kPairs>(x, sm, -sm.cap_ref);
+    if (edge) hide<kPairs>(x, a, b);
+    uint64_t l2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-    for (int e = 0; e < 16; ++e) x[e] = f2(__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1]));
-    cap_scores<16>(x, sm, -sm.cap_ref);
-    if (edge) hide<16>(x, a - ch * 32, b - ch * 32);
-    uint32_t pk[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
+    for (int e = 0; e < kPairs; ++e) {
       float x0, x1;
       f2_split(x[e], x0, x1);
       const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-      l4[e & 3] = f2_add(l4[e & 3], f2(p0, p1));
+      l2[e & 1] = f2_add(l2[e & 1], f2(p0, p1));
       pk[e] = pack_bf16x2(p0, p1);
     }
-    tmem_st_x16(tS + ch * 16, pk);
-    constexpr int kChPerPart = (kBN / 32) / kPParts;
-    if ((ch + 1) % kChPerPart == 0) {
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(ch + 1 < kBN / 32 ? bar_part : bar_full);
-    }
+    float s0, s1;
+    f2_split(f2_add(l2[0], l2[1]), s0, s1);
+    l += s0 + s1;
   }
-  float s0, s1;
-  f2_split(f2_add(f2_add(l4[0], l4[1]), f2_add(l4[2], l4[3])), s0, s1);
-  l += s0 + s1;
+  tmem_st_x32(tP, pk);
+  tmem_st_wait();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar_p);
 }
 
 // One 128-key tile of one row a thread: S from tensor memory at tS, P (bf16
@@ -224,7 +286,12 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int a, in
                                              const ScoreMod& sm, bool have_o, float& m_ref, float& l,
                                              uint32_t bar_part, uint32_t bar_full, int lane) {
   if constexpr (kCap && !kBias) {
-    if (sm.cap_fixed) return softmax_tile_capped(tS, a, b, sm, m_ref, l, bar_part, bar_full, lane);
+    if (sm.cap_fixed) {
+      if (max(a, 0) < min(b, kBN)) m_ref = sm.cap_ref;  // stays -inf until the row sees a key
+      capped_keys(tS, tS, a, b, sm, l, bar_part, lane);
+      capped_keys(tS + 64, tS + 32, a - 64, b - 64, sm, l, bar_full, lane);
+      return;
+    }
   }
   constexpr bool kMod = kCap || kBias;
   float s[kBN];
@@ -236,29 +303,37 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int a, in
   }
   const float c = sm.scale_log2;
   const bool edge = __any_sync(0xffffffffu, a > 0 || b < kBN);
+  float mx;
   if constexpr (kMod) {
     uint64_t x[kBN / 2];
 #pragma unroll
     for (int e = 0; e < kBN / 2; ++e) x[e] = f2(s[2 * e], s[2 * e + 1]);
     if constexpr (kCap) cap_scores<kBN / 2>(x, sm, 0.f);
     if constexpr (kBias) bias_scores<kBN / 2, !kCap>(x, c, slope2, dist0);
+    if (edge) hide<kBN / 2>(x, a, b);
+    float m8[8];
 #pragma unroll
-    for (int e = 0; e < kBN / 2; ++e) f2_split(x[e], s[2 * e], s[2 * e + 1]);
+    for (int e = 0; e < kBN / 2; ++e) {
+      f2_split(x[e], s[2 * e], s[2 * e + 1]);
+      m8[e & 7] = e < 8 ? fmaxf(s[2 * e], s[2 * e + 1]) : max3f(m8[e & 7], s[2 * e], s[2 * e + 1]);
+    }
+    mx = fmaxf(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], max3f(m8[5], m8[6], m8[7])));
+  } else {
+    if (edge) {
+#pragma unroll
+      for (int e = 0; e < kBN; ++e)
+        if (e < a || e >= b) s[e] = -INFINITY;
+    }
+    float m8[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) m8[k] = fmaxf(s[k], s[k + 8]);
+#pragma unroll
+    for (int e = 16; e < kBN; e += 16)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m8[k] = max3f(m8[k], s[e + k], s[e + 8 + k]);
+    mx = fmaxf(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], max3f(m8[5], m8[6], m8[7])));
+    mx *= c;
   }
-  if (edge) {
-#pragma unroll
-    for (int e = 0; e < kBN; ++e)
-      if (e < a || e >= b) s[e] = -INFINITY;
-  }
-  float m8[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) m8[k] = fmaxf(s[k], s[k + 8]);
-#pragma unroll
-  for (int e = 16; e < kBN; e += 16)
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m8[k] = max3f(m8[k], s[e + k], s[e + 8 + k]);
-  float mx = fmaxf(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], max3f(m8[5], m8[6], m8[7])));
-  if constexpr (!kMod) mx *= c;
   float alpha = 1.f;
   bool rescale = false;
   if (mx > m_ref + kRescaleLog2) {
@@ -324,6 +399,42 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int a, in
   tc_fence_before();
   __syncwarp();
   if (lane == 0) mbar_arrive(bar_full);
+}
+
+// Scale this thread's kCols O columns (at tO) by `inv` and store them as bf16
+// through the warp's 1 KB staging area, 16 columns (32 bytes of each of the
+// warp's 32 rows) at a time: row r of the warp at dst + r * row_stride elements,
+// rows r >= rows_left not written.  inv = 0 stores zeros whatever the
+// accumulator holds.  Returns whether the row has a value that is not finite.
+template <int kCols>
+__device__ __noinline__ bool store_cols_bf16(uint32_t tO, uint32_t stg, __nv_bfloat16* dst, long long row_stride,
+                                             int rows_left, float inv) {
+  const int lane = threadIdx.x % 32;
+  float bad = 0.f;  // x * 0 is NaN where x is not finite
+#pragma unroll 1
+  for (int c0 = 0; c0 < kCols; c0 += 16) {
+    uint32_t orr[16], pk[8];
+    tmem_ld_x16(tO + c0, orr);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x0 = __uint_as_float(orr[2 * e]), x1 = __uint_as_float(orr[2 * e + 1]);
+      bad = fmaf(x0, 0.f, fmaf(x1, 0.f, bad));
+      pk[e] = inv == 0.f ? 0u : pack_bf16x2(x0 * inv, x1 * inv);
+    }
+    __syncwarp();  // the previous piece has left the staging area
+    // Chunk u of row r at position u ^ (r / 4 % 2): eight rows fill the banks.
+    const int sw = (lane >> 2) & 1;
+    st_shared_v4(stg + lane * 32 + (sw << 4), pk[0], pk[1], pk[2], pk[3]);
+    st_shared_v4(stg + lane * 32 + ((sw ^ 1) << 4), pk[4], pk[5], pk[6], pk[7]);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = 16 * k + (lane >> 1), u = lane & 1;
+      const uint4 v = ld_shared_v4(stg + r * 32 + ((u ^ ((r >> 2) & 1)) << 4));
+      if (r < rows_left) *reinterpret_cast<uint4*>(dst + r * row_stride + c0 + u * 8) = v;
+    }
+  }
+  return !(bad == 0.f);
 }
 
 // Scale a thread's O row (TMEM columns [tO, tO + D)) by `inv` and store it,
@@ -401,38 +512,38 @@ __device__ __noinline__ bool store_rows(uint32_t tO, uint32_t stg, __nv_bfloat16
 // Rare and slow (about 40 instructions a key); q, k, v: the row's query, and
 // key and value row 0 of its head.  pos: the row's position among the keys.
 // Only keys j with (j % period) / share == which count (share = period: all).
-template <int D>
+// kCols of the row's value columns are computed, those from v and o on.
+template <int D, int kCols>
 __device__ __noinline__ void repair_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
                                         long long k_stride, long long v_stride, int j0, int j1, int share, int period,
-                                        int which, int pos, float m, float inv, float slope2, ScoreMod sm, bool cap, bool bias,
-                                        __nv_bfloat16* o_bf16, float* o_f32) {
-  constexpr int kCols = D / 32;
+                                        int which, int pos, float m, float inv, float slope2, ScoreMod sm, bool cap,
+                                        bool bias, __nv_bfloat16* o_bf16, float* o_f32) {
+  constexpr int kQk = D / 32, kV = kCols / 32;
   const int lane = threadIdx.x % 32;
-  float qv[kCols], acc[kCols];
+  float qv[kQk], acc[kV];
 #pragma unroll
-  for (int u = 0; u < kCols; ++u) {
-    qv[u] = __bfloat162float(q[lane * kCols + u]);
-    acc[u] = 0.f;
-  }
+  for (int u = 0; u < kQk; ++u) qv[u] = __bfloat162float(q[lane * kQk + u]);
+#pragma unroll
+  for (int u = 0; u < kV; ++u) acc[u] = 0.f;
   for (int j = j0; j < j1; ++j) {
     if ((j % period) / share != which) continue;
-    const __nv_bfloat16* kr = k + j * k_stride + lane * kCols;
-    const __nv_bfloat16* vr = v + j * v_stride + lane * kCols;
+    const __nv_bfloat16* kr = k + j * k_stride + lane * kQk;
+    const __nv_bfloat16* vr = v + j * v_stride + lane * kV;
     float dot = 0.f;
 #pragma unroll
-    for (int u = 0; u < kCols; ++u) dot = fmaf(qv[u], __bfloat162float(kr[u]), dot);
+    for (int u = 0; u < kQk; ++u) dot = fmaf(qv[u], __bfloat162float(kr[u]), dot);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
     const float p = ex2_approx(mod_one(dot, sm, cap, bias, slope2, static_cast<float>(pos - j)) - m);
 #pragma unroll
-    for (int u = 0; u < kCols; ++u) acc[u] = fmaf(p, __bfloat162float(vr[u]), acc[u]);
+    for (int u = 0; u < kV; ++u) acc[u] = fmaf(p, __bfloat162float(vr[u]), acc[u]);
   }
 #pragma unroll
-  for (int u = 0; u < kCols; ++u) {
+  for (int u = 0; u < kV; ++u) {
     if (o_bf16 != nullptr)
-      o_bf16[lane * kCols + u] = __float2bfloat16(acc[u] * inv);
+      o_bf16[lane * kV + u] = __float2bfloat16(acc[u] * inv);
     else
-      o_f32[lane * kCols + u] = acc[u] * inv;
+      o_f32[lane * kV + u] = acc[u] * inv;
   }
 }
 
