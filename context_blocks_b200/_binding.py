@@ -69,6 +69,8 @@ class BlockNorm(ctypes.Structure):
                 ("shift_stride", ctypes.c_longlong), ("residual_scale", _F), ("eps", _F)]
 
 
+_Strides12, _Strides10 = ctypes.c_longlong * 12, ctypes.c_longlong * 10
+_nullcontext = contextlib.nullcontext()
 PA_NORM = {"none": 0, "rms": 1, "layer": 2}
 
 
@@ -304,49 +306,59 @@ def residual_diff(cur, prev, out=None, stream=None, check: bool = False):
     return out
 
 
-@contextlib.contextmanager
-def _allocating_for(stream, device):
-    """Buffers allocated inside belong to the stream the kernels run on, so
-    that the allocator hands their memory on only behind those kernels."""
+def _on_stream(stream, device):
+    """A context in which buffers are allocated for the stream the kernels run
+    on, so that the allocator hands their memory on only behind those kernels."""
     import torch
-    if stream is None:
-        yield
-        return
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
-    with torch.cuda.stream(stream):
-        yield
+    return torch.cuda.stream(stream)
 
 
-def _check_rows(name, t, ndim, device=None):
-    """A bf16 CUDA tensor whose last dimension is contiguous."""
+def _refuse_rows(name, t, ndim, index):
+    """Raise what is wrong with an operand that must be a bf16 tensor with a
+    contiguous last dimension on CUDA device ``index``."""
     import torch
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16 (got {t.dtype})")
-    if not t.is_cuda or (device is not None and t.device != device):
-        raise ValueError(f"{name} must live on {'a CUDA device' if device is None else device}")
-    if t.dim() != ndim or (t.stride(-1) != 1 and t.shape[-1] > 1):
-        raise ValueError(f"{name} must be a {ndim}-d tensor with a contiguous last dimension")
+    if not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name} must live on {'a CUDA device' if index is None else f'cuda:{index}'}")
+    raise ValueError(f"{name} must be a {ndim}-d tensor with a contiguous last dimension")
 
 
-def _check_vector(name, t, dtype, shape, device):
+_bf16 = None
+
+
+def _check_rows(name, t, ndim, index=None):
+    """A bf16 CUDA tensor (on device ``index``, where given) whose last
+    dimension is contiguous; returns its device index.  On the way of every
+    call: only cheap accessors."""
+    global _bf16
+    if _bf16 is None:
+        import torch
+        _bf16 = torch.bfloat16
+    try:
+        at = t.get_device()
+        if (t.dtype is _bf16 and at >= 0 and (index is None or at == index) and t.dim() == ndim
+                and (t.stride(-1) == 1 or t.shape[-1] <= 1)):
+            return at
+    except AttributeError:
+        pass
+    _refuse_rows(name, t, ndim, index)
+
+
+def _check_vector(name, t, dtype, shape, index):
+    """The address of a contiguous tensor of this type and shape on device
+    ``index``; None for None."""
     if t is None:
         return None
     import torch
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != tuple(shape)
-            or not t.is_contiguous() or t.device != device):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != index):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
     return t.data_ptr()
-
-
-def _lse_out(lse, shape, device):
-    import torch
-    if lse is None:
-        return torch.empty(shape, dtype=torch.float32, device=device)
-    _check_vector("lse", lse, torch.float32, shape, device)
-    return lse
 
 
 def attn_fwd_mod(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, slopes=None, causal: bool = False,
@@ -368,44 +380,44 @@ def attn_fwd_mod(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, s
     splits the keys over the GPU.
     """
     import torch
-    _check_rows("q", q, 4)
-    _check_rows("k", k, 4, q.device)
-    _check_rows("v", v, 4, q.device)
-    B, Hq, Nq, d = q.shape
-    Hkv, Nk = k.shape[1], k.shape[2]
-    if k.shape[0] != B or k.shape[3] != d or v.shape != k.shape or Hkv < 1 or Hq % Hkv:
+    index = _check_rows("q", q, 4)
+    _check_rows("k", k, 4, index)
+    _check_rows("v", v, 4, index)
+    B, Hq, Nq, d = q_shape = q.shape
+    kB, Hkv, Nk, kd = k_shape = k.shape
+    if kB != B or kd != d or v.shape != k_shape or Hkv < 1 or Hq % Hkv:
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, k {tuple(k.shape)}, v {tuple(v.shape)}")
     n_docs = 0
     if doc_offsets is not None:
         if doc_offsets.dim() != 2 or doc_offsets.shape[1] < 2:
             raise ValueError("doc_offsets must be [B, n_docs + 1] with n_docs >= 1")
         n_docs = doc_offsets.shape[1] - 1
-    mod = ScoreMod(float(softcap), 1 if causal else 0, _check_vector("slopes", slopes, torch.float32, (Hq,), q.device),
-                   None, _check_vector("doc_offsets", doc_offsets, torch.int32, (B, n_docs + 1), q.device), n_docs,
-                   int(Nk - Nq if q_offset is None else q_offset))
+    mod = ScoreMod(softcap, 1 if causal else 0, _check_vector("slopes", slopes, torch.float32, (Hq,), index), None,
+                   _check_vector("doc_offsets", doc_offsets, torch.int32, (B, n_docs + 1), index), n_docs,
+                   Nk - Nq if q_offset is None else q_offset)
     if prefix_lens is not None:
-        shape = (B, n_docs) if n_docs else (B,)
-        if not n_docs and prefix_lens.dim() == 2:
-            shape = (B, 1)
-        mod.prefix_lens = _check_vector("prefix_lens", prefix_lens, torch.int32, shape, q.device)
-    with _allocating_for(stream, q.device):
-        if out is None:
-            out = torch.empty_like(q)  # keeps a dense layout such as [B, Nq, Hq, d]
-            if out.stride(-1) != 1:
-                out = torch.empty((B, Hq, Nq, d), dtype=torch.bfloat16, device=q.device)
-        lse = _lse_out(lse, (B, Hq, Nq), q.device)
-    _check_rows("out", out, 4, q.device)
-    if out.shape != q.shape:
+        shape = (B, n_docs) if n_docs else (B, 1) if prefix_lens.dim() == 2 else (B,)
+        mod.prefix_lens = _check_vector("prefix_lens", prefix_lens, torch.int32, shape, index)
+    if out is None or lse is None:
+        with _nullcontext if stream is None else _on_stream(stream, q.device):
+            if out is None:
+                out = torch.empty_like(q)  # keeps a dense layout such as [B, Nq, Hq, d]
+                if out.stride(-1) != 1:
+                    out = q.new_empty(q_shape)
+            if lse is None:
+                lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
+    _check_rows("out", out, 4, index)
+    if out.shape != q_shape:
         raise ValueError("out must have q's shape")
     strides = None
     if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()):
-        strides = (ctypes.c_longlong * 12)(*[s for t in (q, k, v, out) for s in t.stride()[:3]])
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    rc = load_library().pa_attn_fwd_mod(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B,
-                                         Hq, Hkv, Nq, Nk, d, strides, float(scale), ctypes.byref(mod),
-                                         _stream_handle(stream, q.device))
-    _check(rc, "pa_attn_fwd_mod", check)
+        strides = _Strides12(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *out.stride()[:3])
+    rc = load_library().pa_attn_fwd_mod(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                         _check_vector("lse", lse, torch.float32, (B, Hq, Nq), index), B, Hq, Hkv, Nq,
+                                         Nk, d, strides, 1.0 / math.sqrt(d) if scale is None else scale,
+                                         ctypes.byref(mod), _stream_handle(stream, index))
+    if rc or check:
+        _check(rc, "pa_attn_fwd_mod", check)
     return out, lse
 
 
@@ -422,50 +434,55 @@ def attn_shared_prefix(q, k_prefix, v_prefix, k_tail, v_tail, tail_lens, scale: 
     k_prefix, v_prefix [Hkv,Np,d], read once for all requests, and each
     request's own k_tail, v_tail [B,Hkv,Nt,d] up to tail_lens [B] int32, the
     new tokens' own keys being the last Nq of them.  ``softcap`` and ``slopes``
-    as in ``attn_fwd_mod``.  ``workspace`` (uint8, at least
+    as in ``attn_fwd_mod``.  ``workspace`` (at least
     ``shared_prefix_workspace_bytes``) is allocated when not given; two calls
     that may overlap on the GPU need one each.  Returns (o, lse).
     """
     import torch
-    _check_bf16("q", q, 4)
-    _check_rows("k_prefix", k_prefix, 3, q.device)
-    _check_rows("v_prefix", v_prefix, 3, q.device)
-    _check_rows("k_tail", k_tail, 4, q.device)
-    _check_rows("v_tail", v_tail, 4, q.device)
-    B, Hq, Nq, d = q.shape
-    Hkv, Np = k_prefix.shape[:2]
-    Nt = k_tail.shape[2]
-    if (k_prefix.shape[2] != d or v_prefix.shape != k_prefix.shape or tuple(k_tail.shape) != (B, Hkv, Nt, d)
-            or v_tail.shape != k_tail.shape or Hkv < 1 or Hq % Hkv):
+    index = _check_rows("q", q, 4)
+    _check_rows("k_prefix", k_prefix, 3, index)
+    _check_rows("v_prefix", v_prefix, 3, index)
+    _check_rows("k_tail", k_tail, 4, index)
+    _check_rows("v_tail", v_tail, 4, index)
+    if not q.is_contiguous():
+        raise ValueError("q must be contiguous")
+    B, Hq, Nq, d = q_shape = q.shape
+    Hkv, Np, pd = p_shape = k_prefix.shape
+    tB, tH, Nt, td = t_shape = k_tail.shape
+    if (pd != d or v_prefix.shape != p_shape or tB != B or tH != Hkv or td != d or v_tail.shape != t_shape or Hkv < 1
+            or Hq % Hkv):
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, prefix {tuple(k_prefix.shape)} and "
                          f"{tuple(v_prefix.shape)}, tail {tuple(k_tail.shape)} and {tuple(v_tail.shape)}")
-    lens = _check_vector("tail_lens", tail_lens, torch.int32, (B,), q.device)
-    sl = _check_vector("slopes", slopes, torch.float32, (Hq,), q.device)
+    lens = _check_vector("tail_lens", tail_lens, torch.int32, (B,), index)
+    sl = _check_vector("slopes", slopes, torch.float32, (Hq,), index)
     lib = load_library()
-    need = int(lib.pa_attn_shared_prefix_workspace(B, Hq, Hkv, Nq, Np, Nt, d))
-    with _allocating_for(stream, q.device):
-        if out is None:
-            out = torch.empty((B, Hq, Nq, d), dtype=torch.bfloat16, device=q.device)
-        lse = _lse_out(lse, (B, Hq, Nq), q.device)
-        if workspace is None:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
-    _check_bf16("out", out, 4)
-    if out.shape != q.shape or out.device != q.device:
-        raise ValueError("out must have q's shape and device")
-    if not isinstance(workspace, torch.Tensor) or workspace.device != q.device or not workspace.is_contiguous():
+    if out is None or lse is None or workspace is None:
+        with _nullcontext if stream is None else _on_stream(stream, q.device):
+            if out is None:
+                out = torch.empty_like(q)
+            if lse is None:
+                lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
+            if workspace is None:
+                # in bf16 elements of q: one allocation without a type to look up
+                workspace = q.new_empty((lib.pa_attn_shared_prefix_workspace(B, Hq, Hkv, Nq, Np, Nt, d) // 2,))
+    _check_rows("out", out, 4, index)
+    if out.shape != q_shape or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of q's shape")
+    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on q's device")
     strides = None
     if not (k_prefix.is_contiguous() and v_prefix.is_contiguous() and k_tail.is_contiguous()
             and v_tail.is_contiguous()):
-        strides = (ctypes.c_longlong * 10)(*k_prefix.stride()[:2], *v_prefix.stride()[:2], *k_tail.stride()[:3],
-                                           *v_tail.stride()[:3])
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
+        strides = _Strides10(*k_prefix.stride()[:2], *v_prefix.stride()[:2], *k_tail.stride()[:3],
+                             *v_tail.stride()[:3])
     rc = lib.pa_attn_shared_prefix(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_tail.data_ptr(),
-                                   v_tail.data_ptr(), lens, out.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Nq, Np, Nt, d,
-                                   strides, float(scale), float(softcap), sl, workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream_handle(stream, q.device))
-    _check(rc, "pa_attn_shared_prefix", check)
+                                   v_tail.data_ptr(), lens, out.data_ptr(),
+                                   _check_vector("lse", lse, torch.float32, (B, Hq, Nq), index), B, Hq, Hkv, Nq, Np,
+                                   Nt, d, strides, 1.0 / math.sqrt(d) if scale is None else scale, softcap, sl,
+                                   workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   _stream_handle(stream, index))
+    if rc or check:
+        _check(rc, "pa_attn_shared_prefix", check)
     return out, lse
 
 
@@ -484,42 +501,46 @@ def gate_residual_norm(y, x, gate=None, post: str = "none", post_weight=None, no
     "layer".  Returns (x_new, h); x_new has x's type and goes to ``x_out``, which
     may be x itself, h (bf16, None with norm="none") to ``out``."""
     import torch
-    _check_bf16("y", y, 3)
-    B, N, D = y.shape
-    if (not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32) or x.shape != y.shape
-            or not x.is_contiguous() or x.device != y.device):
+    index = _check_rows("y", y, 3)
+    B, N, D = shape = y.shape
+    if not y.is_contiguous():
+        raise ValueError("y must be contiguous")
+    if (not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32) or x.shape != shape
+            or not x.is_contiguous() or x.get_device() != index):
         raise ValueError("x must be a contiguous bfloat16 or float32 tensor of y's shape on its device")
     if post not in PA_NORM or norm not in PA_NORM:
         raise ValueError(f"post and norm must be one of {sorted(PA_NORM)} (got {post!r}, {norm!r})")
-    cfg = BlockNorm(PA_NORM[post], PA_NORM[norm], _check_vector("post_weight", post_weight, torch.bfloat16, (D,), y.device),
-                    _check_vector("norm_weight", norm_weight, torch.bfloat16, (D,), y.device),
-                    residual_scale=float(residual_scale), eps=float(eps))
+    cfg = BlockNorm(PA_NORM[post], PA_NORM[norm], _check_vector("post_weight", post_weight, torch.bfloat16, (D,), index),
+                    _check_vector("norm_weight", norm_weight, torch.bfloat16, (D,), index), None, None, None, 0, 0, 0,
+                    residual_scale, eps)
     for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
         if t is None:
             continue
-        _check_rows(name, t, 2, y.device)
-        if tuple(t.shape) != (B, D):
+        _check_rows(name, t, 2, index)
+        if t.shape != (B, D):
             raise ValueError(f"{name} must be [B, D] = {(B, D)} (got {tuple(t.shape)})")
         setattr(cfg, name, t.data_ptr())
         setattr(cfg, name + "_stride", t.stride(0))
     if norm == "none" and out is not None:
         raise ValueError("out is written only with a norm")
-    with _allocating_for(stream, y.device):
-        if x_out is None:
-            x_out = torch.empty_like(x)
-        if out is None and norm != "none":
-            out = torch.empty_like(y)
-    if x_out.dtype != x.dtype or x_out.shape != x.shape or not x_out.is_contiguous() or x_out.device != y.device:
+    if x_out is None or (out is None and norm != "none"):
+        with _nullcontext if stream is None else _on_stream(stream, y.device):
+            if x_out is None:
+                x_out = torch.empty_like(x)
+            if out is None and norm != "none":
+                out = torch.empty_like(y)
+    if x_out.dtype != x.dtype or x_out.shape != shape or not x_out.is_contiguous() or x_out.get_device() != index:
         raise ValueError("x_out must be a contiguous tensor of x's type and shape on its device")
     if out is not None:
-        _check_bf16("out", out, 3)
-        if out.shape != y.shape or out.device != y.device:
-            raise ValueError("out must have y's shape and device")
+        _check_rows("out", out, 3, index)
+        if out.shape != shape or not out.is_contiguous():
+            raise ValueError("out must be a contiguous tensor of y's shape")
     rc = load_library().pa_gate_residual_norm(y.data_ptr(), x.data_ptr(), x_out.data_ptr(),
                                                None if out is None else out.data_ptr(), B, N, D,
                                                1 if x.dtype == torch.float32 else 0, ctypes.byref(cfg),
-                                               _stream_handle(stream, y.device))
-    _check(rc, "pa_gate_residual_norm", check)
+                                               _stream_handle(stream, index))
+    if rc or check:
+        _check(rc, "pa_gate_residual_norm", check)
     return x_out, out
 
 

@@ -51,7 +51,7 @@ using namespace mod;
 using R = Roles<false>;  // warps and registers of the single-warpgroup kernel
 
 constexpr int kMaxCtas = 160;  // sizes the workspace; the grid is one CTA an SM, at most this many
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 8;
 constexpr int kLoadWarp = 9;   // + stream
 // Cost of a pair's key tile over a single's, in quarters: how the CTAs are
 // dealt to the two kinds.
@@ -327,6 +327,8 @@ __global__ void __launch_bounds__(R::kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
+  // The merge may be launched as CTAs end; it waits for the last one itself.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -753,7 +755,6 @@ template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __grid_constant__ Params p,
                                                                         __nv_bfloat16* o, float* lse) {
   constexpr int kCols = D / 32;
-  __shared__ int sums[2][kMergeWarps];
   __shared__ float part_m[kMergeWarps], part_l[kMergeWarps];
   __shared__ float part_o[kMergeWarps][D];
   const Plan& plan = p.plan;
@@ -762,19 +763,20 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
 
   // Tail tiles (under one K/V head) of all requests, and of those before req.
   int all = 0, before = 0;
-  for (int b = threadIdx.x; b < plan.B; b += kMergeWarps * 32) {
-    const int n = Plan::tiles_of(plan.len(b));
-    all += n;
-    if (b < req) before += n;
-    if (blockIdx.x == 0 && __ldg(plan.tail_lens + b) != plan.len(b)) atomicCAS(p.status, 0, kStatusBadInput);
+  for (int b0 = 0; b0 < plan.B; b0 += 128) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int b = b0 + u * 32 + lane;
+      if (b >= plan.B) continue;
+      const int n = Plan::tiles_of(plan.len(b));
+      all += n;
+      if (b < req) before += n;
+      if (blockIdx.x == 0 && warp == 0 && __ldg(plan.tail_lens + b) != plan.len(b))
+        atomicCAS(p.status, 0, kStatusBadInput);
+    }
   }
   all = __reduce_add_sync(0xffffffffu, all);
   before = __reduce_add_sync(0xffffffffu, before);
-  if (lane == 0) sums[0][warp] = all, sums[1][warp] = before;
-  __syncthreads();
-  all = before = 0;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) all += sums[0][w], before += sums[1][w];
 
   // Parts [p0, p1) of the pairs' or the singles' line hold the prefix under this
   // row tile, [t0, t1) of the singles' the tail.
@@ -800,6 +802,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
   const int n_p = (p1 - p0) * copies_p, n_parts = n_p + (t1 - t0) * copies_t;
   const float* const p_o = pair ? p.pair_o : p.odd_o;
   const float* const p_lse = pair ? p.pair_lse : p.odd_lse;
+
+  // All of the above runs while the other kernel ends; its results are there
+  // behind this.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   int group = kMergeWarps;  // warps a row
   while (group > 1 && group * plan.rows > kMergeWarps) group /= 2;

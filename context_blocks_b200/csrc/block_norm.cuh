@@ -10,8 +10,7 @@
 // All in fp32, rounded once on output; h is taken from x' before its rounding.
 //
 // HBM-bound: 8 bytes an element with a bf16 residual stream, 12 with fp32.  A row
-// stays in the registers of a group of kWarps warps (kVecs 16-byte vectors a
-// thread) from its loads to its stores, so every input is read once whatever the
+// stays in the registers of a group of warps (kVecs 16-byte vectors a thread) from its loads to its stores, so every input is read once whatever the
 // norms need.  All loads of a thread are issued before the first reduction.
 #pragma once
 
@@ -45,18 +44,16 @@ struct Params {
   float residual_scale, eps;
 };
 
-// Sum over the kWarps warps of a row's group, the same bits in all of them.
-template <int kWarps>
-__device__ __forceinline__ float group_sum(float v, float* red, int group) {
+// Sum over the `warps` warps of a row's group, the same bits in all of them.
+__device__ __forceinline__ float group_sum(float v, float* red, int group, int warps) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  if constexpr (kWarps > 1) {
-    const int w = (threadIdx.x / 32) % kWarps;
-    if (threadIdx.x % 32 == 0) red[group * kWarps + w] = v;
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(kWarps * 32) : "memory");
+  if (warps > 1) {
+    const int first = group * warps;
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(warps * 32) : "memory");
     v = 0.f;
-#pragma unroll
-    for (int u = 0; u < kWarps; ++u) v += red[group * kWarps + u];
+    for (int u = 0; u < warps; ++u) v += red[first + u];
   }
   return v;
 }
@@ -69,12 +66,11 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// v <- norm(v), in the registers of the row's group.  `red` holds two rows of
-// partial sums, used in turn (a group's next sum may start while a slower warp
-// still reads the last one).
-template <int kVecs, int kWarps>
+// v <- norm(v), in the registers of the row's group.  Every sum has a row of
+// `red` of its own, so that none is overwritten while a slower warp reads it.
+template <int kVecs>
 __device__ __forceinline__ void normalise(float (&v)[kVecs][8], int kind, const Params& p, float (&red)[4][8], int first,
-                                          int group, int t) {
+                                          int group, int t, int warps) {
   const float inv_d = 1.f / static_cast<float>(p.D);
   if (kind == kLayer) {
     float s = 0.f;
@@ -82,10 +78,10 @@ __device__ __forceinline__ void normalise(float (&v)[kVecs][8], int kind, const 
     for (int i = 0; i < kVecs; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += v[i][e];
-    const float mean = group_sum<kWarps>(s, red[first], group) * inv_d;
+    const float mean = group_sum(s, red[first], group, warps) * inv_d;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i)
-      if ((t + i * kWarps * 32) * 8 < p.D)  // vectors past the row stay zero
+      if ((t + i * warps * 32) * 8 < p.D)  // vectors past the row stay zero
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[i][e] -= mean;
   }
@@ -94,26 +90,25 @@ __device__ __forceinline__ void normalise(float (&v)[kVecs][8], int kind, const 
   for (int i = 0; i < kVecs; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) s = fmaf(v[i][e], v[i][e], s);
-  const float r = rsqrtf(group_sum<kWarps>(s, red[first + 1], group) * inv_d + p.eps);
+  const float r = rsqrtf(group_sum(s, red[first + 1], group, warps) * inv_d + p.eps);
 #pragma unroll
   for (int i = 0; i < kVecs; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[i][e] *= r;
 }
 
-template <bool kX32, int kVecs, int kWarps>
-__global__ void __launch_bounds__(kThreads) gate_residual_norm_kernel(const Params p) {
-  constexpr int kGroups = kThreads / 32 / kWarps;  // rows a block takes at a time
+template <bool kX32, int kVecs>
+__global__ void __launch_bounds__(kThreads) gate_residual_norm_kernel(const Params p, int warps) {
   __shared__ float red[4][8];
-  const int group = threadIdx.x / (kWarps * 32), t = threadIdx.x % (kWarps * 32);
-  const long long row = static_cast<long long>(blockIdx.x) * kGroups + group;
+  const int group = threadIdx.x / (warps * 32), t = threadIdx.x % (warps * 32);
+  const long long row = static_cast<long long>(blockIdx.x) * (blockDim.x / (warps * 32)) + group;
   if (row >= p.rows) return;  // whole groups leave: their barrier is their own
   const long long b = row / p.rows_per_batch;
   const long long at = row * p.D;
   float v[kVecs][8], x[kVecs][8];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int c = (t + i * kWarps * 32) * 8;
+    const int c = (t + i * warps * 32) * 8;
     if (c < p.D) {
       unpack_bf16x8(__ldcs(reinterpret_cast<const uint4*>(p.y + at + c)), v[i]);
       if constexpr (kX32) {
@@ -129,10 +124,10 @@ __global__ void __launch_bounds__(kThreads) gate_residual_norm_kernel(const Para
       for (int e = 0; e < 8; ++e) v[i][e] = x[i][e] = 0.f;
     }
   }
-  if (p.post != kNone) normalise<kVecs, kWarps>(v, p.post, p, red, 0, group, t);
+  if (p.post != kNone) normalise<kVecs>(v, p.post, p, red, 0, group, t, warps);
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int c = (t + i * kWarps * 32) * 8;
+    const int c = (t + i * warps * 32) * 8;
     if (c < p.D) {
       float w[8];
       if (p.post_weight) {
@@ -157,10 +152,10 @@ __global__ void __launch_bounds__(kThreads) gate_residual_norm_kernel(const Para
     }
   }
   if (p.norm == kNone) return;
-  normalise<kVecs, kWarps>(v, p.norm, p, red, 2, group, t);
+  normalise<kVecs>(v, p.norm, p, red, 2, group, t, warps);
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int c = (t + i * kWarps * 32) * 8;
+    const int c = (t + i * warps * 32) * 8;
     if (c < p.D) {
       float w[8];
       if (p.norm_weight) {

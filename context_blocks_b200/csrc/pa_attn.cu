@@ -537,28 +537,26 @@ int by_mod(int d, bool cap, bool bias, F f) {
 
 // ------------------------------------------------------ gated residual norm
 
-template <bool kX32, int kVecs, int kWarps>
+template <bool kX32, int kVecs>
 int launch_block_norm(const pa::norm::Params& prm, cudaStream_t stream) {
-  constexpr int kRows = pa::norm::kThreads / 32 / kWarps;
-  const long long blocks = (prm.rows + kRows - 1) / kRows;
+  // The fewest warps that hold a row, and as many rows a block as make 8 warps.
+  const int warps = (prm.D / 8 + 32 * kVecs - 1) / (32 * kVecs), rows = 8 / warps;
+  const long long blocks = (prm.rows + rows - 1) / rows;
   if (blocks > 0x7fffffffLL) return fail(PA_ERR_UNSUPPORTED, "too many rows");
-  pa::norm::gate_residual_norm_kernel<kX32, kVecs, kWarps>
-      <<<static_cast<unsigned>(blocks), pa::norm::kThreads, 0, stream>>>(prm);
+  pa::norm::gate_residual_norm_kernel<kX32, kVecs>
+      <<<static_cast<unsigned>(blocks), rows * warps * 32, 0, stream>>>(prm, warps);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "gate_residual_norm launch");
   return PA_OK;
 }
 
-// The fewest warps a row that hold it in four vectors a thread (eight above 8192).
+// kVecs vectors a thread, at most 8 warps a row.
 template <bool kX32>
 int launch_block_norm_x(const pa::norm::Params& prm, cudaStream_t stream) {
-  if (prm.D <= 256) return launch_block_norm<kX32, 1, 1>(prm, stream);
-  if (prm.D <= 512) return launch_block_norm<kX32, 2, 1>(prm, stream);
-  if (prm.D <= 1024) return launch_block_norm<kX32, 4, 1>(prm, stream);
-  if (prm.D <= 2048) return launch_block_norm<kX32, 4, 2>(prm, stream);
-  if (prm.D <= 4096) return launch_block_norm<kX32, 4, 4>(prm, stream);
-  if (prm.D <= 8192) return launch_block_norm<kX32, 4, 8>(prm, stream);
-  return launch_block_norm<kX32, 8, 8>(prm, stream);
+  if (prm.D <= 256) return launch_block_norm<kX32, 1>(prm, stream);
+  if (prm.D <= 4096) return launch_block_norm<kX32, 2>(prm, stream);
+  if (prm.D <= 8192) return launch_block_norm<kX32, 4>(prm, stream);
+  return launch_block_norm<kX32, 8>(prm, stream);
 }
 
 int launch_block_norm(const pa::norm::Params& prm, bool x32, cudaStream_t stream) {
@@ -625,9 +623,20 @@ int launch_shared(DeviceState* st, const CUtensorMap (&maps)[6], const pa::share
   if (prm.plan.Np > 0 || prm.plan.Nt > 0)
     kern<<<prm.plan.ctas, pa::shared::R::kThreads, L::kAllocBytes, stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4],
                                                                        maps[5], prm);
-  pa::shared::shared_merge_kernel<D><<<prm.plan.B * prm.plan.Hkv, pa::shared::kMergeWarps * 32, 0, stream>>>(
-      prm, static_cast<__nv_bfloat16*>(o), lse);
   cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "attn_shared launch");
+  // Launched while the first kernel runs (the merge waits for its results), so
+  // that the launch and the merge's own reckoning cost no time between the two.
+  cudaLaunchAttribute overlap;
+  overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  overlap.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(prm.plan.B * prm.plan.Hkv));
+  cfg.blockDim = dim3(pa::shared::kMergeWarps * 32);
+  cfg.stream = stream;
+  cfg.attrs = &overlap;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, pa::shared::shared_merge_kernel<D>, prm, static_cast<__nv_bfloat16*>(o), lse);
   if (e != cudaSuccess) return cuda_fail(e, "attn_shared launch");
   return PA_OK;
 }
