@@ -66,8 +66,9 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
-// v <- norm(v), in the registers of the row's group.  Every sum has a row of
-// `red` of its own, so that none is overwritten while a slower warp reads it.
+// v <- norm(v), in the registers of the row's group.  Every sum of a row has its
+// own line of `red`, and rows have two tables in turn, so that none is
+// overwritten while a slower warp reads it.
 template <int kVecs>
 __device__ __forceinline__ void normalise(float (&v)[kVecs][8], int kind, const Params& p, float (&red)[4][8], int first,
                                           int group, int t, int warps) {
@@ -97,33 +98,34 @@ __device__ __forceinline__ void normalise(float (&v)[kVecs][8], int kind, const 
     for (int e = 0; e < 8; ++e) v[i][e] *= r;
 }
 
-template <bool kX32, int kVecs>
-__global__ void __launch_bounds__(kThreads) gate_residual_norm_kernel(const Params p, int warps) {
-  __shared__ float red[4][8];
-  const int group = threadIdx.x / (warps * 32), t = threadIdx.x % (warps * 32);
-  const long long row = static_cast<long long>(blockIdx.x) * (blockDim.x / (warps * 32)) + group;
-  if (row >= p.rows) return;  // whole groups leave: their barrier is their own
-  const long long b = row / p.rows_per_batch;
+// One row: from the raw vectors to the outputs; `next` asks for the next row's
+// vectors as soon as this one's are taken.
+template <bool kX32, int kVecs, int kXWords, typename Next>
+__device__ __forceinline__ void one_row(const Params& p, long long row, const uint4 (&ry)[kVecs],
+                                        const uint4 (&rx)[kVecs][kXWords], float (&red)[4][8], int group, int t,
+                                        int warps, Next next) {
+  const long long b = p.rows_per_batch == p.rows ? 0 : row / p.rows_per_batch;
   const long long at = row * p.D;
   float v[kVecs][8], x[kVecs][8];
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
-    const int c = (t + i * warps * 32) * 8;
-    if (c < p.D) {
-      unpack_bf16x8(__ldcs(reinterpret_cast<const uint4*>(p.y + at + c)), v[i]);
+    if ((t + i * warps * 32) * 8 < p.D) {
+      unpack_bf16x8(ry[i], v[i]);
       if constexpr (kX32) {
-        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.x) + at + c);
-        const float4 a = __ldcs(src), d = __ldcs(src + 1);
-        x[i][0] = a.x, x[i][1] = a.y, x[i][2] = a.z, x[i][3] = a.w;
-        x[i][4] = d.x, x[i][5] = d.y, x[i][6] = d.z, x[i][7] = d.w;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          x[i][4 * u] = __uint_as_float(rx[i][u].x), x[i][4 * u + 1] = __uint_as_float(rx[i][u].y);
+          x[i][4 * u + 2] = __uint_as_float(rx[i][u].z), x[i][4 * u + 3] = __uint_as_float(rx[i][u].w);
+        }
       } else {
-        unpack_bf16x8(__ldcs(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.x) + at + c)), x[i]);
+        unpack_bf16x8(rx[i][0], x[i]);
       }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] = x[i][e] = 0.f;
     }
   }
+  next();
   if (p.post != kNone) normalise<kVecs>(v, p.post, p, red, 0, group, t, warps);
 #pragma unroll
   for (int i = 0; i < kVecs; ++i) {
@@ -175,6 +177,43 @@ __global__ void __launch_bounds__(kThreads) gate_residual_norm_kernel(const Para
       }
       __stcs(reinterpret_cast<uint4*>(p.h + at + c), pack8(v[i]));
     }
+  }
+}
+
+__host__ __device__ constexpr bool stays(bool x32) { return !x32; }
+// Blocks of 8 warps an SM, where blocks stay.
+__host__ __device__ constexpr int resident_blocks(int vecs) { return vecs <= 2 ? 3 : vecs == 4 ? 2 : 1; }
+
+template <bool kX32, int kVecs>
+__global__ void __launch_bounds__(kThreads, stays(kX32) ? resident_blocks(kVecs) : 1)
+    gate_residual_norm_kernel(const Params p, int warps) {
+  __shared__ float red[2][4][8];
+  const int group = threadIdx.x / (warps * 32), t = threadIdx.x % (warps * 32);
+  const int groups = blockDim.x / (warps * 32);
+  // This thread's vectors of a row, as they lie in memory.
+  constexpr int kXWords = kX32 ? 2 : 1;
+  uint4 ry[kVecs], rx[kVecs][kXWords];
+  auto fetch = [&](long long row) {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) {
+      const int c = (t + i * warps * 32) * 8;
+      if (row >= p.rows || c >= p.D) continue;
+      const long long at = row * p.D + c;
+      ry[i] = __ldcs(reinterpret_cast<const uint4*>(p.y + at));
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(p.x) + at * (kX32 ? 4 : 2));
+#pragma unroll
+      for (int u = 0; u < kXWords; ++u) rx[i][u] = __ldcs(src + u);
+    }
+  };
+  long long row = static_cast<long long>(blockIdx.x) * groups + group;
+  fetch(row);
+  // Groups of warps leave alone: their barrier is their own.
+  if constexpr (stays(kX32)) {
+    const long long step = static_cast<long long>(gridDim.x) * groups;
+    for (int it = 0; row < p.rows; row += step, ++it)
+      one_row<kX32, kVecs>(p, row, ry, rx, red[it & 1], group, t, warps, [&] { fetch(row + step); });
+  } else {
+    if (row < p.rows) one_row<kX32, kVecs>(p, row, ry, rx, red[0], group, t, warps, [] {});
   }
 }
 

@@ -538,10 +538,15 @@ int by_mod(int d, bool cap, bool bias, F f) {
 // ------------------------------------------------------ gated residual norm
 
 template <bool kX32, int kVecs>
-int launch_block_norm(const pa::norm::Params& prm, cudaStream_t stream) {
-  // The fewest warps that hold a row, and as many rows a block as make 8 warps.
+int launch_block_norm(DeviceState* st, const pa::norm::Params& prm, cudaStream_t stream) {
+  // The fewest warps that hold a row, and as many rows a block as make 8 warps;
+  // where blocks stay, no more of them than are resident at a time.
   const int warps = (prm.D / 8 + 32 * kVecs - 1) / (32 * kVecs), rows = 8 / warps;
-  const long long blocks = (prm.rows + rows - 1) / rows;
+  long long blocks = (prm.rows + rows - 1) / rows;
+  if (pa::norm::stays(kX32)) {
+    const int resident = pa::norm::resident_blocks(kVecs) * 8 / (rows * warps);
+    blocks = std::min(blocks, static_cast<long long>(resident) * st->sm_count);
+  }
   if (blocks > 0x7fffffffLL) return fail(PA_ERR_UNSUPPORTED, "too many rows");
   pa::norm::gate_residual_norm_kernel<kX32, kVecs>
       <<<static_cast<unsigned>(blocks), rows * warps * 32, 0, stream>>>(prm, warps);
@@ -552,15 +557,15 @@ int launch_block_norm(const pa::norm::Params& prm, cudaStream_t stream) {
 
 // kVecs vectors a thread, at most 8 warps a row.
 template <bool kX32>
-int launch_block_norm_x(const pa::norm::Params& prm, cudaStream_t stream) {
-  if (prm.D <= 256) return launch_block_norm<kX32, 1>(prm, stream);
-  if (prm.D <= 4096) return launch_block_norm<kX32, 2>(prm, stream);
-  if (prm.D <= 8192) return launch_block_norm<kX32, 4>(prm, stream);
-  return launch_block_norm<kX32, 8>(prm, stream);
+int launch_block_norm_x(DeviceState* st, const pa::norm::Params& prm, cudaStream_t stream) {
+  if (prm.D <= 256) return launch_block_norm<kX32, 1>(st, prm, stream);
+  if (prm.D <= 4096) return launch_block_norm<kX32, 2>(st, prm, stream);
+  if (prm.D <= 8192) return launch_block_norm<kX32, 4>(st, prm, stream);
+  return launch_block_norm<kX32, 8>(st, prm, stream);
 }
 
-int launch_block_norm(const pa::norm::Params& prm, bool x32, cudaStream_t stream) {
-  return x32 ? launch_block_norm_x<true>(prm, stream) : launch_block_norm_x<false>(prm, stream);
+int launch_block_norm(DeviceState* st, const pa::norm::Params& prm, bool x32, cudaStream_t stream) {
+  return x32 ? launch_block_norm_x<true>(st, prm, stream) : launch_block_norm_x<false>(st, prm, stream);
 }
 
 // Shapes of a shared-prefix call; false where the rows of one request under one
@@ -1068,7 +1073,7 @@ int pa_gate_residual_norm(const void* y, const void* x, void* x_out, void* h, in
   prm.norm = cfg->norm;
   prm.residual_scale = cfg->residual_scale;
   prm.eps = cfg->eps;
-  return launch_block_norm(prm, x_f32 != 0, static_cast<cudaStream_t>(stream));
+  return launch_block_norm(st, prm, x_f32 != 0, static_cast<cudaStream_t>(stream));
 }
 
 int pa_attn_chunks_noalloc(const void* q, const void* const* k_chunks, const void* const* v_chunks,
