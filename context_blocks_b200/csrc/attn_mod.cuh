@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
       if constexpr (kWide)
         bad = store_cols_bf16<kCols>(tO, stage, o, p.o_s[2], p.Nq - wrow, inv);
       else
-        bad = store_rows<D>(tO, stage, o, nullptr, p.o_s[2], p.Nq - wrow, inv);
+        bad = store_rows<D>(tO, stage, o, p.o_s[2], p.Nq - wrow, inv);
       if (half == 0 && row < p.Nq)
         p.lse[static_cast<size_t>(bh) * p.Nq + row] =
             empty ? -INFINITY : (m_ref + lg2_approx(l)) * 0.69314718055994531f;

@@ -55,7 +55,7 @@ constexpr int kMergeWarps = 8;
 constexpr int kLoadWarp = 9;   // + stream
 // Cost of a pair's key tile over a single's, in quarters: how the CTAs are
 // dealt to the two kinds.
-constexpr int kPairCost4 = 4;
+constexpr int kPairCost4 = 8;
 
 // A line of n units cut into `parts` parts, none empty, sizes differing by one.
 struct Cut {
@@ -103,11 +103,11 @@ struct Params {
   const __nv_bfloat16* vt;
   long long kt_s[3], vt_s[3];  // tail strides: batch, head, row (elements)
   float* pair_o;               // [(Hkv * pairs + ctas) * 2][tile_rows][D]
-  float* pair_lse;
+  float2* pair_ml;
   float* odd_o;                // [(Hkv + 2 * ctas) * copies][tile_rows][D]
-  float* odd_lse;
+  float2* odd_ml;
   float* tail_o;               // [(B * Hkv + 2 * ctas) * copies][rows][D]
-  float* tail_lse;
+  float2* tail_ml;
   ScoreMod sm;
   int* status;
   unsigned long long timeout_ns;
@@ -230,30 +230,59 @@ __device__ __forceinline__ void softmax_share(uint32_t tS, uint32_t tO, int kq, 
   }
 }
 
-// Scale a thread's O row by inv and store it as fp32 at dst, where `write`.
-// For a warp with few rows: no staging.  inv = 0 stores zeros.  Returns whether
-// the row has a value that is not finite.
+// A thread's O row as it is, to dst, where `write`.  For a warp with few rows: no
+// staging.  Kept as short as it can be, like store_raw_rows: it runs once a piece,
+// and long straight code that has left the instruction cache costs more than
+// its instructions (scaling and checking the row here: 4 500 clocks).
 template <int D>
-__device__ __noinline__ bool store_row_f32(uint32_t tO, float* dst, bool write, float inv) {
-  float bad = 0.f;
+__device__ __noinline__ void store_raw_row(uint32_t tO, float* dst, bool write) {
+  uint32_t w[D];
+  if constexpr (D == 128)
+    tmem_ld_x128(tO, w);
+  else
+    tmem_ld_x64(tO, w);
+  if (write)
+#pragma unroll
+    for (int u = 0; u < D / 4; ++u)
+      reinterpret_cast<uint4*>(dst)[u] = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+}
+
+// The O rows of a warp as they are, through its staging area (see attn_fwd.cuh):
+// row r at dst + r * D, rows r >= rows_left not written.
+template <int D>
+__device__ __noinline__ void store_raw_rows(uint32_t tO, uint32_t stg, float* dst, int rows_left) {
+  const int lane = threadIdx.x % 32;
+  const int r0 = lane >> 3, c = lane & 7;
 #pragma unroll 1
   for (int ch = 0; ch < D / 32; ++ch) {
-    uint32_t orr[32];
-    tmem_ld_x32(tO + ch * 32, orr);
-    float v[32];
+    uint32_t w[32];
+    tmem_ld_x32(tO + ch * 32, w);
+    __syncwarp();  // the previous piece has left the staging area
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float x = __uint_as_float(orr[e]);
-      bad = fmaf(x, 0.f, bad);
-      v[e] = inv == 0.f ? 0.f : x * inv;
-    }
-    if (write) {
+    for (int u = 0; u < 8; ++u)
+      st_shared_v4(stg + lane * 128 + ((u ^ (lane & 7)) << 4), w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+    __syncwarp();
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        reinterpret_cast<float4*>(dst + ch * 32)[u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+    for (int k = 0; k < 8; ++k) {
+      const int r = 4 * k + r0;
+      const uint4 x = ld_shared_v4(stg + r * 128 + ((c ^ (r & 7)) << 4));
+      if (r < rows_left) *reinterpret_cast<uint4*>(dst + r * D + ch * 32 + c * 4) = x;
     }
   }
-  return !(bad == 0.f);
+}
+
+// Whether a thread's O row is finite throughout.
+template <int D>
+__device__ __noinline__ bool row_is_finite(uint32_t tO) {
+  float sum = 0.f;  // x * 0 is NaN where x is not finite
+#pragma unroll 1
+  for (int ch = 0; ch < D / 16; ++ch) {
+    uint32_t w[16];
+    tmem_ld_x16(tO + ch * 16, w);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) sum = fmaf(__uint_as_float(w[e]), 0.f, sum);
+  }
+  return sum == 0.f;
 }
 
 template <int D, bool kCap, bool kBias>
@@ -704,34 +733,33 @@ __global__ void __launch_bounds__(R::kThreads, 1)
         tc_fence_after();
       }
       if (!active) continue;
-      const bool empty = !mine || l == 0.f;
-      const float inv = empty ? 0.f : 1.f / l;
       const size_t row0 = x.kind == kPair ? static_cast<size_t>(2 * x.slot + i) * plan.tile_rows()
                                           : static_cast<size_t>(x.slot * copies + kq) *
                                                 (x.kind == kOdd ? plan.tile_rows() : plan.rows);
       float* o = (x.kind == kPair ? p.pair_o : x.kind == kOdd ? p.odd_o : p.tail_o) + (row0 + wr) * D;
-      const bool bad = copies > 1 ? store_row_f32<D>(tO, o + lane * D, mine, inv)
-                                  : store_rows<D>(tO, base + L::kStageOff + warp * L::kStageWarpBytes, nullptr, o, D,
-                                                  rows - wr, inv);
+      if (copies > 1)
+        store_raw_row<D>(tO, o + lane * D, mine);
+      else
+        store_raw_rows<D>(tO, base + L::kStageOff + warp * L::kStageWarpBytes, o, rows - wr);
       if (mine)
-        (x.kind == kPair ? p.pair_lse : x.kind == kOdd ? p.odd_lse : p.tail_lse)[row0 + r] =
-            empty ? -INFINITY : m_ref + lg2_approx(l);
+        (x.kind == kPair ? p.pair_ml : x.kind == kOdd ? p.odd_ml : p.tail_ml)[row0 + r] =
+            make_float2(l == 0.f ? -INFINITY : m_ref, l);
       // A value row that is not finite among the new tokens of a request does
       // not reach the tokens before it (see repair_row).
       if (x.kind == kTail && plan.Nq > 1) {
-        unsigned redo = __ballot_sync(0xffffffffu, bad && !empty && l <= FLT_MAX);
+        unsigned redo = __ballot_sync(0xffffffffu, !row_is_finite<D>(tO) && mine && l > 0.f && l <= FLT_MAX);
         while (redo != 0u) {
           const int k = __ffs(redo) - 1;
           redo &= redo - 1;
           __syncwarp();
           const int ps = __shfl_sync(0xffffffffu, pos, k), sn = __shfl_sync(0xffffffffu, seen, k);
-          const float mr = __shfl_sync(0xffffffffu, m_ref, k), iv = __shfl_sync(0xffffffffu, inv, k);
+          const float mr = __shfl_sync(0xffffffffu, m_ref, k);
           const float sl = __shfl_sync(0xffffffffu, slope2, k);
           const size_t q_row =
               (static_cast<size_t>(x.req) * plan.Hq + x.hk * plan.G) * plan.Nq + wr + k;  // rows of a K/V head are adjacent
           repair_row<D, D>(p.q + q_row * D, p.kt + x.req * p.kt_s[0] + x.hk * p.kt_s[1],
                         p.vt + x.req * p.vt_s[0] + x.hk * p.vt_s[1], p.kt_s[2], p.vt_s[2], x.t0 * kBN,
-                        min(sn, x.t1 * kBN), kBN / copies, kBN, kq, ps, mr, iv, sl, p.sm, kCap, kBias, nullptr,
+                        min(sn, x.t1 * kBN), kBN / copies, kBN, kq, ps, mr, 1.f, sl, p.sm, kCap, kBias, nullptr,
                         o + k * D);
         }
       }
@@ -746,8 +774,9 @@ __global__ void __launch_bounds__(R::kThreads, 1)
   }
 }
 
-// Joins the partial results of every row, as pa_attn_merge defines it:
-//     M = max_p lse_p,  w_p = 2^(lse_p - M),  o = sum w_p o_p / sum w_p
+// Joins the partial results of every row:
+//     M = max_p m_p,  w_p = 2^(m_p - M),  L = sum w_p l_p
+//     o = sum w_p o_p / L,  lse = (M + log2 L) ln 2
 // One block a (request, K/V head); its rows are dealt to groups of warps, the
 // partials of a row to the warps of its group.  The partials lie where the
 // kernel above put them: the same lines are cut into the same parts.
@@ -801,7 +830,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
   }
   const int n_p = (p1 - p0) * copies_p, n_parts = n_p + (t1 - t0) * copies_t;
   const float* const p_o = pair ? p.pair_o : p.odd_o;
-  const float* const p_lse = pair ? p.pair_lse : p.odd_lse;
+  const float2* const p_ml = pair ? p.pair_ml : p.odd_ml;
 
   // All of the above runs while the other kernel ends; its results are there
   // behind this.
@@ -819,28 +848,28 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
     for (int k0 = 0; k0 < n_parts && row_ok; k0 += 32 * group) {
       const int k = k0 + lane * group + wi;
       const float* src = nullptr;
-      float my = -INFINITY;
+      float2 my = make_float2(-INFINITY, 0.f);  // m = -inf, l = 0: a part that saw nothing
       if (k < n_parts) {
         if (k < n_p) {
           const int slot = pair ? 2 * (seg_p + p0 + k) + (mt & 1) : (seg_p + p0) * copies_p + k;
           const size_t row = static_cast<size_t>(slot) * plan.tile_rows() + (req % plan.tile_reqs) * plan.rows + rr;
-          my = __ldcg(p_lse + row);
+          my = __ldcg(p_ml + row);
           src = p_o + row * D;
         } else {
           const size_t row = static_cast<size_t>((seg_t + t0) * copies_t + k - n_p) * plan.rows + rr;
-          my = __ldcg(p.tail_lse + row);
+          my = __ldcg(p.tail_ml + row);
           src = p.tail_o + row * D;
         }
       }
-      float mx = my;
+      float mx = my.x;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       const float nm = fmaxf(m, mx);
-      if (nm == -INFINITY && !__any_sync(0xffffffffu, my != my)) continue;
-      const float w = (my == -INFINITY) ? 0.f : exp2f(my - nm);
+      if (nm == -INFINITY) continue;
+      const float w = (my.x == -INFINITY) ? 0.f : exp2f(my.x - nm);
       const float keep = (m == -INFINITY) ? 0.f : exp2f(m - nm);
       m = nm;
-      float lw = w;
+      float lw = (my.x == -INFINITY) ? 0.f : w * my.y;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
       l = l * keep + lw;

@@ -595,7 +595,7 @@ bool shared_plan(int B, int Hq, int Hkv, int Nq, int Np, int Nt, int ctas, pa::s
 // Byte offsets of the parts of a shared-prefix workspace (each on a 256-byte
 // boundary), and their end.
 struct SharedWorkspace {
-  uint64_t pair_o, pair_lse, odd_o, odd_lse, tail_o, tail_lse, end;
+  uint64_t pair_o, pair_ml, odd_o, odd_ml, tail_o, tail_ml, end;
 };
 
 SharedWorkspace shared_workspace(const pa::shared::Plan& plan, int d) {
@@ -608,12 +608,12 @@ SharedWorkspace shared_workspace(const pa::shared::Plan& plan, int d) {
       plan.Nt > 0 ? (static_cast<uint64_t>(plan.B) * plan.Hkv + 2ull * kMaxCtas) * plan.copies(plan.rows) * rows : 0;
   SharedWorkspace w;
   w.pair_o = 0;
-  w.pair_lse = up(pair * d * 4);
-  w.odd_o = w.pair_lse + up(pair * 4);
-  w.odd_lse = w.odd_o + up(odd * d * 4);
-  w.tail_o = w.odd_lse + up(odd * 4);
-  w.tail_lse = w.tail_o + up(tail * d * 4);
-  w.end = w.tail_lse + up(tail * 4);
+  w.pair_ml = up(pair * d * 4);
+  w.odd_o = w.pair_ml + up(pair * 8);
+  w.odd_ml = w.odd_o + up(odd * d * 4);
+  w.tail_o = w.odd_ml + up(odd * 8);
+  w.tail_ml = w.tail_o + up(tail * d * 4);
+  w.end = w.tail_ml + up(tail * 8);
   return w;
 }
 
@@ -733,11 +733,11 @@ int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_pre
   }
   uint8_t* w = static_cast<uint8_t*>(workspace);
   prm.pair_o = reinterpret_cast<float*>(w + ws.pair_o);
-  prm.pair_lse = reinterpret_cast<float*>(w + ws.pair_lse);
+  prm.pair_ml = reinterpret_cast<float2*>(w + ws.pair_ml);
   prm.odd_o = reinterpret_cast<float*>(w + ws.odd_o);
-  prm.odd_lse = reinterpret_cast<float*>(w + ws.odd_lse);
+  prm.odd_ml = reinterpret_cast<float2*>(w + ws.odd_ml);
   prm.tail_o = reinterpret_cast<float*>(w + ws.tail_o);
-  prm.tail_lse = reinterpret_cast<float*>(w + ws.tail_lse);
+  prm.tail_ml = reinterpret_cast<float2*>(w + ws.tail_ml);
   prm.sm = score_mod(scale, softcap, slopes);
   prm.status = st->status;
   prm.timeout_ns = g_wait_limit_ns.load(std::memory_order_relaxed);

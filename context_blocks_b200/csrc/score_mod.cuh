@@ -437,71 +437,45 @@ __device__ __noinline__ bool store_cols_bf16(uint32_t tO, uint32_t stg, __nv_bfl
   return !(bad == 0.f);
 }
 
-// Scale a thread's O row (TMEM columns [tO, tO + D)) by `inv` and store it,
-// through the warp's 4 KB staging area (see attn_fwd.cuh), as bf16 or, where
-// o_bf16 is null, as fp32.  Row r of the warp is at dst0 + r * row_stride
-// elements; rows r >= rows_left are not written.  inv = 0 stores zeros
-// whatever the accumulator holds.  Returns whether this thread's row has a
-// value that is not finite.
+// Scale a thread's O row (TMEM columns [tO, tO + D)) by `inv` and store it as
+// bf16, through the warp's 4 KB staging area (see attn_fwd.cuh).  Row r of the
+// warp is at dst + r * row_stride elements; rows r >= rows_left are not written.
+// inv = 0 stores zeros whatever the accumulator holds.  Returns whether this
+// thread's row has a value that is not finite.
 template <int D>
-__device__ __noinline__ bool store_rows(uint32_t tO, uint32_t stg, __nv_bfloat16* o_bf16, float* o_f32,
-                                        long long row_stride, int rows_left, float inv) {
+__device__ __noinline__ bool store_rows(uint32_t tO, uint32_t stg, __nv_bfloat16* dst, long long row_stride,
+                                        int rows_left, float inv) {
   const int lane = threadIdx.x % 32;
   const int r0 = lane >> 3, c = lane & 7;
-  float bad = 0.f;  // x * 0 is NaN where x is not finite
-  auto value = [&](uint32_t w) {
-    const float x = __uint_as_float(w);
-    bad = fmaf(x, 0.f, bad);
-    return inv == 0.f ? 0.f : x * inv;
-  };
-  auto stage4 = [&](int c0, const uint32_t (&w)[16]) {
+  float bad[2] = {0.f, 0.f};  // x * 0 is NaN where x is not finite
+#pragma unroll 1
+  for (int h = 0; h < D / 64; ++h) {
+    __syncwarp();  // the previous piece has left the staging area
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      st_shared_v4(stg + lane * 128 + (((c0 + u) ^ (lane & 7)) << 4), w[4 * u], w[4 * u + 1], w[4 * u + 2],
-                   w[4 * u + 3]);
-  };
-  auto drain = [&](uint8_t* dst, long long row_bytes) {
-    dst += r0 * row_bytes + c * 16;
+    for (int hh = 0; hh < 2; ++hh) {
+      uint32_t orr[32], pk[16];
+      tmem_ld_x32(tO + h * 64 + hh * 32, orr);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float x0 = __uint_as_float(orr[2 * e]), x1 = __uint_as_float(orr[2 * e + 1]);
+        bad[0] = fmaf(x0, 0.f, bad[0]);
+        bad[1] = fmaf(x1, 0.f, bad[1]);
+        pk[e] = inv == 0.f ? 0u : pack_bf16x2(x0 * inv, x1 * inv);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        st_shared_v4(stg + lane * 128 + (((4 * hh + u) ^ (lane & 7)) << 4), pk[4 * u], pk[4 * u + 1], pk[4 * u + 2],
+                     pk[4 * u + 3]);
+    }
+    __syncwarp();
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const int r = 4 * k + r0;
       const uint4 x = ld_shared_v4(stg + r * 128 + ((c ^ (r & 7)) << 4));
-      if (r < rows_left) *reinterpret_cast<uint4*>(dst + k * 4 * row_bytes) = x;
-    }
-  };
-  if (o_bf16 != nullptr) {
-#pragma unroll 1
-    for (int h = 0; h < D / 64; ++h) {
-      __syncwarp();
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t orr[32], pk[16];
-        tmem_ld_x32(tO + h * 64 + hh * 32, orr);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(value(orr[2 * e]), value(orr[2 * e + 1]));
-        stage4(4 * hh, pk);
-      }
-      __syncwarp();
-      drain(reinterpret_cast<uint8_t*>(o_bf16 + h * 64), row_stride * 2);
-    }
-  } else {
-#pragma unroll 1
-    for (int ch = 0; ch < D / 32; ++ch) {
-      uint32_t orr[32];
-      tmem_ld_x32(tO + ch * 32, orr);
-      __syncwarp();
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(value(orr[16 * hh + e]));
-        stage4(4 * hh, w);
-      }
-      __syncwarp();
-      drain(reinterpret_cast<uint8_t*>(o_f32 + ch * 32), row_stride * 4);
+      if (r < rows_left) *reinterpret_cast<uint4*>(dst + r * row_stride + h * 64 + c * 8) = x;
     }
   }
-  return !(bad == 0.f);
+  return !(bad[0] + bad[1] == 0.f);
 }
 
 // Recompute one output row with the whole warp, reading only the keys [j0, j1)
