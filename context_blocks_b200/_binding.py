@@ -328,20 +328,27 @@ def _refuse_rows(name, t, ndim, index):
     raise ValueError(f"{name} must be a {ndim}-d tensor with a contiguous last dimension")
 
 
-_bf16 = None
+class _Torch:
+    """torch and what of it the calls below need on every call, looked up on the
+    first one (importing this package alone does not import torch)."""
+
+    def __getattr__(self, name):
+        import torch
+        self.torch, self.bf16, self.f32, self.i32 = torch, torch.bfloat16, torch.float32, torch.int32
+        self.empty_like = torch.empty_like
+        return self.__dict__[name]
+
+
+_t = _Torch()
 
 
 def _check_rows(name, t, ndim, index=None):
     """A bf16 CUDA tensor (on device ``index``, where given) whose last
     dimension is contiguous; returns its device index.  On the way of every
     call: only cheap accessors."""
-    global _bf16
-    if _bf16 is None:
-        import torch
-        _bf16 = torch.bfloat16
     try:
         at = t.get_device()
-        if (t.dtype is _bf16 and at >= 0 and (index is None or at == index) and t.dim() == ndim
+        if (t.dtype is _t.bf16 and at >= 0 and (index is None or at == index) and t.dim() == ndim
                 and (t.stride(-1) == 1 or t.shape[-1] <= 1)):
             return at
     except AttributeError:
@@ -354,11 +361,12 @@ def _check_vector(name, t, dtype, shape, index):
     ``index``; None for None."""
     if t is None:
         return None
-    import torch
-    if (not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_contiguous()
-            or t.get_device() != index):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
 
 
 def attn_fwd_mod(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, slopes=None, causal: bool = False,
@@ -379,7 +387,6 @@ def attn_fwd_mod(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, s
     q's layout.  With very few query rows use ``attn_shared_prefix``, which
     splits the keys over the GPU.
     """
-    import torch
     index = _check_rows("q", q, 4)
     _check_rows("k", k, 4, index)
     _check_rows("v", v, 4, index)
@@ -392,28 +399,30 @@ def attn_fwd_mod(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, s
         if doc_offsets.dim() != 2 or doc_offsets.shape[1] < 2:
             raise ValueError("doc_offsets must be [B, n_docs + 1] with n_docs >= 1")
         n_docs = doc_offsets.shape[1] - 1
-    mod = ScoreMod(softcap, 1 if causal else 0, _check_vector("slopes", slopes, torch.float32, (Hq,), index), None,
-                   _check_vector("doc_offsets", doc_offsets, torch.int32, (B, n_docs + 1), index), n_docs,
+    mod = ScoreMod(softcap, 1 if causal else 0, _check_vector("slopes", slopes, _t.f32, (Hq,), index), None,
+                   _check_vector("doc_offsets", doc_offsets, _t.i32, (B, n_docs + 1), index), n_docs,
                    Nk - Nq if q_offset is None else q_offset)
     if prefix_lens is not None:
         shape = (B, n_docs) if n_docs else (B, 1) if prefix_lens.dim() == 2 else (B,)
-        mod.prefix_lens = _check_vector("prefix_lens", prefix_lens, torch.int32, shape, index)
-    if out is None or lse is None:
+        mod.prefix_lens = _check_vector("prefix_lens", prefix_lens, _t.i32, shape, index)
+    fresh = out is None
+    if fresh or lse is None:
         with _nullcontext if stream is None else _on_stream(stream, q.device):
             if out is None:
-                out = torch.empty_like(q)  # keeps a dense layout such as [B, Nq, Hq, d]
+                out = _t.empty_like(q)  # keeps a dense layout such as [B, Nq, Hq, d]
                 if out.stride(-1) != 1:
                     out = q.new_empty(q_shape)
             if lse is None:
-                lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
-    _check_rows("out", out, 4, index)
-    if out.shape != q_shape:
-        raise ValueError("out must have q's shape")
+                lse = q.new_empty((B, Hq, Nq), dtype=_t.f32)
+    if not fresh:
+        _check_rows("out", out, 4, index)
+        if out.shape != q_shape:
+            raise ValueError("out must have q's shape")
     strides = None
     if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()):
         strides = _Strides12(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *out.stride()[:3])
     rc = load_library().pa_attn_fwd_mod(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                         _check_vector("lse", lse, torch.float32, (B, Hq, Nq), index), B, Hq, Hkv, Nq,
+                                         _check_vector("lse", lse, _t.f32, (B, Hq, Nq), index), B, Hq, Hkv, Nq,
                                          Nk, d, strides, 1.0 / math.sqrt(d) if scale is None else scale,
                                          ctypes.byref(mod), _stream_handle(stream, index))
     if rc or check:
@@ -438,7 +447,6 @@ def attn_shared_prefix(q, k_prefix, v_prefix, k_tail, v_tail, tail_lens, scale: 
     ``shared_prefix_workspace_bytes``) is allocated when not given; two calls
     that may overlap on the GPU need one each.  Returns (o, lse).
     """
-    import torch
     index = _check_rows("q", q, 4)
     _check_rows("k_prefix", k_prefix, 3, index)
     _check_rows("v_prefix", v_prefix, 3, index)
@@ -453,22 +461,25 @@ def attn_shared_prefix(q, k_prefix, v_prefix, k_tail, v_tail, tail_lens, scale: 
             or Hq % Hkv):
         raise ValueError(f"shape mismatch: q {tuple(q.shape)}, prefix {tuple(k_prefix.shape)} and "
                          f"{tuple(v_prefix.shape)}, tail {tuple(k_tail.shape)} and {tuple(v_tail.shape)}")
-    lens = _check_vector("tail_lens", tail_lens, torch.int32, (B,), index)
-    sl = _check_vector("slopes", slopes, torch.float32, (Hq,), index)
+    lens = _check_vector("tail_lens", tail_lens, _t.i32, (B,), index)
+    sl = _check_vector("slopes", slopes, _t.f32, (Hq,), index)
     lib = load_library()
-    if out is None or lse is None or workspace is None:
+    fresh, own_space = out is None, workspace is None
+    if fresh or own_space or lse is None:
         with _nullcontext if stream is None else _on_stream(stream, q.device):
             if out is None:
-                out = torch.empty_like(q)
+                out = _t.empty_like(q)
             if lse is None:
-                lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
-            if workspace is None:
+                lse = q.new_empty((B, Hq, Nq), dtype=_t.f32)
+            if own_space:
                 # in bf16 elements of q: one allocation without a type to look up
                 workspace = q.new_empty((lib.pa_attn_shared_prefix_workspace(B, Hq, Hkv, Nq, Np, Nt, d) // 2,))
-    _check_rows("out", out, 4, index)
-    if out.shape != q_shape or not out.is_contiguous():
-        raise ValueError("out must be a contiguous tensor of q's shape")
-    if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
+    if not fresh:
+        _check_rows("out", out, 4, index)
+        if out.shape != q_shape or not out.is_contiguous():
+            raise ValueError("out must be a contiguous tensor of q's shape")
+    if not own_space and (not isinstance(workspace, _t.torch.Tensor) or workspace.get_device() != index
+                          or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous tensor on q's device")
     strides = None
     if not (k_prefix.is_contiguous() and v_prefix.is_contiguous() and k_tail.is_contiguous()
@@ -477,7 +488,7 @@ def attn_shared_prefix(q, k_prefix, v_prefix, k_tail, v_tail, tail_lens, scale: 
                              *v_tail.stride()[:3])
     rc = lib.pa_attn_shared_prefix(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_tail.data_ptr(),
                                    v_tail.data_ptr(), lens, out.data_ptr(),
-                                   _check_vector("lse", lse, torch.float32, (B, Hq, Nq), index), B, Hq, Hkv, Nq, Np,
+                                   _check_vector("lse", lse, _t.f32, (B, Hq, Nq), index), B, Hq, Hkv, Nq, Np,
                                    Nt, d, strides, 1.0 / math.sqrt(d) if scale is None else scale, softcap, sl,
                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                    _stream_handle(stream, index))
@@ -500,18 +511,17 @@ def gate_residual_norm(y, x, gate=None, post: str = "none", post_weight=None, no
     they are), weights [D] bf16; ``post`` and ``norm`` are "none", "rms" or
     "layer".  Returns (x_new, h); x_new has x's type and goes to ``x_out``, which
     may be x itself, h (bf16, None with norm="none") to ``out``."""
-    import torch
     index = _check_rows("y", y, 3)
     B, N, D = shape = y.shape
     if not y.is_contiguous():
         raise ValueError("y must be contiguous")
-    if (not isinstance(x, torch.Tensor) or x.dtype not in (torch.bfloat16, torch.float32) or x.shape != shape
+    if (not isinstance(x, _t.torch.Tensor) or x.dtype not in (_t.bf16, _t.f32) or x.shape != shape
             or not x.is_contiguous() or x.get_device() != index):
         raise ValueError("x must be a contiguous bfloat16 or float32 tensor of y's shape on its device")
     if post not in PA_NORM or norm not in PA_NORM:
         raise ValueError(f"post and norm must be one of {sorted(PA_NORM)} (got {post!r}, {norm!r})")
-    cfg = BlockNorm(PA_NORM[post], PA_NORM[norm], _check_vector("post_weight", post_weight, torch.bfloat16, (D,), index),
-                    _check_vector("norm_weight", norm_weight, torch.bfloat16, (D,), index), None, None, None, 0, 0, 0,
+    cfg = BlockNorm(PA_NORM[post], PA_NORM[norm], _check_vector("post_weight", post_weight, _t.bf16, (D,), index),
+                    _check_vector("norm_weight", norm_weight, _t.bf16, (D,), index), None, None, None, 0, 0, 0,
                     residual_scale, eps)
     for name, t in (("gate", gate), ("scale", scale), ("shift", shift)):
         if t is None:
@@ -526,9 +536,9 @@ def gate_residual_norm(y, x, gate=None, post: str = "none", post_weight=None, no
     if x_out is None or (out is None and norm != "none"):
         with _nullcontext if stream is None else _on_stream(stream, y.device):
             if x_out is None:
-                x_out = torch.empty_like(x)
+                x_out = _t.empty_like(x)
             if out is None and norm != "none":
-                out = torch.empty_like(y)
+                out = _t.empty_like(y)
     if x_out.dtype != x.dtype or x_out.shape != shape or not x_out.is_contiguous() or x_out.get_device() != index:
         raise ValueError("x_out must be a contiguous tensor of x's type and shape on its device")
     if out is not None:
@@ -537,7 +547,7 @@ def gate_residual_norm(y, x, gate=None, post: str = "none", post_weight=None, no
             raise ValueError("out must be a contiguous tensor of y's shape")
     rc = load_library().pa_gate_residual_norm(y.data_ptr(), x.data_ptr(), x_out.data_ptr(),
                                                None if out is None else out.data_ptr(), B, N, D,
-                                               1 if x.dtype == torch.float32 else 0, ctypes.byref(cfg),
+                                               1 if x.dtype == _t.f32 else 0, ctypes.byref(cfg),
                                                _stream_handle(stream, index))
     if rc or check:
         _check(rc, "pa_gate_residual_norm", check)

@@ -342,6 +342,20 @@ __global__ void __launch_bounds__(R::kThreads, 1)
     *abort_word = 0;
     fence_barrier_init();
   }
+  // The load warps reckon while the barriers and tensor memory are set up: all
+  // tail tiles under one K/V head, and the CTAs that take pairs.
+  int tails = 0, pair_ctas = 0;
+  if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+    for (int b0 = 0; b0 < plan.B; b0 += 128) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int b = b0 + u * 32 + lane;
+        if (b < plan.B) tails += Plan::tiles_of(plan.len(b));
+      }
+    }
+    tails = __reduce_add_sync(0xffffffffu, tails);
+    pair_ctas = plan.pair_ctas(tails);
+  }
   if (warp == kLoadWarp && lane == 0) {
     prefetch_tensormap(&tm_qp);
     prefetch_tensormap(&tm_kp);
@@ -462,17 +476,6 @@ __global__ void __launch_bounds__(R::kThreads, 1)
           ++idx;
         }
     };
-    // All tail tiles under one K/V head.
-    int tails = 0;
-    for (int b0 = 0; b0 < plan.B; b0 += 128) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int b = b0 + u * 32 + lane;
-        if (b < plan.B) tails += Plan::tiles_of(plan.len(b));
-      }
-    }
-    tails = __reduce_add_sync(0xffffffffu, tails);
-    const int pair_ctas = plan.pair_ctas(tails);
     if (static_cast<int>(blockIdx.x) < pair_ctas) {
       if (i == 0) {
         slot0 = 0, n_slots = kStages;
