@@ -11,11 +11,16 @@
 //
 // Work: an item is 256 query rows (two tiles of 128) of one (batch, head); only
 // the key tiles that some row of a tile sees are loaded, and a query tile takes
-// part only in those its own rows see.  Warps:
+// part only in those its own rows see.  The grid has a block for every item.  A
+// CTA works on its own block's item and then takes over blocks that have not
+// started (cluster launch control), one ahead: the longest items, the last query
+// rows under a causal mask, come first and the short ones fill up the end
+// (4096 causal keys, 24 heads: 111 us, 127 us with a fixed share a CTA).  Warps:
 //   0-3, 4-7   softmax of query tile 0 and 1, a row a thread (208 registers)
 //   8          tcgen05.mma issue      9   TMA loads (Q of the item, K/V ring)
 //   10         scheduler: the next item, its intervals' hull per query tile and
-//              the documents it spans, through a two-slot ring in shared memory
+//              the documents it spans, through a slot in shared memory that is
+//              free once all other warps have begun the item before
 //   11         idle (completes the register split's warpgroup)
 // Key tiles are walked from the last to the first: the nearest keys come
 // first, so a bias that falls with distance settles the row maximum at once
@@ -117,6 +122,31 @@ struct ItemSlot {
   int doc0, doc1;         // documents of the item's first and last row
 };
 
+// Cluster launch control: ask for a block of this grid that has not started, to
+// work on it here.  The answer (16 bytes) is written to `resp` and counted on
+// `bar`; no further request may follow one that came back empty.
+__device__ __forceinline__ void clc_request(uint32_t resp, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(resp),
+      "r"(bar)
+      : "memory");
+}
+
+// The block of an answer, or -1.
+__device__ __forceinline__ int clc_block(uint32_t resp) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+      "ld.shared.b128 r, [%1];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "mov.b32 %0, -1;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%0, y, z, w}, r;\n\t}\n"
+      : "=r"(x)
+      : "r"(resp)
+      : "memory");
+  return x;
+}
+
 template <int D, bool kWide>
 struct Layout {
   static constexpr int kBoxBytes = 128 * 128;
@@ -131,10 +161,12 @@ struct Layout {
   static constexpr int kSumOff = kStageOff + Roles<kWide>::kGroups * 4 * kStageWarpBytes;
   static constexpr int kBarOff = kSumOff + (kWide ? 2 * 2 * 2 * 128 * 4 : 0);
   // q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], p_part[2], p_full[2],
-  // o_full[2], drain, item_full[2], item_empty[2], swap[2][4 warps]
-  static constexpr int kNumBars = 2 + 2 * kStages + 8 + 1 + 4 + 8;
-  static constexpr int kItemOff = kBarOff + kNumBars * 8;
-  static constexpr int kTmemSlotOff = kItemOff + 2 * static_cast<int>(sizeof(ItemSlot));
+  // o_full[2], drain, item_full, item_empty, claim, swap[2][4 warps]
+  static constexpr int kNumBars = 2 + 2 * kStages + 8 + 1 + 3 + 8;
+  static constexpr int kClaimOff = kBarOff + kNumBars * 8;  // a claim's answer, 16 bytes
+  static_assert(kClaimOff % 16 == 0, "the answer's place must be 16-byte aligned");
+  static constexpr int kItemOff = kClaimOff + 16;
+  static constexpr int kTmemSlotOff = kItemOff + static_cast<int>(sizeof(ItemSlot));
   static constexpr int kAbortOff = kTmemSlotOff + 4;
   static constexpr int kBytes = kAbortOff + 4;
   // Never two CTAs an SM: each takes all of tensor memory.
@@ -166,10 +198,11 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
   const uint32_t bar_p_full0 = bars + 8 * (6 + 2 * kStages);
   const uint32_t bar_o_full0 = bars + 8 * (8 + 2 * kStages);
   const uint32_t bar_drain = bars + 8 * (10 + 2 * kStages);
-  const uint32_t bar_item_full0 = bars + 8 * (11 + 2 * kStages);
-  const uint32_t bar_item_empty0 = bars + 8 * (13 + 2 * kStages);
-  const uint32_t bar_swap0 = bars + 8 * (15 + 2 * kStages);  // + 8 * (4 * query tile + warp of the warpgroup)
-  volatile ItemSlot* slots = reinterpret_cast<volatile ItemSlot*>(gbase + L::kItemOff);
+  const uint32_t bar_item_full = bars + 8 * (11 + 2 * kStages);
+  const uint32_t bar_item_empty = bars + 8 * (12 + 2 * kStages);
+  const uint32_t bar_claim = bars + 8 * (13 + 2 * kStages);
+  const uint32_t bar_swap0 = bars + 8 * (14 + 2 * kStages);  // + 8 * (4 * query tile + warp of the warpgroup)
+  volatile ItemSlot* slot = reinterpret_cast<volatile ItemSlot*>(gbase + L::kItemOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + L::kTmemSlotOff);
   volatile int* abort_word = reinterpret_cast<volatile int*>(gbase + L::kAbortOff);
 
@@ -189,9 +222,10 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
       mbar_init(bar_p_part0 + 8 * i, 4);  // one arrival per softmax warp
       mbar_init(bar_p_full0 + 8 * i, 4);
       mbar_init(bar_o_full0 + 8 * i, 1);
-      mbar_init(bar_item_full0 + 8 * i, 1);
-      mbar_init(bar_item_empty0 + 8 * i, 4 * R::kGroups + 2);  // softmax warps, MMA, TMA
     }
+    mbar_init(bar_item_full, 1);
+    mbar_init(bar_item_empty, 4 * R::kGroups + 2);  // softmax warps, MMA, TMA
+    mbar_init(bar_claim, 1);
     mbar_init(bar_drain, 1);
     for (int u = 0; u < 8; ++u) mbar_init(bar_swap0 + 8 * u, 2);  // the two warps of the same rows
     *abort_word = 0;
@@ -215,20 +249,19 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
     const bool got = mbar_wait_hint(bar, parity, abort_word, p.status, kStatusTimeout, lim, kSuspendHintNs);
     return __all_sync(0xffffffffu, got);
   };
-  // The it-th item of this CTA, copied out of its slot; false at the end (or
+  // The it-th item of this CTA, copied out of the slot; false at the end (or
   // where a wait gave up, with `ok` cleared).
   auto next_item = [&](int it, ItemSlot& x, bool& ok) {
-    const int s = it & 1;
-    if (!wait_all(bar_item_full0 + 8 * s, (it >> 1) & 1)) {
+    if (!wait_all(bar_item_full, it & 1)) {
       ok = false;
       return false;
     }
-    x.item = slots[s].item;
-    x.first[0] = slots[s].first[0], x.first[1] = slots[s].first[1];
-    x.last[0] = slots[s].last[0], x.last[1] = slots[s].last[1];
-    x.doc0 = slots[s].doc0, x.doc1 = slots[s].doc1;
+    x.item = slot->item;
+    x.first[0] = slot->first[0], x.first[1] = slot->first[1];
+    x.last[0] = slot->last[0], x.last[1] = slot->last[1];
+    x.doc0 = slot->doc0, x.doc1 = slot->doc1;
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar_item_empty0 + 8 * s);
+    if (lane == 0) mbar_arrive(bar_item_empty);
     return x.item >= 0;
   };
   auto first_of = [](const ItemSlot& x, int i) { return i ? x.first[1] : x.first[0]; };
@@ -245,14 +278,29 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
   } else if (warp == R::kSched) {
     setmaxnreg_dec<R::kControlRegs>();
     // ----------------------------------------------------------- scheduler
-    int it = 0;
-    for (int item = blockIdx.x;; item += gridDim.x, ++it) {
-      const int s = it & 1;
-      if (!wait_all(bar_item_empty0 + 8 * s, ((it >> 1) & 1) ^ 1)) break;
-      if (item >= p.items) {
-        if (lane == 0) slots[s].item = -1;
+    const uint32_t answer = base + L::kClaimOff;
+    int item = static_cast<int>(blockIdx.x);
+    for (int it = 0;; ++it) {
+      if (!wait_all(bar_item_empty, (it & 1) ^ 1)) break;
+      if (it > 0) {
+        if (lane == 0) {
+          // The answer before has been read (by this warp) when it is written over.
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          mbar_arrive_expect_tx(bar_claim, 16);
+          clc_request(answer, bar_claim);
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar_item_full0 + 8 * s);
+        if (!wait_all(bar_claim, (it - 1) & 1)) {
+          // The answer still on its way lands before the CTA exits.
+          mbar_wait(bar_claim, (it - 1) & 1, nullptr, p.status, kStatusTimeout, lim);
+          break;
+        }
+        item = clc_block(answer);
+      }
+      if (item < 0) {
+        if (lane == 0) slot->item = -1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_item_full);
         break;
       }
       // Items run from the last query rows to the first: with a causal mask the
@@ -288,17 +336,17 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
         hi[i] = __reduce_max_sync(0xffffffffu, hi[i]);
       }
       if (lane == 0) {
-        slots[s].item = item;
+        slot->item = item;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          slots[s].first[i] = hi[i] > 0 ? lo[i] / kBN : 0;
-          slots[s].last[i] = hi[i] > 0 ? (hi[i] + kBN - 1) / kBN : 0;
+          slot->first[i] = hi[i] > 0 ? lo[i] / kBN : 0;
+          slot->last[i] = hi[i] > 0 ? (hi[i] + kBN - 1) / kBN : 0;
         }
-        slots[s].doc0 = doc0;
-        slots[s].doc1 = doc1;
+        slot->doc0 = doc0;
+        slot->doc1 = doc1;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar_item_full0 + 8 * s);
+      if (lane == 0) mbar_arrive(bar_item_full);
     }
   } else if (warp == R::kTma) {
     setmaxnreg_dec<R::kControlRegs>();

@@ -577,11 +577,12 @@ __global__ void __launch_bounds__(R::kThreads, 1)
     int g = 0;    // key tiles so far: phase of the P barriers (the same for both streams of a pair CTA)
     int q_used = 0;
     Piece x;
-    for (int it = 0; ok && next_piece(me, it, x, ok); ++it) {
-      const bool both = x.kind == kPair;
-      if (both && me == 1) continue;  // warp 8 issues for both streams
-      const int slot0 = both ? 0 : me * kHalf, n_slots = both ? kStages : kHalf;
-      const int i0 = both ? 0 : me, i1 = both ? 2 : me + 1;
+    // A piece, for the streams [i0, i1): constants, see attn_mod.cuh.
+    auto work = [&](auto lo, auto hi) {
+      constexpr int i0 = decltype(lo)::value, i1 = decltype(hi)::value;
+      constexpr bool both = i1 - i0 == 2;
+      const int slot0 = both ? 0 : me * kHalf;
+      constexpr int n_slots = both ? kStages : kHalf;
       auto take = [&](int& slot) {
         slot = slot0 + idx % n_slots;
         if (!wait_all(bar_kv_full0 + 8 * slot, (idx / n_slots) & 1)) return false;
@@ -590,10 +591,14 @@ __global__ void __launch_bounds__(R::kThreads, 1)
         return true;
       };
       int slot_k = 0, slot_v = 0;
-      if (!wait_all(bar_q_full0 + 8 * me, q_used & 1) || !take(slot_k)) break;
+      if (!wait_all(bar_q_full0 + 8 * me, q_used & 1) || !take(slot_k)) {
+        ok = false;
+        return;
+      }
       ++q_used;
       tc_fence_after();
       if (leader) {
+#pragma unroll
         for (int i = i0; i < i1; ++i) issue_qk(i, slot_k);
         umma_commit(bar_kv_empty0 + 8 * slot_k);
         if (x.t1 - 1 == x.t0) umma_commit(bar_q_empty0 + 8 * me);
@@ -619,7 +624,9 @@ __global__ void __launch_bounds__(R::kThreads, 1)
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
         }
-        for (int i = i0; i < i1 && ok; ++i) {
+#pragma unroll
+        for (int i = i0; i < i1; ++i) {
+          if (!ok) break;
           if (!wait_all(bar_p_part0 + 8 * i, g & 1)) {
             ok = false;
             break;
@@ -654,6 +661,15 @@ __global__ void __launch_bounds__(R::kThreads, 1)
           }
         }
       }
+    };
+    using std::integral_constant;
+    for (int it = 0; ok && next_piece(me, it, x, ok); ++it) {
+      if (x.kind != kPair && me == 0)
+        work(integral_constant<int, 0>{}, integral_constant<int, 1>{});
+      else if (x.kind != kPair)
+        work(integral_constant<int, 1>{}, integral_constant<int, 2>{});
+      else if (me == 0)  // warp 8 issues for both streams
+        work(integral_constant<int, 0>{}, integral_constant<int, 2>{});
     }
     // Every MMA issued completes before tensor memory is freed.
     if (leader) umma_commit(bar_drain0 + 8 * me);

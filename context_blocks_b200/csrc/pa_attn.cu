@@ -516,8 +516,7 @@ int launch_mod(DeviceState* st, const CUtensorMap& tq, const CUtensorMap& tk, co
   bool* const ready = kWide ? &st->wide_attr[D == 128] : &st->mod_attr[4 * (D == 128) + 2 * kCap + kBias];
   const int rc = ready_kernel(kern, ready, L::kAllocBytes, R::kLaunchRegs, "modified-score forward");
   if (rc != PA_OK) return rc;
-  const unsigned grid = static_cast<unsigned>(std::min(prm.items, st->sm_count));
-  kern<<<grid, R::kThreads, L::kAllocBytes, stream>>>(tq, tk, tv, prm);
+  kern<<<static_cast<unsigned>(prm.items), R::kThreads, L::kAllocBytes, stream>>>(tq, tk, tv, prm);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "attn_mod launch");
   return PA_OK;
