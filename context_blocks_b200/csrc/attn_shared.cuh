@@ -10,12 +10,17 @@
 // Work.  A segment is the keys one row tile has to go over: the prefix under one
 // K/V head, or one request's tail under one K/V head.  Two row tiles over the
 // same prefix make a pair, which shares its K and V tiles; what is left (the
-// prefix under an odd row tile, and the tails) is single.  Pairs and singles
-// each form a line of key tiles (128 keys), cut into equal parts: a pair part
-// for each CTA of the first kind, a single part for each of the two streams (a
-// softmax warpgroup, its MMA and its load warp) of the others, so that every SM
-// gets the same share whatever the lengths are, without counters and without
-// host knowledge of them.  The part of a segment that falls to one part of the
+// prefix under an odd row tile, and the tails) is single.  The singles form a line
+// of key tiles (128 keys), cut into equal parts, one for each of the two streams
+// (a softmax warpgroup, its MMA and its load warp) of the CTAs that take singles.
+// The other CTAs take pairs, as many CTAs a pair: CTA c has pair c mod (pairs), and
+// the prefix, cut into equal parts, part c / (pairs) of it, so that the CTAs of
+// one part read the same tiles at the same time and HBM gives them once (with
+// one line of all pairs the same tile was read at two far times, and tails
+// streaming through L2 drove it out in between, by chance: 100 to 130 us with
+// neighbouring numbers of CTAs, where this takes 109 to 113).
+// Every SM gets the same share whatever the lengths are, without counters and
+// without host knowledge of them.  The part of a segment that falls to one part of the
 // line is a piece; segment + part is another number for every piece, since both
 // only grow along the line, and names the place of its partial results in the
 // caller's workspace: normalised fp32 O rows and their LSE (base 2).
@@ -53,9 +58,11 @@ using R = Roles<false>;  // warps and registers of the single-warpgroup kernel
 constexpr int kMaxCtas = 160;  // sizes the workspace; the grid is one CTA an SM, at most this many
 constexpr int kMergeWarps = 8;
 constexpr int kLoadWarp = 9;   // + stream
-// Cost of a pair's key tile over a single's, in quarters: how the CTAs are
-// dealt to the two kinds.
-constexpr int kPairCost4 = 8;
+// What a pair's key tile, a single's and a tail costs, in parts of one another:
+// how the CTAs are dealt to the two kinds.  From the shares of CTAs that were
+// fastest for 128 requests on 32768 keys: with tails of one key tile
+// 1.25 single tiles a pair tile, with four 2, with eight 2.2.
+constexpr int kPairCost = 15, kSingleCost = 6, kTailCost = 6;
 
 // A line of n units cut into `parts` parts, none empty, sizes differing by one.
 struct Cut {
@@ -80,19 +87,25 @@ struct Plan {
   __host__ __device__ int pairs() const { return row_tiles / 2; }
   __host__ __device__ bool odd() const { return (row_tiles & 1) != 0; }
   __host__ __device__ int pair_units() const { return Hkv * pairs() * prefix_tiles; }
+  // Pairs side by side, lane l of them taken by the CTAs c with c mod lanes = l;
+  // with more pairs than CTAs a lane has several, l, l + lanes, ..
+  __host__ __device__ int lanes(int pair_ctas) const { return pairs() < pair_ctas ? pairs() : pair_ctas; }
+  __host__ __device__ int lane_pairs(int lanes, int l) const { return (pairs() - l + lanes - 1) / lanes; }
   __host__ __device__ int odd_units() const { return odd() ? Hkv * prefix_tiles : 0; }
   // Copies of a row tile's rows.
   __host__ __device__ static int copies(int n) { return n <= 32 ? 4 : n <= 64 ? 2 : 1; }
   __device__ int len(int b) const { return min(max(__ldg(tail_lens + b), 0), Nt); }
   __device__ static int tiles_of(int keys) { return (keys + kBN - 1) / kBN; }
-  // CTAs that take pairs, given the tail tiles (under one K/V head) of all
-  // requests.
-  __device__ int pair_ctas(int tails) const {
-    const long long p = static_cast<long long>(pair_units()) * kPairCost4;
-    const long long s = (odd_units() + static_cast<long long>(tails) * Hkv) * 4;
+  // CTAs that take pairs, given the tail tiles (under one K/V head) of all requests
+  // and the number of requests that have any.
+  __device__ int pair_ctas(int tiles, int tails) const {
+    const long long p = static_cast<long long>(pair_units()) * kPairCost;
+    const long long s = odd_units() * static_cast<long long>(kSingleCost) +
+                        (tiles * static_cast<long long>(kSingleCost) + tails * kTailCost) * Hkv;
     if (p == 0) return 0;
-    if (s == 0) return ctas;
-    return static_cast<int>(min(max((ctas * p + (p + s) / 2) / (p + s), 1ll), ctas - 1ll));
+    if (s == 0) return ctas <= pairs() ? ctas : ctas - ctas % pairs();
+    const int n = static_cast<int>(min(max((ctas * p + (p + s) / 2) / (p + s), 1ll), ctas - 1ll));
+    return n <= pairs() ? n : n - n % pairs();  // as many for every pair
   }
 };
 
@@ -102,7 +115,7 @@ struct Params {
   const __nv_bfloat16* kt;
   const __nv_bfloat16* vt;
   long long kt_s[3], vt_s[3];  // tail strides: batch, head, row (elements)
-  float* pair_o;               // [(Hkv * pairs + ctas) * 2][tile_rows][D]
+  float* pair_o;               // [((segments of a lane + parts) * lanes) * 2][tile_rows][D]
   float2* pair_ml;
   float* odd_o;                // [(Hkv + 2 * ctas) * copies][tile_rows][D]
   float2* odd_ml;
@@ -346,15 +359,18 @@ __global__ void __launch_bounds__(R::kThreads, 1)
   // tail tiles under one K/V head, and the CTAs that take pairs.
   int tails = 0, pair_ctas = 0;
   if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+    int some = 0;
     for (int b0 = 0; b0 < plan.B; b0 += 128) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int b = b0 + u * 32 + lane;
-        if (b < plan.B) tails += Plan::tiles_of(plan.len(b));
+        const int n = b < plan.B ? Plan::tiles_of(plan.len(b)) : 0;
+        tails += n;
+        some += n > 0;
       }
     }
     tails = __reduce_add_sync(0xffffffffu, tails);
-    pair_ctas = plan.pair_ctas(tails);
+    pair_ctas = plan.pair_ctas(tails, __reduce_add_sync(0xffffffffu, some));
   }
   if (warp == kLoadWarp && lane == 0) {
     prefetch_tensormap(&tm_qp);
@@ -479,13 +495,13 @@ __global__ void __launch_bounds__(R::kThreads, 1)
     if (static_cast<int>(blockIdx.x) < pair_ctas) {
       if (i == 0) {
         slot0 = 0, n_slots = kStages;
-        const Cut cut(plan.pair_units(), pair_ctas);
-        const int c = blockIdx.x;
+        const int lanes = plan.lanes(pair_ctas), l = blockIdx.x % lanes, c = blockIdx.x / lanes;
+        const Cut cut(plan.lane_pairs(lanes, l) * plan.Hkv * plan.prefix_tiles, pair_ctas / lanes);
         const int u0 = c < cut.parts ? cut.begin(c) : 0, u1 = c < cut.parts ? cut.begin(c + 1) : 0;
         for (int u = u0; u < u1 && ok;) {
           const int s = u / plan.prefix_tiles, t0 = u - s * plan.prefix_tiles;
           const int t1 = min(plan.prefix_tiles, t0 + u1 - u);
-          run(kPair, s / plan.pairs(), 2 * (s % plan.pairs()) * plan.tile_reqs, t0, t1, s + c, plan.Np);
+          run(kPair, s % plan.Hkv, 2 * (l + s / plan.Hkv * lanes) * plan.tile_reqs, t0, t1, (s + c) * lanes + l, plan.Np);
           u += t1 - t0;
         }
         if (ok) publish(kEnd, 0, 0, 0, 0, 0, 0, true);
@@ -810,7 +826,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
   const int req = blockIdx.x / plan.Hkv, hk = blockIdx.x % plan.Hkv;
 
   // Tail tiles (under one K/V head) of all requests, and of those before req.
-  int all = 0, before = 0;
+  int all = 0, before = 0, some = 0;
   for (int b0 = 0; b0 < plan.B; b0 += 128) {
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -818,6 +834,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
       if (b >= plan.B) continue;
       const int n = Plan::tiles_of(plan.len(b));
       all += n;
+      some += n > 0;
       if (b < req) before += n;
       if (blockIdx.x == 0 && warp == 0 && __ldg(plan.tail_lens + b) != plan.len(b))
         atomicCAS(p.status, 0, kStatusBadInput);
@@ -825,19 +842,23 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
   }
   all = __reduce_add_sync(0xffffffffu, all);
   before = __reduce_add_sync(0xffffffffu, before);
+  some = __reduce_add_sync(0xffffffffu, some);
 
   // Parts [p0, p1) of the pairs' or the singles' line hold the prefix under this
   // row tile, [t0, t1) of the singles' the tail.
   const int n_tail = Plan::tiles_of(plan.len(req));
-  const int pair_ctas = plan.pair_ctas(all);
+  const int pair_ctas = plan.pair_ctas(all, some);
   const int mt = req / plan.tile_reqs;
   const bool pair = mt < 2 * plan.pairs();
   const int copies_p = pair ? 1 : Plan::copies(plan.tile_rows()), copies_t = Plan::copies(plan.rows);
-  const int seg_p = pair ? hk * plan.pairs() + mt / 2 : hk, seg_t = req * plan.Hkv + hk;
+  // The prefix under this row tile: its segment on the line of its pair's lane, or
+  // on the singles'.
+  const int lanes = pair ? plan.lanes(pair_ctas) : 1, l = pair ? mt / 2 % lanes : 0;
+  const int seg_p = pair ? mt / 2 / lanes * plan.Hkv + hk : hk, seg_t = req * plan.Hkv + hk;
   const Cut singles(plan.odd_units() + all * plan.Hkv, 2 * (plan.ctas - pair_ctas));
   int p0 = 0, p1 = 0, t0 = 0, t1 = 0;
   if (plan.row_tiles > 0) {
-    const Cut pairs(plan.pair_units(), pair_ctas);
+    const Cut pairs(pair ? plan.lane_pairs(lanes, l) * plan.Hkv * plan.prefix_tiles : 1, pair ? pair_ctas / lanes : 1);
     const Cut& cut = pair ? pairs : singles;
     p0 = cut.holder(seg_p * plan.prefix_tiles);
     p1 = cut.holder((seg_p + 1) * plan.prefix_tiles - 1) + 1;
@@ -870,7 +891,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
       float2 my = make_float2(-INFINITY, 0.f);  // m = -inf, l = 0: a part that saw nothing
       if (k < n_parts) {
         if (k < n_p) {
-          const int slot = pair ? 2 * (seg_p + p0 + k) + (mt & 1) : (seg_p + p0) * copies_p + k;
+          const int slot =
+              pair ? 2 * ((seg_p + p0 + k) * lanes + l) + (mt & 1) : (seg_p + p0) * copies_p + k;
           const size_t row = static_cast<size_t>(slot) * plan.tile_rows() + (req % plan.tile_reqs) * plan.rows + rr;
           my = __ldcg(p_ml + row);
           src = p_o + row * D;

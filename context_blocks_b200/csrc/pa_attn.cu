@@ -601,7 +601,8 @@ SharedWorkspace shared_workspace(const pa::shared::Plan& plan, int d) {
   using pa::shared::kMaxCtas;
   auto up = [](uint64_t n) { return (n + 255) & ~255ull; };
   const uint64_t rows = plan.rows, tile = plan.tile_rows();
-  const uint64_t pair = plan.pairs() > 0 ? (static_cast<uint64_t>(plan.Hkv) * plan.pairs() + kMaxCtas) * 2 * tile : 0;
+  // (segments of a lane + parts) * lanes, for any number of lanes up to the pairs.
+  const uint64_t pair = plan.pairs() > 0 ? (2ull * plan.Hkv * plan.pairs() + kMaxCtas) * 2 * tile : 0;
   const uint64_t odd = plan.odd() ? (plan.Hkv + 2ull * kMaxCtas) * plan.copies(plan.tile_rows()) * tile : 0;
   const uint64_t tail =
       plan.Nt > 0 ? (static_cast<uint64_t>(plan.B) * plan.Hkv + 2ull * kMaxCtas) * plan.copies(plan.rows) * rows : 0;
