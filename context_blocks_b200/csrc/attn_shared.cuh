@@ -853,12 +853,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
   const int copies_p = pair ? 1 : Plan::copies(plan.tile_rows()), copies_t = Plan::copies(plan.rows);
   // The prefix under this row tile: its segment on the line of its pair's lane, or
   // on the singles'.
-  const int lanes = pair ? plan.lanes(pair_ctas) : 1, l = pair ? mt / 2 % lanes : 0;
+  const int lanes = pair ? plan.lanes(pair_ctas) : 1, my_lane = pair ? mt / 2 % lanes : 0;
   const int seg_p = pair ? mt / 2 / lanes * plan.Hkv + hk : hk, seg_t = req * plan.Hkv + hk;
   const Cut singles(plan.odd_units() + all * plan.Hkv, 2 * (plan.ctas - pair_ctas));
   int p0 = 0, p1 = 0, t0 = 0, t1 = 0;
   if (plan.row_tiles > 0) {
-    const Cut pairs(pair ? plan.lane_pairs(lanes, l) * plan.Hkv * plan.prefix_tiles : 1, pair ? pair_ctas / lanes : 1);
+    const Cut pairs(pair ? plan.lane_pairs(lanes, my_lane) * plan.Hkv * plan.prefix_tiles : 1,
+                    pair ? pair_ctas / lanes : 1);
     const Cut& cut = pair ? pairs : singles;
     p0 = cut.holder(seg_p * plan.prefix_tiles);
     p1 = cut.holder((seg_p + 1) * plan.prefix_tiles - 1) + 1;
@@ -892,7 +893,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
       if (k < n_parts) {
         if (k < n_p) {
           const int slot =
-              pair ? 2 * ((seg_p + p0 + k) * lanes + l) + (mt & 1) : (seg_p + p0) * copies_p + k;
+              pair ? 2 * ((seg_p + p0 + k) * lanes + my_lane) + (mt & 1) : (seg_p + p0) * copies_p + k;
           const size_t row = static_cast<size_t>(slot) * plan.tile_rows() + (req % plan.tile_reqs) * plan.rows + rr;
           my = __ldcg(p_ml + row);
           src = p_o + row * D;

@@ -483,12 +483,20 @@ int check_scores(int B, int Hq, int Hkv, int Nq, int d, float scale, float softc
   if (Hq % Hkv) return fail(PA_ERR_INVALID_ARG, "Hq must be a multiple of Hkv (got %d, %d)", Hq, Hkv);
   if (Nq < 0) return fail(PA_ERR_INVALID_ARG, "Nq must be >= 0 (got %d)", Nq);
   if (!std::isfinite(scale) || !(scale > 0.f)) return fail(PA_ERR_INVALID_ARG, "scale must be finite and > 0");
-  if (!std::isfinite(softcap) || softcap < 0.f)
-    return fail(PA_ERR_INVALID_ARG, "softcap must be finite and >= 0 (0: no cap)");
+  // Between these, no factor of the cap over- or underflows fp32.
+  if (!(softcap == 0.f || (softcap >= 1e-15f && softcap <= 1e15f && scale / softcap >= 1e-25f && scale / softcap <= 1e25f)))
+    return fail(PA_ERR_INVALID_ARG, "softcap must be 0 (no cap) or in [1e-15, 1e15], and scale / softcap in [1e-25, 1e25]");
   if (d != 64 && d != 128) return fail(PA_ERR_UNSUPPORTED, "d must be 64 or 128 (got %d)", d);
   if (static_cast<long long>(B) * Hq > 65535) return fail(PA_ERR_UNSUPPORTED, "B*Hq must be <= 65535");
   if (slopes && !aligned(slopes, 4)) return fail(PA_ERR_MISALIGNED, "slopes must be 4-byte aligned");
   return PA_OK;
+}
+
+// Limit of a wait in the modified-score kernels, where a warp may wait while
+// another goes over all the keys: the library's limit, and 20 us (ten times
+// what one takes) for every key tile.
+unsigned long long wait_limit_ns(long long key_tiles) {
+  return g_wait_limit_ns.load(std::memory_order_relaxed) + 20000ull * static_cast<unsigned long long>(key_tiles);
 }
 
 pa::mod::ScoreMod score_mod(float scale, float softcap, const float* slopes) {
@@ -740,7 +748,7 @@ int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_pre
   prm.tail_ml = reinterpret_cast<float2*>(w + ws.tail_ml);
   prm.sm = score_mod(scale, softcap, slopes);
   prm.status = st->status;
-  prm.timeout_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  prm.timeout_ns = wait_limit_ns(plan.prefix_tiles + (Nt + pa::kBN - 1) / pa::kBN);
   return by_mod(d, softcap > 0.f, slopes != nullptr, [&](auto dd, auto cap, auto bias) {
     return launch_shared<decltype(dd)::value, decltype(cap)::value, decltype(bias)::value>(
         st, maps, prm, o, lse, static_cast<cudaStream_t>(stream));
@@ -821,7 +829,7 @@ int pa_attn_fwd_mod(const void* q, const void* k, const void* v, void* o, float*
   prm.n_docs = n_docs;
   prm.sm = score_mod(scale, mod->softcap, mod->slopes);
   prm.status = st->status;
-  prm.timeout_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  prm.timeout_ns = wait_limit_ns((Nk + pa::kBN - 1) / pa::kBN);
   return by_mod(d, mod->softcap > 0.f, mod->slopes != nullptr, [&](auto dd, auto cap, auto bias) {
     return launch_mod<decltype(dd)::value, decltype(cap)::value, decltype(bias)::value>(
         st, tq, tk, tv, prm, static_cast<cudaStream_t>(stream));

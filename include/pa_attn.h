@@ -255,7 +255,8 @@ int pa_attn_merge(const void* o_parts, const float* lse_parts, int n_parts, void
  * structure is plain, unmasked attention.
  */
 typedef struct pa_score_mod {
-  float softcap;          /* c > 0: s <- c * tanh(s / c); 0: no cap */
+  float softcap;          /* c > 0: s <- c * tanh(s / c); 0: no cap (1e-15 <= c <= 1e15 and
+                             1e-25 <= scale / c <= 1e25) */
   int causal;             /* non-zero: a row sees no key behind its own position,
                              those of its prefix apart */
   const float* slopes;    /* [Hq] fp32, device, finite: s <- s - slopes[h] * |p_i - j|; or NULL */
@@ -480,7 +481,9 @@ int pa_selftest_timeout(int limit_us, void* stream);
 /*
  * Limit of every device-side barrier wait, in milliseconds (1 .. 600000;
  * default 5000), for launches made after the call, process-wide.  A wait that
- * makes no progress for this long gives up and reports PA_ERR_TIMEOUT.  Raise
+ * makes no progress for this long gives up and reports PA_ERR_TIMEOUT (in
+ * pa_attn_fwd_mod and pa_attn_shared_prefix, where a warp may wait while another
+ * goes over all the keys, after 20 us more for every 128 keys).  Raise
  * it where the GPU is time-sliced among many processes and a kernel may be
  * held off the GPU for long stretches.  Returns PA_OK or PA_ERR_INVALID_ARG.
  */

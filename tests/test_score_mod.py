@@ -154,7 +154,8 @@ def test_many_items_and_long_keys():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf"), 3e38])
-@pytest.mark.parametrize("kw", [dict(causal=True), dict(causal=True, slopes=True, softcap=20.0)], ids=str)
+@pytest.mark.parametrize("kw", [dict(causal=True), dict(causal=True, softcap=20.0),
+                                dict(causal=True, slopes=True, softcap=20.0)], ids=str)
 def test_hidden_keys_do_not_matter(bad, kw):
     """NaN, Inf and the type's largest values in keys and values that a row does
     not see leave the row as it is: behind the last document, and one document's
@@ -174,6 +175,49 @@ def test_hidden_keys_do_not_matter(bad, kw):
     assert torch.isfinite(o2[:, :, rows]).all()
     # recomputed rows do not round their weights to bf16: both are 2^-8 from exact
     assert (o2[:, :, rows].float() - o[:, :, rows].float()).abs().max() <= 2.0 ** -6 * float(v.abs().max())
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Calls that overlap on the GPU share nothing."""
+    ops = [(_rand((1, 8, 2000, 64), 10 * i), _rand((1, 8, 2000, 64), 10 * i + 1), _rand((1, 8, 2000, 64), 10 * i + 2))
+           for i in range(2)]
+    want = [pa.attn_fwd_mod(*o, causal=True, softcap=10.0) for o in ops]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ops]
+    got = [[pa.attn_fwd_mod(*o, causal=True, softcap=10.0, stream=s) for _ in range(5)] for o, s in zip(ops, streams)]
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for o, lse in g:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+    assert pa.poll_device_status() == pa.PA_OK
+
+
+@pytest.mark.gpu
+def test_long_keys_with_a_short_wait_limit():
+    """A warp that waits while another works through a long item is not taken
+    for one that is stuck: one query tile sees the last key only, the other all
+    200 000."""
+    pa.set_wait_limit_ms(1)
+    try:
+        q, k, v = _rand((1, 1, 256, 64), 1), _rand((1, 1, 200000, 64), 2), _rand((1, 1, 200000, 64), 3)
+        docs = torch.tensor([[0, 199872, 199873]], dtype=torch.int32, device="cuda")
+        o, lse = pa.attn_fwd_mod(q, k, v, q_offset=199872 - 128, doc_offsets=docs, check=True)
+        assert torch.isfinite(o[:, :, :129]).all() and torch.equal(o[:, :, 128], v[:, :, 199872])
+        assert (o[:, :, 129:] == 0).all()
+    finally:
+        pa.set_wait_limit_ms(5000)
+
+
+@pytest.mark.gpu
+def test_offsets_that_decrease_do_no_harm():
+    """Undefined results, as documented, but no fault and no stuck wait."""
+    q, k, v = _rand((2, 2, 600, 64), 1), _rand((2, 2, 600, 64), 2), _rand((2, 2, 600, 64), 3)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for _ in range(5):
+        docs = torch.randint(-1000, 2000, (2, 9), generator=g, device="cuda", dtype=torch.int32)
+        lens = torch.randint(-(1 << 31), (1 << 31) - 1, (2, 8), generator=g, device="cuda", dtype=torch.int32)
+        pa.attn_fwd_mod(q, k, v, causal=True, doc_offsets=docs, prefix_lens=lens, check=True)
 
 
 @pytest.mark.gpu
@@ -241,7 +285,8 @@ A, MB = 1 << 20, 1 << 24
     (dict(Hkv=3), B.PA_ERR_INVALID_ARG), (dict(Hkv=0), B.PA_ERR_INVALID_ARG), (dict(Nk=0), B.PA_ERR_INVALID_ARG),
     (dict(Nq=-1), B.PA_ERR_INVALID_ARG), (dict(d=96), B.PA_ERR_UNSUPPORTED), (dict(Bn=40000), B.PA_ERR_UNSUPPORTED),
     (dict(Nk=(1 << 30) + 1), B.PA_ERR_UNSUPPORTED), (dict(softcap=-1.0), B.PA_ERR_INVALID_ARG),
-    (dict(softcap=math.inf), B.PA_ERR_INVALID_ARG), (dict(softcap=math.nan), B.PA_ERR_INVALID_ARG),
+    (dict(softcap=math.inf), B.PA_ERR_INVALID_ARG), (dict(softcap=1e-20), B.PA_ERR_INVALID_ARG),
+    (dict(softcap=1e20), B.PA_ERR_INVALID_ARG), (dict(softcap=1e14, scale=1e-20), B.PA_ERR_INVALID_ARG), (dict(softcap=math.nan), B.PA_ERR_INVALID_ARG),
     (dict(scale=0.0), B.PA_ERR_INVALID_ARG), (dict(prefix=A), B.PA_ERR_INVALID_ARG),
     (dict(docs=A), B.PA_ERR_INVALID_ARG), (dict(docs=A + 2, n_docs=1), B.PA_ERR_MISALIGNED),
     (dict(slopes=A + 1), B.PA_ERR_MISALIGNED), (dict(k=A + MB + 8), B.PA_ERR_MISALIGNED),

@@ -66,6 +66,44 @@ def test_row_tiles(Bn, G, Nq):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kw", [dict(), dict(softcap=4.0), dict(softcap=60.0), dict(slopes=True),
+                                dict(softcap=4.0, slopes=True)], ids=str)
+@pytest.mark.parametrize("Bn,G", [(40, 4), (70, 4), (100, 7)])
+def test_pairs_of_row_tiles(Bn, G, kw):
+    """Two row tiles, five (two pairs and an odd one), six; several key tiles."""
+    _case(Bn, 2 * G, 2, 1, 900, 70, 128, [(7 * b) % 71 for b in range(Bn)], seed=16, **kw)
+
+
+@pytest.mark.gpu
+def test_more_pairs_than_ctas():
+    """300 row tiles of 128 rows: every CTA has a pair or more to itself.  All rows
+    see the whole prefix, so the unmasked forward is the reference."""
+    q, kp, vp = _rand((300, 8, 16, 64), 1, 2.0), _rand((1, 300, 64), 2), _rand((1, 300, 64), 3)
+    none = torch.zeros((300, 1, 0, 64), dtype=torch.bfloat16, device="cuda")
+    o, lse = pa.attn_shared_prefix(q, kp, vp, none, none, torch.zeros(300, dtype=torch.int32, device="cuda"), check=True)
+    o2, lse2 = pa.attn_fwd(q.view(1, 1, -1, 64), kp[None], vp[None])
+    assert (lse.view(-1) - lse2.view(-1)).abs().max() <= LSE_ABS
+    assert (o.view(-1, 64).float() - o2.view(-1, 64).float()).abs().max() <= 2.0 ** -6 * float(vp.abs().max())
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Calls that overlap on the GPU, each with a workspace of its own."""
+    cases = [(_rand((20, 4, 1, 64), 10 * i, 2.0), *(_rand((2, 3000, 64), 10 * i + j) for j in (1, 2)),
+              *(_rand((20, 2, 300, 64), 10 * i + j) for j in (3, 4)),
+              torch.tensor([(31 * b) % 301 for b in range(20)], dtype=torch.int32, device="cuda")) for i in range(2)]
+    want = [pa.attn_shared_prefix(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[pa.attn_shared_prefix(*c, stream=s) for _ in range(5)] for c, s in zip(cases, streams)]
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for o, lse in g:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+    assert pa.poll_device_status() == pa.PA_OK
+
+
+@pytest.mark.gpu
 def test_long_keys_over_many_ctas():
     """Few rows, long keys: every segment is cut over several CTAs.  Against the
     package's unmasked attention over the same keys."""
@@ -205,7 +243,7 @@ A, MB = 1 << 20, 1 << 24
     (dict(kt=A + 3 * MB + 8), B.PA_ERR_MISALIGNED), (dict(lens=A + 5 * MB + 2), B.PA_ERR_MISALIGNED),
     (dict(Hkv=3), B.PA_ERR_INVALID_ARG), (dict(Np=-1), B.PA_ERR_INVALID_ARG), (dict(Nt=-1), B.PA_ERR_INVALID_ARG),
     (dict(Nq=65), B.PA_ERR_UNSUPPORTED), (dict(d=32), B.PA_ERR_UNSUPPORTED), (dict(Np=1 << 30), B.PA_ERR_UNSUPPORTED),
-    (dict(Bn=20000), B.PA_ERR_UNSUPPORTED), (dict(cap=-1.0), B.PA_ERR_INVALID_ARG),
+    (dict(Bn=20000), B.PA_ERR_UNSUPPORTED), (dict(cap=-1.0), B.PA_ERR_INVALID_ARG), (dict(cap=1e-20), B.PA_ERR_INVALID_ARG),
     (dict(slopes=A + 1), B.PA_ERR_MISALIGNED), (dict(o=A), B.PA_ERR_INVALID_ARG), (dict(ws=A + MB), B.PA_ERR_INVALID_ARG),
     (dict(strides=[1024, 0, 1024, 128, 2048, 1024, 128, 2048, 1024, 128]), B.PA_ERR_INVALID_ARG),
     (dict(strides=[1024, 128, 1024, 128, 2048, 1024, 132, 2048, 1024, 128]), B.PA_ERR_MISALIGNED),
