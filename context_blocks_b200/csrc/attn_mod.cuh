@@ -155,7 +155,7 @@ struct Layout {
   static constexpr int kQOff = 0;
   static constexpr int kRingOff = kQOff + kQTiles * kTileBytes;
   static constexpr int kStageOff = kRingOff + kStages * kTileBytes;
-  static constexpr int kStageWarpBytes = kWide ? 32 * 32 : 32 * 128;
+  static constexpr int kStageWarpBytes = kWide ? 32 * 32 : 32 * 64;
   // Wide: what the two threads of a row tell each other at the end, the sums of
   // their weights; [two slots in turn][query tile][key half][row].
   static constexpr int kSumOff = kStageOff + Roles<kWide>::kGroups * 4 * kStageWarpBytes;

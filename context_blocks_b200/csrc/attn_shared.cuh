@@ -181,7 +181,7 @@ __device__ __forceinline__ void softmax_share(uint32_t tS, uint32_t tO, int kq, 
     for (int e = 0; e < kKeys / 2; ++e) x[e] = f2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
   }
   if constexpr (kCap) cap_scores<kKeys / 2>(x, sm, 0.f);
-  if constexpr (kBias) bias_scores<kKeys / 2, !kCap>(x, sm.scale_log2, slope2, dist0 - static_cast<float>(e0));
+  if constexpr (kBias) bias_scores<kKeys / 2, !kCap>(x, sm.scale_log2, slope2, dist0 - static_cast<float>(e0), 0, b - e0);
   if (__any_sync(0xffffffffu, b < e0 + kKeys)) hide<kKeys / 2>(x, 0, b - e0);
   float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll

@@ -69,6 +69,13 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
+// max(|a|, |b|, |c|), NaN where one of them is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Scalars of the score modification, set by the host.
 struct ScoreMod {
   float scale_log2;     // scale * log2(e)
@@ -208,14 +215,16 @@ __device__ __forceinline__ void hide(uint64_t (&x)[kPairs], int a, int b) {
   }
 }
 
-// x <- x * mul - slope2 * |dist0 - key| for kPairs pairs of keys 0, 1, ..  The
-// distance is linear in the key on either side of the row's own position: away
-// from it the bias is a base for every eight keys plus one of four pairs of
-// multiples of the slope, two packed operations a pair.
+// x <- x * mul - slope2 * |dist0 - key| for kPairs pairs of keys 0, 1, .., of
+// which those in [a, b) count.  The distance is linear in the key on either side
+// of the row's own position: unless a row sees keys on both sides, the bias is
+// a base for every eight keys plus one of four pairs of multiples of the slope,
+// two packed operations a pair.
 template <int kPairs, bool kMul>
-__device__ __forceinline__ void bias_scores(uint64_t (&x)[kPairs], float mul, float slope2, float dist0) {
-  if (__all_sync(0xffffffffu, dist0 <= 0.f || dist0 >= static_cast<float>(2 * kPairs - 1))) {
-    const float sl = dist0 <= 0.f ? -slope2 : slope2;
+__device__ __forceinline__ void bias_scores(uint64_t (&x)[kPairs], float mul, float slope2, float dist0, int a, int b) {
+  const bool behind = dist0 >= static_cast<float>(min(b, 2 * kPairs) - 1);  // all keys that count
+  if (__all_sync(0xffffffffu, behind || dist0 <= static_cast<float>(max(a, 0)))) {
+    const float sl = behind ? slope2 : -slope2;
     uint64_t step[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) step[u] = f2(sl * static_cast<float>(2 * u), sl * static_cast<float>(2 * u + 1));
@@ -244,6 +253,15 @@ __device__ __forceinline__ void capped_keys(uint32_t tS, uint32_t tP, int a, int
                                             uint32_t bar_p, int lane) {
   constexpr int kPairs = 32;
   const bool edge = __any_sync(0xffffffffu, a > 0 || b < 2 * kPairs);
+  if (!__any_sync(0xffffffffu, max(a, 0) < min(b, 2 * kPairs))) {  // no row of this warp sees any of it
+    const uint32_t none[32] = {};
+    tmem_st_x32(tP, none);
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar_p);
+    return;
+  }
   uint64_t x[kPairs];
   {
     uint32_t sr[2 * kPairs];
@@ -295,6 +313,19 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int a, in
     }
   }
   constexpr bool kMod = kCap || kBias;
+  if (!__any_sync(0xffffffffu, max(a, 0) < min(b, kBN))) {  // no row of this warp sees any of it
+    const uint32_t none[16] = {};
+#pragma unroll
+    for (int ch = 0; ch < kBN / 32; ++ch) tmem_st_x16(tS + ch * 16, none);
+    tmem_st_wait();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(bar_part);
+      mbar_arrive(bar_full);
+    }
+    return;
+  }
   float s[kBN];
   {
     uint32_t sr[kBN];
@@ -310,7 +341,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int a, in
 #pragma unroll
     for (int e = 0; e < kBN / 2; ++e) x[e] = f2(s[2 * e], s[2 * e + 1]);
     if constexpr (kCap) cap_scores<kBN / 2>(x, sm, 0.f);
-    if constexpr (kBias) bias_scores<kBN / 2, !kCap>(x, c, slope2, dist0);
+    if constexpr (kBias) bias_scores<kBN / 2, !kCap>(x, c, slope2, dist0, a, b);
     if (edge) hide<kBN / 2>(x, a, b);
     float m8[8];
 #pragma unroll
@@ -411,7 +442,7 @@ template <int kCols>
 __device__ __noinline__ bool store_cols_bf16(uint32_t tO, uint32_t stg, __nv_bfloat16* dst, long long row_stride,
                                              int rows_left, float inv) {
   const int lane = threadIdx.x % 32;
-  float bad = 0.f;  // x * 0 is NaN where x is not finite
+  float top = 0.f;  // the largest magnitude, or NaN
 #pragma unroll 1
   for (int c0 = 0; c0 < kCols; c0 += 16) {
     uint32_t orr[16], pk[8];
@@ -419,7 +450,7 @@ __device__ __noinline__ bool store_cols_bf16(uint32_t tO, uint32_t stg, __nv_bfl
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float x0 = __uint_as_float(orr[2 * e]), x1 = __uint_as_float(orr[2 * e + 1]);
-      bad = fmaf(x0, 0.f, fmaf(x1, 0.f, bad));
+      top = max3_nan(top, x0, x1);
       pk[e] = inv == 0.f ? 0u : pack_bf16x2(x0 * inv, x1 * inv);
     }
     __syncwarp();  // the previous piece has left the staging area
@@ -435,11 +466,11 @@ __device__ __noinline__ bool store_cols_bf16(uint32_t tO, uint32_t stg, __nv_bfl
       if (r < rows_left) *reinterpret_cast<uint4*>(dst + r * row_stride + c0 + u * 8) = v;
     }
   }
-  return !(bad == 0.f);
+  return !(top <= FLT_MAX);
 }
 
 // Scale a thread's O row (TMEM columns [tO, tO + D)) by `inv` and store it as
-// bf16, through the warp's 4 KB staging area (see attn_fwd.cuh).  Row r of the
+// bf16, through the warp's staging area (see attn_fwd.cuh).  Row r of the
 // warp is at dst + r * row_stride elements; rows r >= rows_left are not written.
 // inv = 0 stores zeros whatever the accumulator holds.  Returns whether this
 // thread's row has a value that is not finite.
@@ -447,36 +478,34 @@ template <int D>
 __device__ __noinline__ bool store_rows(uint32_t tO, uint32_t stg, __nv_bfloat16* dst, long long row_stride,
                                         int rows_left, float inv) {
   const int lane = threadIdx.x % 32;
-  const int r0 = lane >> 3, c = lane & 7;
-  float bad[2] = {0.f, 0.f};  // x * 0 is NaN where x is not finite
+  // 32 columns (64 bytes of each row) at a time, in a loop that stays short: it runs
+  // once an item, mostly from beyond the instruction cache.
+  float top[2] = {0.f, 0.f};  // the largest magnitude, or NaN
 #pragma unroll 1
-  for (int h = 0; h < D / 64; ++h) {
-    __syncwarp();  // the previous piece has left the staging area
+  for (int c0 = 0; c0 < D; c0 += 32) {
+    uint32_t orr[32], pk[16];
+    tmem_ld_x32(tO + c0, orr);
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      uint32_t orr[32], pk[16];
-      tmem_ld_x32(tO + h * 64 + hh * 32, orr);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float x0 = __uint_as_float(orr[2 * e]), x1 = __uint_as_float(orr[2 * e + 1]);
-        bad[0] = fmaf(x0, 0.f, bad[0]);
-        bad[1] = fmaf(x1, 0.f, bad[1]);
-        pk[e] = inv == 0.f ? 0u : pack_bf16x2(x0 * inv, x1 * inv);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        st_shared_v4(stg + lane * 128 + (((4 * hh + u) ^ (lane & 7)) << 4), pk[4 * u], pk[4 * u + 1], pk[4 * u + 2],
-                     pk[4 * u + 3]);
+    for (int e = 0; e < 16; ++e) {
+      const float x0 = __uint_as_float(orr[2 * e]), x1 = __uint_as_float(orr[2 * e + 1]);
+      top[e & 1] = max3_nan(top[e & 1], x0, x1);
+      pk[e] = inv == 0.f ? 0u : pack_bf16x2(x0 * inv, x1 * inv);
     }
+    __syncwarp();  // the previous piece has left the staging area
+    // Chunk u of row r at position u ^ (r / 2 % 4): eight rows fill the banks twice.
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      st_shared_v4(stg + lane * 64 + ((u ^ ((lane >> 1) & 3)) << 4), pk[4 * u], pk[4 * u + 1], pk[4 * u + 2],
+                   pk[4 * u + 3]);
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int r = 4 * k + r0;
-      const uint4 x = ld_shared_v4(stg + r * 128 + ((c ^ (r & 7)) << 4));
-      if (r < rows_left) *reinterpret_cast<uint4*>(dst + r * row_stride + h * 64 + c * 8) = x;
+    for (int k = 0; k < 4; ++k) {
+      const int r = 8 * k + (lane >> 2), u = lane & 3;
+      const uint4 v = ld_shared_v4(stg + r * 64 + ((u ^ ((r >> 1) & 3)) << 4));
+      if (r < rows_left) *reinterpret_cast<uint4*>(dst + r * row_stride + c0 + u * 8) = v;
     }
   }
-  return !(bad[0] + bad[1] == 0.f);
+  return !(max3_nan(top[0], top[1], 0.f) <= FLT_MAX);
 }
 
 // Recompute one output row with the whole warp, reading only the keys [j0, j1)
