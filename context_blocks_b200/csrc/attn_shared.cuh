@@ -11,8 +11,9 @@
 // K/V head, or one request's tail under one K/V head.  Two row tiles over the
 // same prefix make a pair, which shares its K and V tiles; what is left (the
 // prefix under an odd row tile, and the tails) is single.  The singles form a line
-// of key tiles (128 keys), cut into equal parts, one for each of the two streams
-// (a softmax warpgroup, its MMA and its load warp) of the CTAs that take singles.
+// of key tiles (128 keys), and one more unit for the start of each tail, cut into
+// equal parts, one for each of the two streams (a softmax warpgroup, its MMA and
+// its load warp) of the CTAs that take singles.
 // The other CTAs take pairs, as many CTAs a pair: CTA c has pair c mod (pairs), and
 // the prefix, cut into equal parts, part c / (pairs) of it, so that the CTAs of
 // one part read the same tiles at the same time and HBM gives them once (with
@@ -62,7 +63,7 @@ constexpr int kLoadWarp = 9;   // + stream
 // how the CTAs are dealt to the two kinds.  From the shares of CTAs that were
 // fastest for 128 requests on 32768 keys: with tails of one key tile
 // 1.25 single tiles a pair tile, with four 2, with eight 2.2.
-constexpr int kPairCost = 15, kSingleCost = 6, kTailCost = 6;
+constexpr int kPairCost = 15, kSingleCost = 6;
 
 // A line of n units cut into `parts` parts, none empty, sizes differing by one.
 struct Cut {
@@ -96,15 +97,18 @@ struct Plan {
   __host__ __device__ static int copies(int n) { return n <= 32 ? 4 : n <= 64 ? 2 : 1; }
   __device__ int len(int b) const { return min(max(__ldg(tail_lens + b), 0), Nt); }
   __device__ static int tiles_of(int keys) { return (keys + kBN - 1) / kBN; }
-  // CTAs that take pairs, given the tail tiles (under one K/V head) of all requests
-  // and the number of requests that have any.
-  __device__ int pair_ctas(int tiles, int tails) const {
+  // Units of the line that a tail of so many key tiles has under one K/V head: its
+  // tiles behind one for its start.
+  __device__ static int tail_units(int tiles) { return tiles + (tiles > 0); }
+  // CTAs that take pairs, given the units (under one K/V head) of all tails.
+  __device__ int pair_ctas(int tails) const {
     const long long p = static_cast<long long>(pair_units()) * kPairCost;
-    const long long s = odd_units() * static_cast<long long>(kSingleCost) +
-                        (tiles * static_cast<long long>(kSingleCost) + tails * kTailCost) * Hkv;
+    const long long s = (odd_units() + tails * static_cast<long long>(Hkv)) * kSingleCost;
     if (p == 0) return 0;
     if (s == 0) return ctas <= pairs() ? ctas : ctas - ctas % pairs();
-    const int n = static_cast<int>(min(max((ctas * p + (p + s) / 2) / (p + s), 1ll), ctas - 1ll));
+    // Rounded the same way in both kernels.
+    const float share = __fdiv_rn(__ll2float_rn(p), __ll2float_rn(p + s));
+    const int n = min(max(__float2int_rn(__fmul_rn(static_cast<float>(ctas), share)), 1), ctas - 1);
     return n <= pairs() ? n : n - n % pairs();  // as many for every pair
   }
 };
@@ -356,21 +360,18 @@ __global__ void __launch_bounds__(R::kThreads, 1)
     fence_barrier_init();
   }
   // The load warps reckon while the barriers and tensor memory are set up: all
-  // tail tiles under one K/V head, and the CTAs that take pairs.
+  // units of tails under one K/V head, and the CTAs that take pairs.
   int tails = 0, pair_ctas = 0;
   if (warp == kLoadWarp || warp == kLoadWarp + 1) {
-    int some = 0;
     for (int b0 = 0; b0 < plan.B; b0 += 128) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int b = b0 + u * 32 + lane;
-        const int n = b < plan.B ? Plan::tiles_of(plan.len(b)) : 0;
-        tails += n;
-        some += n > 0;
+        if (b < plan.B) tails += Plan::tail_units(Plan::tiles_of(plan.len(b)));
       }
     }
     tails = __reduce_add_sync(0xffffffffu, tails);
-    pair_ctas = plan.pair_ctas(tails, __reduce_add_sync(0xffffffffu, some));
+    pair_ctas = plan.pair_ctas(tails);
   }
   if (warp == kLoadWarp && lane == 0) {
     prefetch_tensormap(&tm_qp);
@@ -520,29 +521,31 @@ __global__ void __launch_bounds__(R::kThreads, 1)
         run(kOdd, s, (plan.row_tiles - 1) * plan.tile_reqs, t0, t1, s + c, plan.Np);
         u += t1 - t0;
       }
-      int at = plan.odd_units();  // place of request b0's first tile
+      int at = plan.odd_units();  // place of request b0's first unit
       for (int b0 = 0; b0 < plan.B && at < u1 && ok; b0 += 32) {
         const int n = b0 + lane < plan.B ? plan.len(b0 + lane) : 0;
         const int nt = Plan::tiles_of(n);
-        int upto = nt;  // inclusive scan
+        const int nu = Plan::tail_units(nt);
+        int upto = nu;  // inclusive scan
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
           const int y = __shfl_up_sync(0xffffffffu, upto, off);
           if (lane >= off) upto += y;
         }
-        const int mine0 = at + (upto - nt) * plan.Hkv, mine1 = at + upto * plan.Hkv;
+        const int mine0 = at + (upto - nu) * plan.Hkv, mine1 = at + upto * plan.Hkv;
         at += __shfl_sync(0xffffffffu, upto, 31) * plan.Hkv;
-        // Requests of these 32 that have a tile in this part.
-        unsigned todo = __ballot_sync(0xffffffffu, nt > 0 && mine0 < u1 && mine1 > u0);
+        // Requests of these 32 that have a unit in this part.
+        unsigned todo = __ballot_sync(0xffffffffu, nu > 0 && mine0 < u1 && mine1 > u0);
         while (todo != 0u && ok) {
           const int k = __ffs(todo) - 1;
           todo &= todo - 1;
           const int a0 = __shfl_sync(0xffffffffu, mine0, k);
           const int kn = __shfl_sync(0xffffffffu, n, k), knt = __shfl_sync(0xffffffffu, nt, k);
-          for (int hk = max(u0 - a0, 0) / knt; hk < plan.Hkv && ok; ++hk) {
-            const int a = a0 + hk * knt;
+          for (int hk = max(u0 - a0, 0) / (knt + 1); hk < plan.Hkv && ok; ++hk) {
+            const int a = a0 + hk * (knt + 1) + 1;  // the first tile's place
             if (a >= u1) break;
-            run(kTail, hk, b0 + k, max(u0 - a, 0), min(u1 - a, knt), (b0 + k) * plan.Hkv + hk + c, kn);
+            if (a + knt > u0)
+              run(kTail, hk, b0 + k, max(u0 - a, 0), min(u1 - a, knt), (b0 + k) * plan.Hkv + hk + c, kn);
           }
         }
       }
@@ -809,100 +812,113 @@ __global__ void __launch_bounds__(R::kThreads, 1)
   }
 }
 
+// Warps of a merge block.  Eight, which divide a row's partials among them, as long
+// as all blocks fit on the GPU at once; with more of them four.  MEASURED_MERGE
+inline int merge_warps(const Plan& plan) {
+  return plan.B * plan.Hkv <= 4 * plan.ctas ? kMergeWarps : kMergeWarps / 2;
+}
+
 // Joins the partial results of every row:
 //     M = max_p m_p,  w_p = 2^(m_p - M),  L = sum w_p l_p
 //     o = sum w_p o_p / L,  lse = (M + log2 L) ln 2
 // One block a (request, K/V head); its rows are dealt to groups of warps, the
 // partials of a row to the warps of its group.  The partials lie where the
-// kernel above put them: the same lines are cut into the same parts.
+// kernel above put them: the same lines are cut into the same parts, which one
+// warp reckons for its block (all of them doing so took longer than the
+// joining: some 15 integer divisions).
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __grid_constant__ Params p,
+__global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const __grid_constant__ Params p,
                                                                         __nv_bfloat16* o, float* lse) {
   constexpr int kCols = D / 32;
+  constexpr int kBatch = 4;  // partial rows a warp has on the way at once
   __shared__ float part_m[kMergeWarps], part_l[kMergeWarps];
   __shared__ float part_o[kMergeWarps][D];
+  // Where the partials of this block's rows lie: number k < n_p, of the prefix, in
+  // place base_p + k * step_p, the others in place base_t + k - n_p.
+  __shared__ int s_pair, s_base_p, s_step_p, s_n_p, s_base_t, s_n_parts;
   const Plan& plan = p.plan;
+  const int warps = blockDim.x / 32;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int req = blockIdx.x / plan.Hkv, hk = blockIdx.x % plan.Hkv;
 
-  // Tail tiles (under one K/V head) of all requests, and of those before req.
-  int all = 0, before = 0, some = 0;
-  for (int b0 = 0; b0 < plan.B; b0 += 128) {
+  if (warp == 0) {
+    // Units of all tails (under one K/V head), and of those before req.
+    int all = 0, before = 0;
+    for (int b0 = 0; b0 < plan.B; b0 += 128) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int b = b0 + u * 32 + lane;
-      if (b >= plan.B) continue;
-      const int n = Plan::tiles_of(plan.len(b));
-      all += n;
-      some += n > 0;
-      if (b < req) before += n;
-      if (blockIdx.x == 0 && warp == 0 && __ldg(plan.tail_lens + b) != plan.len(b))
-        atomicCAS(p.status, 0, kStatusBadInput);
+      for (int u = 0; u < 4; ++u) {
+        const int b = b0 + u * 32 + lane;
+        if (b >= plan.B) continue;
+        const int n = Plan::tail_units(Plan::tiles_of(plan.len(b)));
+        all += n;
+        if (b < req) before += n;
+        if (blockIdx.x == 0 && __ldg(plan.tail_lens + b) != plan.len(b)) atomicCAS(p.status, 0, kStatusBadInput);
+      }
+    }
+    all = __reduce_add_sync(0xffffffffu, all);
+    before = __reduce_add_sync(0xffffffffu, before);
+
+    // Parts [p0, p1) of the pairs' or the singles' line hold the prefix under this
+    // row tile, [t0, t1) of the singles' the tail.
+    const int n_tail = Plan::tiles_of(plan.len(req));
+    const int pair_ctas = plan.pair_ctas(all);
+    const int mt = req / plan.tile_reqs;
+    const bool pair = mt < 2 * plan.pairs();
+    const int copies_p = pair ? 1 : Plan::copies(plan.tile_rows()), copies_t = Plan::copies(plan.rows);
+    // The prefix under this row tile: its segment on the line of its pair's lane, or
+    // on the singles'.
+    const int lanes = pair ? plan.lanes(pair_ctas) : 1, my_lane = pair ? mt / 2 % lanes : 0;
+    const int seg_p = pair ? mt / 2 / lanes * plan.Hkv + hk : hk, seg_t = req * plan.Hkv + hk;
+    const Cut singles(plan.odd_units() + all * plan.Hkv, 2 * (plan.ctas - pair_ctas));
+    int p0 = 0, p1 = 0, t0 = 0, t1 = 0;
+    if (plan.row_tiles > 0) {
+      const Cut cut = pair ? Cut(plan.lane_pairs(lanes, my_lane) * plan.Hkv * plan.prefix_tiles, pair_ctas / lanes)
+                           : singles;
+      p0 = cut.holder(seg_p * plan.prefix_tiles);
+      p1 = cut.holder((seg_p + 1) * plan.prefix_tiles - 1) + 1;
+    }
+    if (n_tail > 0) {
+      const int at = plan.odd_units() + before * plan.Hkv + hk * (n_tail + 1) + 1;
+      t0 = singles.holder(at);
+      t1 = singles.holder(at + n_tail - 1) + 1;
+    }
+    if (lane == 0) {
+      s_pair = pair;
+      s_base_p = pair ? 2 * ((seg_p + p0) * lanes + my_lane) + (mt & 1) : (seg_p + p0) * copies_p;
+      s_step_p = pair ? 2 * lanes : 1;
+      s_n_p = (p1 - p0) * copies_p;
+      s_base_t = (seg_t + t0) * copies_t;
+      s_n_parts = (p1 - p0) * copies_p + (t1 - t0) * copies_t;
     }
   }
-  all = __reduce_add_sync(0xffffffffu, all);
-  before = __reduce_add_sync(0xffffffffu, before);
-  some = __reduce_add_sync(0xffffffffu, some);
-
-  // Parts [p0, p1) of the pairs' or the singles' line hold the prefix under this
-  // row tile, [t0, t1) of the singles' the tail.
-  const int n_tail = Plan::tiles_of(plan.len(req));
-  const int pair_ctas = plan.pair_ctas(all, some);
-  const int mt = req / plan.tile_reqs;
-  const bool pair = mt < 2 * plan.pairs();
-  const int copies_p = pair ? 1 : Plan::copies(plan.tile_rows()), copies_t = Plan::copies(plan.rows);
-  // The prefix under this row tile: its segment on the line of its pair's lane, or
-  // on the singles'.
-  const int lanes = pair ? plan.lanes(pair_ctas) : 1, my_lane = pair ? mt / 2 % lanes : 0;
-  const int seg_p = pair ? mt / 2 / lanes * plan.Hkv + hk : hk, seg_t = req * plan.Hkv + hk;
-  const Cut singles(plan.odd_units() + all * plan.Hkv, 2 * (plan.ctas - pair_ctas));
-  int p0 = 0, p1 = 0, t0 = 0, t1 = 0;
-  if (plan.row_tiles > 0) {
-    const Cut pairs(pair ? plan.lane_pairs(lanes, my_lane) * plan.Hkv * plan.prefix_tiles : 1,
-                    pair ? pair_ctas / lanes : 1);
-    const Cut& cut = pair ? pairs : singles;
-    p0 = cut.holder(seg_p * plan.prefix_tiles);
-    p1 = cut.holder((seg_p + 1) * plan.prefix_tiles - 1) + 1;
-  }
-  if (n_tail > 0) {
-    const int at = plan.odd_units() + before * plan.Hkv + hk * n_tail;
-    t0 = singles.holder(at);
-    t1 = singles.holder(at + n_tail - 1) + 1;
-  }
-  const int n_p = (p1 - p0) * copies_p, n_parts = n_p + (t1 - t0) * copies_t;
-  const float* const p_o = pair ? p.pair_o : p.odd_o;
-  const float2* const p_ml = pair ? p.pair_ml : p.odd_ml;
+  __syncthreads();
+  const int base_p = s_base_p, step_p = s_step_p, n_p = s_n_p, base_t = s_base_t, n_parts = s_n_parts;
+  const float* const p_o = s_pair ? p.pair_o : p.odd_o;
+  const float2* const p_ml = s_pair ? p.pair_ml : p.odd_ml;
+  const int in_tile = req % plan.tile_reqs * plan.rows;
 
   // All of the above runs while the other kernel ends; its results are there
   // behind this.
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  int group = kMergeWarps;  // warps a row
-  while (group > 1 && group * plan.rows > kMergeWarps) group /= 2;
+  int group = warps;  // warps a row
+  while (group > 1 && group * plan.rows > warps) group /= 2;
   const int wi = warp % group;
-  for (int r0 = 0; r0 < plan.rows; r0 += kMergeWarps / group) {
+  for (int r0 = 0; r0 < plan.rows; r0 += warps / group) {
     const int rr = r0 + warp / group;
     const bool row_ok = rr < plan.rows;
+    // Row of the workspace that holds partial k.
+    auto place = [&](int k) {
+      return k < n_p ? static_cast<size_t>(base_p + k * step_p) * plan.tile_rows() + in_tile + rr
+                     : static_cast<size_t>(base_t + k - n_p) * plan.rows + rr;
+    };
     float m = -INFINITY, l = 0.f, acc[kCols];
 #pragma unroll
     for (int u = 0; u < kCols; ++u) acc[u] = 0.f;
-    for (int k0 = 0; k0 < n_parts && row_ok; k0 += 32 * group) {
-      const int k = k0 + lane * group + wi;
-      const float* src = nullptr;
+    for (int k0 = wi; k0 < n_parts && row_ok; k0 += 32 * group) {
+      const int k = k0 + lane * group;
       float2 my = make_float2(-INFINITY, 0.f);  // m = -inf, l = 0: a part that saw nothing
-      if (k < n_parts) {
-        if (k < n_p) {
-          const int slot =
-              pair ? 2 * ((seg_p + p0 + k) * lanes + my_lane) + (mt & 1) : (seg_p + p0) * copies_p + k;
-          const size_t row = static_cast<size_t>(slot) * plan.tile_rows() + (req % plan.tile_reqs) * plan.rows + rr;
-          my = __ldcg(p_ml + row);
-          src = p_o + row * D;
-        } else {
-          const size_t row = static_cast<size_t>((seg_t + t0) * copies_t + k - n_p) * plan.rows + rr;
-          my = __ldcg(p.tail_ml + row);
-          src = p.tail_o + row * D;
-        }
-      }
+      if (k < n_parts) my = __ldcg((k < n_p ? p_ml : p.tail_ml) + place(k));
       float mx = my.x;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
@@ -917,25 +933,30 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
       l = l * keep + lw;
 #pragma unroll
       for (int u = 0; u < kCols; ++u) acc[u] *= keep;
-      const int cnt = min(32, (n_parts - k0 - wi + group - 1) / group);
-#pragma unroll 8
-      for (int e = 0; e < cnt; ++e) {
-        const float we = __shfl_sync(0xffffffffu, w, e);
-        const float* s = reinterpret_cast<const float*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), e));
-        if (we != 0.f) {
-          if constexpr (D == 128) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + lane);
-            acc[0] = fmaf(we, v.x, acc[0]);
-            acc[1] = fmaf(we, v.y, acc[1]);
-            acc[2] = fmaf(we, v.z, acc[2]);
-            acc[3] = fmaf(we, v.w, acc[3]);
-          } else {
-            const float2 v = __ldcg(reinterpret_cast<const float2*>(s) + lane);
-            acc[0] = fmaf(we, v.x, acc[0]);
-            acc[1] = fmaf(we, v.y, acc[1]);
+      const int cnt = min(32, (n_parts - k0 + group - 1) / group);
+      for (int e0 = 0; e0 < cnt; e0 += kBatch) {
+        float we[kBatch], v[kBatch][kCols];
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) {
+          we[e] = __shfl_sync(0xffffffffu, w, e0 + e);  // 0 behind the last part
+#pragma unroll
+          for (int u = 0; u < kCols; ++u) v[e][u] = 0.f;
+          if (we[e] != 0.f) {  // a part of no weight may hold anything
+            const int ke = k0 + (e0 + e) * group;
+            const float* s = (ke < n_p ? p_o : p.tail_o) + place(ke) * D;
+            if constexpr (D == 128) {
+              const float4 x = __ldcg(reinterpret_cast<const float4*>(s) + lane);
+              v[e][0] = x.x, v[e][1] = x.y, v[e][2] = x.z, v[e][3] = x.w;
+            } else {
+              const float2 x = __ldcg(reinterpret_cast<const float2*>(s) + lane);
+              v[e][0] = x.x, v[e][1] = x.y;
+            }
           }
         }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e)
+#pragma unroll
+          for (int u = 0; u < kCols; ++u) acc[u] = fmaf(we[e], v[e][u], acc[u]);
       }
     }
     // Warps of a group join through shared memory, in warp order.

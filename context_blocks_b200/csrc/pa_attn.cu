@@ -645,7 +645,7 @@ int launch_shared(DeviceState* st, const CUtensorMap (&maps)[6], const pa::share
   overlap.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(prm.plan.B * prm.plan.Hkv));
-  cfg.blockDim = dim3(pa::shared::kMergeWarps * 32);
+  cfg.blockDim = dim3(pa::shared::merge_warps(prm.plan) * 32);
   cfg.stream = stream;
   cfg.attrs = &overlap;
   cfg.numAttrs = 1;
