@@ -3,7 +3,7 @@
     python -m context_blocks_b200.build [--verbose]
 
 The library is a single translation unit (``csrc/pa_attn.cu``) that holds the
-C ABI of ``include/pa_attn.h`` and both kernels.  The CUDA runtime is linked
+C ABI of ``include/pa_attn.h`` and all kernels.  The CUDA runtime is linked
 statically; the TMA tensor-map encoder is fetched from the driver at run time,
 so no link against libcuda is needed and the library cross-compiles on a
 machine without a GPU.
@@ -23,8 +23,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libpa_attn.so")
 SOURCES = [os.path.join(CSRC, "pa_attn.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "fwd_common.cuh", "attn_fwd.cuh", "attn_mod.cuh",
-                                                  "attn_shared.cuh", "block_norm.cuh", "lse_merge.cuh", "quantize.cuh", "residual_diff.cuh",
-                                                  "score_mod.cuh")] + [
+                                                  "attn_shared.cuh", "block_norm.cuh", "lse_merge.cuh",
+                                                  "quantize.cuh", "residual_diff.cuh", "score_mod.cuh")] + [
     os.path.join(INCLUDE, "pa_attn.h")]
 
 NVCC_FLAGS = [

@@ -35,8 +35,13 @@
 // both threads of a row would have to agree on a maximum for every tile, which
 // costs more than it gains (4096 keys, 24 heads: 207 us against 181).
 //
-// Bound: the special-function unit and the tensor pipe, as the plain forward;
-// a cap adds an ex2 and a reciprocal a score.
+// Bound: the chain from a tile's scores to its weights, which the tensor pipe waits
+// for as in the plain forward (4096 x 4096 keys, 24 heads: 181 us, 0.69 of the
+// matrix rate); with a cap the FMA pipe, on which the polynomial runs (8192 capped
+// causal keys, 24 heads: 430 us, FMA 56 % busy, special-function unit and tensor
+// pipe 48 %); with short documents an item's start and end, some 8 000 clocks beside
+// the 5 000 to 7 500 of a tile that the mask cuts (8192 keys in 24 documents, 24
+// heads, biased: 115 us, tensor pipe 25 % busy).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -19,7 +19,7 @@
 // one part read the same tiles at the same time and HBM gives them once (with
 // one line of all pairs the same tile was read at two far times, and tails
 // streaming through L2 drove it out in between, by chance: 100 to 130 us with
-// neighbouring numbers of CTAs, where this takes 109 to 113).
+// neighbouring numbers of CTAs, where this takes 107 to 111).
 // Every SM gets the same share whatever the lengths are, without counters and
 // without host knowledge of them.  The part of a segment that falls to one part of the
 // line is a piece; segment + part is another number for every piece, since both
@@ -32,8 +32,11 @@
 // less; 64 or less) hold their rows four times (twice): every copy lies in the
 // tensor-memory lanes of a warp of its own, which takes its quarter (half) of
 // the tile's keys, with zero weights for the rest.  One warp working through 128
-// keys a row took longer than the tile's loads: 4.5 TB/s where this reaches 5.6
-// (24 heads, 119056 keys, 21 rows).  The copies' results are joined like those of different pieces.
+// keys a row took longer than the tile's loads: 4.5 TB/s where the copies reached
+// 5.6 (24 heads, 119056 keys, 21 rows).  The copies' results are joined like those
+// of different pieces.  A tail's start counts as a tile on the line because with
+// tiles alone the streams at its end had some forty short tails each and finished
+// 60 us behind the others: 270 us, now 222 for 1.47 GB, 6.6 TB/s.
 //
 // Warps: 0-3, 4-7 softmax of stream 0 and 1 (208 registers); 8, 11 MMA issue of
 // stream 0 and 1 (8 issues for both in a pair CTA); 9, 10 pieces and TMA loads
@@ -59,10 +62,10 @@ using R = Roles<false>;  // warps and registers of the single-warpgroup kernel
 constexpr int kMaxCtas = 160;  // sizes the workspace; the grid is one CTA an SM, at most this many
 constexpr int kMergeWarps = 8;
 constexpr int kLoadWarp = 9;   // + stream
-// What a pair's key tile, a single's and a tail costs, in parts of one another:
-// how the CTAs are dealt to the two kinds.  From the shares of CTAs that were
-// fastest for 128 requests on 32768 keys: with tails of one key tile
-// 1.25 single tiles a pair tile, with four 2, with eight 2.2.
+// What a pair's key tile and a unit of the singles cost, in parts of one another:
+// how the CTAs are dealt to the two kinds.  128 requests on 32768 capped keys,
+// tails of 16, 512 and 1024 tokens: 112, 132 and 162 us at 15 : 6; at 12 : 6 113,
+// 143 and 174; at 18 : 6 107, 136 and 160; at 22 : 6 121, 153 and 179.
 constexpr int kPairCost = 15, kSingleCost = 6;
 
 // A line of n units cut into `parts` parts, none empty, sizes differing by one.
@@ -185,7 +188,8 @@ __device__ __forceinline__ void softmax_share(uint32_t tS, uint32_t tO, int kq, 
     for (int e = 0; e < kKeys / 2; ++e) x[e] = f2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
   }
   if constexpr (kCap) cap_scores<kKeys / 2>(x, sm, 0.f);
-  if constexpr (kBias) bias_scores<kKeys / 2, !kCap>(x, sm.scale_log2, slope2, dist0 - static_cast<float>(e0), 0, b - e0);
+  if constexpr (kBias)
+    bias_scores<kKeys / 2, !kCap>(x, sm.scale_log2, slope2, dist0 - static_cast<float>(e0), 0, b - e0);
   if (__any_sync(0xffffffffu, b < e0 + kKeys)) hide<kKeys / 2>(x, 0, b - e0);
   float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -225,9 +229,9 @@ __device__ __forceinline__ void softmax_share(uint32_t tS, uint32_t tO, int kq, 
     uint32_t pk[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const uint64_t nm2 = f2(neg_m, neg_m);
+      const uint64_t nm2 = f2(neg_m, neg_m), xe = x[ch * 16 + e];
       float x0, x1;
-      f2_split(kMod ? f2_add(x[ch * 16 + e], nm2) : f2_fma(x[ch * 16 + e], f2(sm.scale_log2, sm.scale_log2), nm2), x0, x1);
+      f2_split(kMod ? f2_add(xe, nm2) : f2_fma(xe, f2(sm.scale_log2, sm.scale_log2), nm2), x0, x1);
       const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
       l2[0] += p0;
       l2[1] += p1;
@@ -502,7 +506,8 @@ __global__ void __launch_bounds__(R::kThreads, 1)
         for (int u = u0; u < u1 && ok;) {
           const int s = u / plan.prefix_tiles, t0 = u - s * plan.prefix_tiles;
           const int t1 = min(plan.prefix_tiles, t0 + u1 - u);
-          run(kPair, s % plan.Hkv, 2 * (l + s / plan.Hkv * lanes) * plan.tile_reqs, t0, t1, (s + c) * lanes + l, plan.Np);
+          run(kPair, s % plan.Hkv, 2 * (l + s / plan.Hkv * lanes) * plan.tile_reqs, t0, t1, (s + c) * lanes + l,
+              plan.Np);
           u += t1 - t0;
         }
         if (ok) publish(kEnd, 0, 0, 0, 0, 0, 0, true);
@@ -793,8 +798,8 @@ __global__ void __launch_bounds__(R::kThreads, 1)
           const int ps = __shfl_sync(0xffffffffu, pos, k), sn = __shfl_sync(0xffffffffu, seen, k);
           const float mr = __shfl_sync(0xffffffffu, m_ref, k);
           const float sl = __shfl_sync(0xffffffffu, slope2, k);
-          const size_t q_row =
-              (static_cast<size_t>(x.req) * plan.Hq + x.hk * plan.G) * plan.Nq + wr + k;  // rows of a K/V head are adjacent
+          // Rows of a K/V head are adjacent.
+          const size_t q_row = (static_cast<size_t>(x.req) * plan.Hq + x.hk * plan.G) * plan.Nq + wr + k;
           repair_row<D, D>(p.q + q_row * D, p.kt + x.req * p.kt_s[0] + x.hk * p.kt_s[1],
                         p.vt + x.req * p.vt_s[0] + x.hk * p.vt_s[1], p.kt_s[2], p.vt_s[2], x.t0 * kBN,
                         min(sn, x.t1 * kBN), kBN / copies, kBN, kq, ps, mr, 1.f, sl, p.sm, kCap, kBias, nullptr,
@@ -813,7 +818,9 @@ __global__ void __launch_bounds__(R::kThreads, 1)
 }
 
 // Warps of a merge block.  Eight, which divide a row's partials among them, as long
-// as all blocks fit on the GPU at once; with more of them four.  MEASURED_MERGE
+// as the blocks fit on the GPU at once (four an SM); with more of them four.  From the
+// first kernel's end, d = 128: 512 blocks 7.0 us with eight and 11.9 with four, 168
+// blocks of 52 partials a row 10.2 and 16.4, 1024 blocks 11.7 and 7.2.
 inline int merge_warps(const Plan& plan) {
   return plan.B * plan.Hkv <= 4 * plan.ctas ? kMergeWarps : kMergeWarps / 2;
 }
@@ -830,7 +837,7 @@ template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const __grid_constant__ Params p,
                                                                         __nv_bfloat16* o, float* lse) {
   constexpr int kCols = D / 32;
-  constexpr int kBatch = 4;  // partial rows a warp has on the way at once
+  constexpr int kBatch = 4;  // partial rows a warp has on the way at once; 8 cost a third of the resident blocks
   __shared__ float part_m[kMergeWarps], part_l[kMergeWarps];
   __shared__ float part_o[kMergeWarps][D];
   // Where the partials of this block's rows lie: number k < n_p, of the prefix, in

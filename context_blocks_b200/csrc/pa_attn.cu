@@ -484,8 +484,10 @@ int check_scores(int B, int Hq, int Hkv, int Nq, int d, float scale, float softc
   if (Nq < 0) return fail(PA_ERR_INVALID_ARG, "Nq must be >= 0 (got %d)", Nq);
   if (!std::isfinite(scale) || !(scale > 0.f)) return fail(PA_ERR_INVALID_ARG, "scale must be finite and > 0");
   // Between these, no factor of the cap over- or underflows fp32.
-  if (!(softcap == 0.f || (softcap >= 1e-15f && softcap <= 1e15f && scale / softcap >= 1e-25f && scale / softcap <= 1e25f)))
-    return fail(PA_ERR_INVALID_ARG, "softcap must be 0 (no cap) or in [1e-15, 1e15], and scale / softcap in [1e-25, 1e25]");
+  if (!(softcap == 0.f ||
+        (softcap >= 1e-15f && softcap <= 1e15f && scale / softcap >= 1e-25f && scale / softcap <= 1e25f)))
+    return fail(PA_ERR_INVALID_ARG,
+                "softcap must be 0 (no cap) or in [1e-15, 1e15], and scale / softcap in [1e-25, 1e25]");
   if (d != 64 && d != 128) return fail(PA_ERR_UNSUPPORTED, "d must be 64 or 128 (got %d)", d);
   if (static_cast<long long>(B) * Hq > 65535) return fail(PA_ERR_UNSUPPORTED, "B*Hq must be <= 65535");
   if (slopes && !aligned(slopes, 4)) return fail(PA_ERR_MISALIGNED, "slopes must be 4-byte aligned");
@@ -634,8 +636,8 @@ int launch_shared(DeviceState* st, const CUtensorMap (&maps)[6], const pa::share
                               pa::shared::R::kLaunchRegs, "shared-prefix");
   if (rc != PA_OK) return rc;
   if (prm.plan.Np > 0 || prm.plan.Nt > 0)
-    kern<<<prm.plan.ctas, pa::shared::R::kThreads, L::kAllocBytes, stream>>>(maps[0], maps[1], maps[2], maps[3], maps[4],
-                                                                       maps[5], prm);
+    kern<<<prm.plan.ctas, pa::shared::R::kThreads, L::kAllocBytes, stream>>>(maps[0], maps[1], maps[2], maps[3],
+                                                                             maps[4], maps[5], prm);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "attn_shared launch");
   // Launched while the first kernel runs (the merge waits for its results), so
@@ -699,8 +701,8 @@ int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_pre
     if (!workspace) return fail(PA_ERR_INVALID_ARG, "null pointer argument (workspace)");
     if (!aligned(workspace, 16)) return fail(PA_ERR_MISALIGNED, "workspace must be 16-byte aligned");
     if (workspace_bytes < ws.end)
-      return fail(PA_ERR_INVALID_ARG, "the workspace needs %llu bytes (got %llu)", static_cast<unsigned long long>(ws.end),
-                  static_cast<unsigned long long>(workspace_bytes));
+      return fail(PA_ERR_INVALID_ARG, "the workspace needs %llu bytes (got %llu)",
+                  static_cast<unsigned long long>(ws.end), static_cast<unsigned long long>(workspace_bytes));
   }
   const uint64_t lse_bytes = static_cast<uint64_t>(B) * Hq * Nq * 4;
   const void* ins[7] = {q, kp.ptr, vp.ptr, kt.ptr, vt.ptr, tail_lens, slopes};
@@ -772,7 +774,8 @@ int pa_attn_fwd_mod(const void* q, const void* k, const void* v, void* o, float*
   if (Nq == 0) return PA_OK;  // an empty tensor may have no address
   if (!lse) return fail(PA_ERR_INVALID_ARG, "null pointer argument (lse)");
   if (!aligned(lse, 4)) return fail(PA_ERR_MISALIGNED, "lse must be 4-byte aligned");
-  const Operand oq = operand(q, "q", B, Hq, Nq, d, strides), ok = operand(k, "k", B, Hkv, Nk, d, strides ? strides + 3 : nullptr),
+  const Operand oq = operand(q, "q", B, Hq, Nq, d, strides),
+                ok = operand(k, "k", B, Hkv, Nk, d, strides ? strides + 3 : nullptr),
                 ov = operand(v, "v", B, Hkv, Nk, d, strides ? strides + 6 : nullptr),
                 oo = operand(o, "o", B, Hq, Nq, d, strides ? strides + 9 : nullptr);
   for (const Operand* x : {&oq, &ok, &ov, &oo})

@@ -13,10 +13,9 @@
 // 1 - 2 / (2^(2 u log2 e) + 1) otherwise: ex2 and rcp of the special-function
 // unit, whose errors (2^-22 relative) become at most c * 2^-21 in the capped
 // score.  The polynomial takes half the special-function work of a score away,
-// which bounds the kernels (8192 capped causal keys, 24 heads: 800 us before, 639
-// us with it).  The unit's own
-// tanh has a relative error of 2^-11, which at c = 50 would be 0.02 in the
-// exponent.
+// which bounded the kernels (8192 capped causal keys, 24 heads: 800 us before, 639
+// us with it).  The unit's own tanh has a relative error of 2^-11, which at c = 50
+// would be 0.02 in the exponent.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -14,7 +14,11 @@
  * pa_attn_fwd_chunks (up to 8 chunks in one launch, no partials),
  * pa_attn_fwd_fp8 / pa_attn_fwd_fp8_dev with pa_quantize_e4m3 (e4m3 inputs),
  * pa_attn_chunks_noalloc (chunks + merge with library-owned static scratch),
- * and the status helpers at the end of this file.
+ * the parts of a language model's layer (pa_attn_fwd_mod: causal, prefix and
+ * document masks, capped and biased scores, grouped heads; pa_attn_shared_prefix:
+ * a decoding step of requests that share a prefix; pa_gate_residual_norm: the
+ * residual update between blocks with its norms), and the status helpers at
+ * the end of this file.
  *
  * Together they are the per-device step of Ring Attention as the diffusers
  * guide "Context parallelism" describes it (section "Ring Attention": each
@@ -22,14 +26,15 @@
  * full turn every device has seen the K/V of every token).  Chunks of any
  * length are accepted (section "Ring Anything Attention": blocks are trimmed
  * to their real length before attention, so padding never enters the
- * softmax).  Attention is the non-causal, unmasked scaled-dot-product
- * attention of the guide "Accelerate inference" (section "Scaled dot product
+ * softmax).  Apart from pa_attn_fwd_mod and pa_attn_shared_prefix, attention is
+ * the non-causal, unmasked scaled-dot-product attention of the guide "Accelerate inference" (section "Scaled dot product
  * attention"; inference only, attn_mask None), computed on bf16 inputs (same
  * guide, section "Model data type") with fp32 accumulation.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
- * - Layouts are contiguous, row-major, head dimension innermost:
+ * - Layouts are contiguous (where an entry point takes no strides), row-major,
+ *   head dimension innermost:
  *     q, o   [B, H, Nq, d] bf16          k, v   [B, H, Nk, d] bf16
  *     (q, k, v are one-byte e4m3 codes in the fp8 entry points; o stays bf16)
  *     lse    [B, H, Nq]    fp32, natural log

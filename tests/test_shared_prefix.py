@@ -87,6 +87,15 @@ def test_more_pairs_than_ctas():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Bn,Hkv,Nt", [(20, 8, 16), (37, 4, 40), (3, 2, 700), (61, 8, 129)])
+@pytest.mark.parametrize("Np", [0, 150])
+def test_short_tails_in_many_parts(Bn, Hkv, Nt, Np):
+    """About as many units of work as parts: parts that hold a tail's start alone,
+    tails that are cut before each of their tiles."""
+    _case(Bn, Hkv, Hkv, 1, Np, Nt, 64, [(b * 17) % Nt + 1 for b in range(Bn)], seed=18)
+
+
+@pytest.mark.gpu
 def test_two_streams_at_once():
     """Calls that overlap on the GPU, each with a workspace of its own."""
     cases = [(_rand((20, 4, 1, 64), 10 * i, 2.0), *(_rand((2, 3000, 64), 10 * i + j) for j in (1, 2)),
@@ -276,19 +285,29 @@ def _line(total_tiles, ctas):
     return [(c * q + min(c, r), (c + 1) * q + min(c + 1, r)) for c in range(parts)]
 
 
+@pytest.mark.parametrize("start", [0, 1])
 @pytest.mark.parametrize("segs", [[3, 1, 4, 1, 5], [0, 0, 7, 0], [1] * 400, [1000], [37, 0, 2, 511, 1]])
 @pytest.mark.parametrize("ctas", [1, 5, 148])
-def test_pieces_have_slots_of_their_own(segs, ctas):
-    """The arithmetic that places partial results: cut the line of key tiles into
-    equal parts, name a piece by segment + CTA, and no two pieces share a name,
-    none is past segments + CTAs, and every tile is in one piece."""
-    total, at, seen, tiles = sum(segs), 0, set(), 0
+def test_pieces_have_slots_of_their_own(segs, ctas, start):
+    """The arithmetic that places partial results: cut the line of key tiles (with
+    ``start`` units before each segment that has any) into equal parts, name a
+    piece by segment + part, and no two pieces share a name, none is past
+    segments + parts, every tile is in one piece, and the parts that hold a
+    segment's first and last tile and those between are those with a piece of it."""
+    total, at, seen, tiles = sum(n + start for n in segs if n), 0, set(), 0
+    line = _line(total, ctas)
     for s, n in enumerate(segs):
-        for c, (u0, u1) in enumerate(_line(total, ctas)):
+        at += start if n else 0
+        with_piece = []
+        for c, (u0, u1) in enumerate(line):
             t0, t1 = max(u0 - at, 0), min(u1 - at, n)
             if t0 < t1:
                 assert s + c not in seen and s + c < len(segs) + ctas
                 seen.add(s + c)
                 tiles += t1 - t0
+                with_piece.append(c)
+        if n:
+            holder = [next(c for c, (u0, u1) in enumerate(line) if u0 <= u < u1) for u in (at, at + n - 1)]
+            assert with_piece == list(range(holder[0], holder[1] + 1))
         at += n
-    assert tiles == total
+    assert tiles == sum(segs)
