@@ -11,9 +11,9 @@
 // K/V head, or one request's tail under one K/V head.  Two row tiles over the
 // same prefix make a pair, which shares its K and V tiles; what is left (the
 // prefix under an odd row tile, and the tails) is single.  The singles form a line
-// of key tiles (128 keys), and one more unit for the start of each tail, cut into
-// equal parts, one for each of the two streams (a softmax warpgroup, its MMA and
-// its load warp) of the CTAs that take singles.
+// of key tiles (128 keys), and in some calls one more unit for the start of each
+// tail (start_units), cut into equal parts, one for each of the two streams (a
+// softmax warpgroup, its MMA and its load warp) of the CTAs that take singles.
 // The other CTAs take pairs, as many CTAs a pair: CTA c has pair c mod (pairs), and
 // the prefix, cut into equal parts, part c / (pairs) of it, so that the CTAs of
 // one part read the same tiles at the same time and HBM gives them once (with
@@ -34,9 +34,9 @@
 // the tile's keys, with zero weights for the rest.  One warp working through 128
 // keys a row took longer than the tile's loads: 4.5 TB/s where the copies reached
 // 5.6 (24 heads, 119056 keys, 21 rows).  The copies' results are joined like those
-// of different pieces.  A tail's start counts as a tile on the line because with
-// tiles alone the streams at its end had some forty short tails each and finished
-// 60 us behind the others: 270 us, now 222 for 1.47 GB, 6.6 TB/s.
+// of different pieces.  Without starts on the line, the streams at its end had some
+// forty short tails each there and finished 60 us behind the others; with them the
+// kernel takes 222 us for 1.47 GB, 6.6 TB/s.
 //
 // Warps: 0-3, 4-7 softmax of stream 0 and 1 (208 registers); 8, 11 MMA issue of
 // stream 0 and 1 (8 issues for both in a pair CTA); 9, 10 pieces and TMA loads
@@ -100,13 +100,11 @@ struct Plan {
   __host__ __device__ static int copies(int n) { return n <= 32 ? 4 : n <= 64 ? 2 : 1; }
   __device__ int len(int b) const { return min(max(__ldg(tail_lens + b), 0), Nt); }
   __device__ static int tiles_of(int keys) { return (keys + kBN - 1) / kBN; }
-  // Units of the line that a tail of so many key tiles has under one K/V head: its
-  // tiles behind one for its start.
-  __device__ static int tail_units(int tiles) { return tiles + (tiles > 0); }
-  // CTAs that take pairs, given the units (under one K/V head) of all tails.
-  __device__ int pair_ctas(int tails) const {
+  // CTAs that take pairs, given the key tiles (under one K/V head) of all tails
+  // and the number of tails that have any; a tail's start costs about a tile.
+  __device__ int pair_ctas(int tiles, int tails) const {
     const long long p = static_cast<long long>(pair_units()) * kPairCost;
-    const long long s = (odd_units() + tails * static_cast<long long>(Hkv)) * kSingleCost;
+    const long long s = (odd_units() + (tiles + tails) * static_cast<long long>(Hkv)) * kSingleCost;
     if (p == 0) return 0;
     if (s == 0) return ctas <= pairs() ? ctas : ctas - ctas % pairs();
     // Rounded the same way in both kernels.
@@ -114,6 +112,13 @@ struct Plan {
     const int n = min(max(__float2int_rn(__fmul_rn(static_cast<float>(ctas), share)), 1), ctas - 1);
     return n <= pairs() ? n : n - n % pairs();  // as many for every pair
   }
+  // Units of the line before a tail's own tiles, for its start: one where the prefix
+  // has more row tiles x key tiles than the tails (`tiles` of them).  Counted and
+  // not: 7 requests of 119056 + 333 keys 234 and 258 us, 32 of 32768 + 300 52 and 57,
+  // 128 on pairs of 32768 + 1024 132 and 142.  Where tails are most of the work,
+  // HBM evens out their starts, and a coarser line only costs: 100 requests of
+  // 1000 + 600 47 and 41, 128 of 100 + 2000 75 and 73, 32 of 4608 + 1152 35 and 33.
+  __device__ int start_units(int tiles) const { return row_tiles * prefix_tiles >= tiles ? 1 : 0; }
 };
 
 struct Params {
@@ -365,17 +370,23 @@ __global__ void __launch_bounds__(R::kThreads, 1)
   }
   // The load warps reckon while the barriers and tensor memory are set up: all
   // units of tails under one K/V head, and the CTAs that take pairs.
-  int tails = 0, pair_ctas = 0;
+  int tails = 0, pair_ctas = 0, start = 0;
   if (warp == kLoadWarp || warp == kLoadWarp + 1) {
+    int some = 0;
     for (int b0 = 0; b0 < plan.B; b0 += 128) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int b = b0 + u * 32 + lane;
-        if (b < plan.B) tails += Plan::tail_units(Plan::tiles_of(plan.len(b)));
+        const int n = b < plan.B ? Plan::tiles_of(plan.len(b)) : 0;
+        tails += n;
+        some += n > 0;
       }
     }
     tails = __reduce_add_sync(0xffffffffu, tails);
-    pair_ctas = plan.pair_ctas(tails);
+    some = __reduce_add_sync(0xffffffffu, some);
+    pair_ctas = plan.pair_ctas(tails, some);
+    start = plan.start_units(tails);
+    tails += start * some;
   }
   if (warp == kLoadWarp && lane == 0) {
     prefetch_tensormap(&tm_qp);
@@ -530,7 +541,7 @@ __global__ void __launch_bounds__(R::kThreads, 1)
       for (int b0 = 0; b0 < plan.B && at < u1 && ok; b0 += 32) {
         const int n = b0 + lane < plan.B ? plan.len(b0 + lane) : 0;
         const int nt = Plan::tiles_of(n);
-        const int nu = Plan::tail_units(nt);
+        const int nu = nt > 0 ? nt + start : 0;
         int upto = nu;  // inclusive scan
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -546,8 +557,8 @@ __global__ void __launch_bounds__(R::kThreads, 1)
           todo &= todo - 1;
           const int a0 = __shfl_sync(0xffffffffu, mine0, k);
           const int kn = __shfl_sync(0xffffffffu, n, k), knt = __shfl_sync(0xffffffffu, nt, k);
-          for (int hk = max(u0 - a0, 0) / (knt + 1); hk < plan.Hkv && ok; ++hk) {
-            const int a = a0 + hk * (knt + 1) + 1;  // the first tile's place
+          for (int hk = max(u0 - a0, 0) / (knt + start); hk < plan.Hkv && ok; ++hk) {
+            const int a = a0 + hk * (knt + start) + start;  // the first tile's place
             if (a >= u1) break;
             if (a + knt > u0)
               run(kTail, hk, b0 + k, max(u0 - a, 0), min(u1 - a, knt), (b0 + k) * plan.Hkv + hk + c, kn);
@@ -849,26 +860,30 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const
   const int req = blockIdx.x / plan.Hkv, hk = blockIdx.x % plan.Hkv;
 
   if (warp == 0) {
-    // Units of all tails (under one K/V head), and of those before req.
-    int all = 0, before = 0;
+    // Key tiles of all tails (under one K/V head) and of those before req, and how
+    // many of them have any.
+    int all = 0, before = 0, some = 0, some_before = 0;
     for (int b0 = 0; b0 < plan.B; b0 += 128) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int b = b0 + u * 32 + lane;
         if (b >= plan.B) continue;
-        const int n = Plan::tail_units(Plan::tiles_of(plan.len(b)));
+        const int n = Plan::tiles_of(plan.len(b));
         all += n;
-        if (b < req) before += n;
+        some += n > 0;
+        if (b < req) before += n, some_before += n > 0;
         if (blockIdx.x == 0 && __ldg(plan.tail_lens + b) != plan.len(b)) atomicCAS(p.status, 0, kStatusBadInput);
       }
     }
     all = __reduce_add_sync(0xffffffffu, all);
     before = __reduce_add_sync(0xffffffffu, before);
+    some = __reduce_add_sync(0xffffffffu, some);
+    some_before = __reduce_add_sync(0xffffffffu, some_before);
 
     // Parts [p0, p1) of the pairs' or the singles' line hold the prefix under this
     // row tile, [t0, t1) of the singles' the tail.
     const int n_tail = Plan::tiles_of(plan.len(req));
-    const int pair_ctas = plan.pair_ctas(all);
+    const int pair_ctas = plan.pair_ctas(all, some), start = plan.start_units(all);
     const int mt = req / plan.tile_reqs;
     const bool pair = mt < 2 * plan.pairs();
     const int copies_p = pair ? 1 : Plan::copies(plan.tile_rows()), copies_t = Plan::copies(plan.rows);
@@ -876,7 +891,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const
     // on the singles'.
     const int lanes = pair ? plan.lanes(pair_ctas) : 1, my_lane = pair ? mt / 2 % lanes : 0;
     const int seg_p = pair ? mt / 2 / lanes * plan.Hkv + hk : hk, seg_t = req * plan.Hkv + hk;
-    const Cut singles(plan.odd_units() + all * plan.Hkv, 2 * (plan.ctas - pair_ctas));
+    const Cut singles(plan.odd_units() + (all + start * some) * plan.Hkv, 2 * (plan.ctas - pair_ctas));
     int p0 = 0, p1 = 0, t0 = 0, t1 = 0;
     if (plan.row_tiles > 0) {
       const Cut cut = pair ? Cut(plan.lane_pairs(lanes, my_lane) * plan.Hkv * plan.prefix_tiles, pair_ctas / lanes)
@@ -885,7 +900,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const
       p1 = cut.holder((seg_p + 1) * plan.prefix_tiles - 1) + 1;
     }
     if (n_tail > 0) {
-      const int at = plan.odd_units() + before * plan.Hkv + hk * (n_tail + 1) + 1;
+      const int at = plan.odd_units() + (before + start * some_before) * plan.Hkv + hk * (n_tail + start) + start;
       t0 = singles.holder(at);
       t1 = singles.holder(at + n_tail - 1) + 1;
     }

@@ -88,10 +88,11 @@ def test_more_pairs_than_ctas():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("Bn,Hkv,Nt", [(20, 8, 16), (37, 4, 40), (3, 2, 700), (61, 8, 129)])
-@pytest.mark.parametrize("Np", [0, 150])
+@pytest.mark.parametrize("Np", [0, 150, 8000])
 def test_short_tails_in_many_parts(Bn, Hkv, Nt, Np):
-    """About as many units of work as parts: parts that hold a tail's start alone,
-    tails that are cut before each of their tiles."""
+    """About as many units of work as parts, and with the long prefix the tails'
+    starts among them: parts that hold a start alone, tails that are cut before
+    each of their tiles."""
     _case(Bn, Hkv, Hkv, 1, Np, Nt, 64, [(b * 17) % Nt + 1 for b in range(Bn)], seed=18)
 
 
