@@ -41,7 +41,7 @@
 // causal keys, 24 heads: 430 us, FMA 56 % busy, special-function unit and tensor
 // pipe 48 %); with short documents an item's start and end, some 8 000 clocks beside
 // the 5 000 to 7 500 of a tile that the mask cuts (8192 keys in 24 documents, 24
-// heads, biased: 115 us, tensor pipe 25 % busy).
+// heads, biased: 110 us, tensor pipe 25 % busy).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -78,6 +78,7 @@ struct FwdModParams {
   int B, Hq, G;                              // G = Hq / Hkv
   int Nq, Nk;
   int items, blocks_per_bh;
+  bool by_order;  // items in PairOrder's order
   int q_offset;
   int causal;
   const int* prefix;  // [B, max(n_docs, 1)] or null
@@ -119,6 +120,68 @@ __device__ __forceinline__ int2 row_interval(const FwdModParams& p, int b, int p
   }
   return make_int2(lo, hi);
 }
+
+// With documents, the (row block, batch) pairs in the order of the keys their rows
+// span, the most first, so that the long items start first whatever the documents
+// are.  Every scheduler reckons the same order: lane l holds the ranks of pairs
+// l, l + 32, ..  Without and with it, 24 heads: 8192 keys in 24 documents 115 and
+// 110 us, seen in both directions 181 and 164, in 8 documents 174 and 161, 2 x 4603
+// keys in 3 documents 272 and 234.  Ranking takes a microsecond or two at the start,
+// which it does not give back with
+//  - more than kMax pairs: there are many items a CTA then (128 pairs: 400 and 404)
+//  - fewer than two items an SM (192 items: 33 and 35)
+//  - more documents than row blocks: items are much alike (96 documents on 32
+//    blocks: 83 and 85).
+struct PairOrder {
+  static constexpr int kPer = 2, kMax = 32 * kPer;
+  static bool pays(int pairs, int blocks, int n_docs, int items, int sms) {
+    return n_docs > 0 && pairs <= kMax && items >= 2 * sms && n_docs <= blocks;
+  }
+  int rank[kPer];
+
+  __device__ __forceinline__ void reckon(const FwdModParams& p, int pairs) {
+    const int lane = threadIdx.x % 32;
+    int key[kPer];  // the pair's key tiles, then its place from the end: no two alike
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const int e = u * 32 + lane;
+      key[u] = -1;
+      rank[u] = e < pairs ? 0 : -1;
+      if (e >= pairs) continue;
+      const int b = e % p.B, row0 = (p.blocks_per_bh - 1 - e / p.B) * (kQTiles * kBM);
+      const int pos0 = row0 + p.q_offset, pos1 = min(row0 + kQTiles * kBM, p.Nq) - 1 + p.q_offset;
+      const int* off = p.docs + static_cast<long long>(b) * (p.n_docs + 1);
+      const int t0 = find_doc(off, pos0, -1, p.n_docs), t1 = find_doc(off, pos1, t0, p.n_docs);
+      key[u] = kMax - 1 - e;
+      if (t1 < 0 || t0 >= p.n_docs) continue;
+      const int lo = row_interval(p, b, pos0, max(t0, 0)).x;
+      const int hi = row_interval(p, b, pos1, min(t1, p.n_docs - 1)).y;
+      key[u] += max(hi - lo, 0) / kBN * kMax;
+    }
+#pragma unroll
+    for (int v = 0; v < kPer; ++v) {
+      if (v * 32 >= pairs) break;
+#pragma unroll 8
+      for (int l = 0; l < 32; ++l) {
+        const int other = __shfl_sync(0xffffffffu, key[v], l);
+#pragma unroll
+        for (int u = 0; u < kPer; ++u)
+          if (key[u] >= 0) rank[u] += other > key[u];
+      }
+    }
+  }
+  // The item in the n-th place, heads of a pair side by side.
+  __device__ __forceinline__ int item(int n, int Hq) const {
+    const int g = n / Hq;
+    int e = 0;
+#pragma unroll
+    for (int u = 0; u < kPer; ++u) {
+      const unsigned at = __ballot_sync(0xffffffffu, rank[u] == g);
+      if (at != 0u) e = u * 32 + __ffs(at) - 1;
+    }
+    return e * Hq + n % Hq;
+  }
+};
 
 // What the scheduler tells the other warps about an item (item < 0: no more).
 struct ItemSlot {
@@ -245,6 +308,9 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), kTmemCols);
     tmem_relinquish();
   }
+  // The scheduler reckons while the barriers and tensor memory are set up.
+  PairOrder order;
+  if (warp == R::kSched && p.by_order) order.reckon(p, p.blocks_per_bh * p.B);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -308,8 +374,9 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
         if (lane == 0) mbar_arrive(bar_item_full);
         break;
       }
-      // Items run from the last query rows to the first: with a causal mask the
-      // long ones come first.
+      // Items run from the last query rows to the first (with a causal mask the
+      // long ones come first), or in the order reckoned.
+      if (p.by_order) item = order.item(item, p.Hq);
       const int bh = item % (p.B * p.Hq);
       const int row0 = (p.blocks_per_bh - 1 - item / (p.B * p.Hq)) * (kQTiles * kBM);
       const int b = bh / p.Hq;

@@ -80,10 +80,9 @@ struct DeviceState {
   unsigned char* noalloc_scratch = nullptr;  // device address of pa::g_noalloc_scratch
   bool fwd_attr[5] = {};  // d = 64, d = 128, e4m3 d = 128, accumulate d = 64, accumulate d = 128
   bool mod_attr[8] = {};  // modified scores: 4 * (d = 128) + 2 * capped + biased
-  bool wide_attr[2] = {};    // capped with the fixed reference: d = 64, d = 128
-  bool shared_attr[8] = {};  // shared prefix: the same
+  bool wide_attr[2] = {};  // capped with the fixed reference: d = 64, d = 128
+  bool shared_attr[8] = {};  // shared prefix: 4 * (d = 128) + 2 * capped + biased
 };
-
 
 std::mutex g_mu;
 DeviceState g_dev[kMaxDevices];
@@ -825,6 +824,8 @@ int pa_attn_fwd_mod(const void* q, const void* k, const void* v, void* o, float*
   const long long items = static_cast<long long>(prm.blocks_per_bh) * B * Hq;
   if (items > 0x3fffffffLL) return fail(PA_ERR_UNSUPPORTED, "too many query blocks");
   prm.items = static_cast<int>(items);
+  prm.by_order =
+      pa::mod::PairOrder::pays(prm.blocks_per_bh * B, prm.blocks_per_bh, n_docs, prm.items, st->sm_count);
   prm.q_offset = mod->q_offset;
   prm.causal = mod->causal != 0;
   prm.prefix = mod->prefix_lens;

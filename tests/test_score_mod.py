@@ -324,6 +324,29 @@ def test_oracle_masks_by_hand():
     assert o[0, 0] == 5.0 and abs(lse[0] - (2.0 * math.tanh(1.5) - 0.25)) < 1e-15
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("Bn,Hq,Nq,Nk,d", [(2, 20, 2100, 2100, 64), (7, 8, 2300, 2300, 64), (1, 36, 2400, 3001, 128)])
+@pytest.mark.parametrize("kw", [dict(), dict(causal=True), dict(causal=True, softcap=4.0), dict(slopes=True)], ids=str)
+def test_many_heads_take_the_same_values_as_few(Bn, Hq, Nq, Nk, d, kw):
+    """The order in which items are worked on (longest first with many items and
+    few documents) changes no bit: all heads at once against the first two alone,
+    which is too few items to order."""
+    q, k, v = _rand((Bn, Hq, Nq, d), 31, 2.0), _rand((Bn, Hq // 2, Nk, d), 32), _rand((Bn, Hq // 2, Nk, d), 33)
+    cuts = [[0, 0, 5 + 37 * b, 700, 700 + 130 * b, Nk - 700, Nk - 40 * b] for b in range(Bn)]
+    kw = dict(kw, doc_offsets=torch.tensor(cuts, dtype=torch.int32, device="cuda"))
+    few = dict(kw)
+    if kw.pop("slopes", False):
+        kw["slopes"] = _slopes(Hq)
+        few["slopes"] = kw["slopes"][:2].contiguous()
+    o, lse = pa.attn_fwd_mod(q, k, v, check=True, **kw)
+    o2, lse2 = pa.attn_fwd_mod(q[:, :2], k[:, :1], v[:, :1], check=True, **few)
+    assert torch.equal(o[:, :2], o2) and torch.equal(lse[:, :2], lse2)
+    assert torch.isfinite(o.float()).all()
+    some = torch.isfinite(lse[:, 0]).sum(-1).tolist()
+    at = [range(Nk - Nq, Nk)] * Bn
+    assert some == [sum(c[0] <= p < c[-1] for p in r) for c, r in zip(cuts, at)]
+
+
 def test_tanh_polynomial_matches_its_fit_and_bound():
     import os
     import re
