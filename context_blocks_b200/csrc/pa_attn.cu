@@ -634,13 +634,15 @@ int launch_shared(DeviceState* st, const CUtensorMap (&maps)[6], const pa::share
   const int rc = ready_kernel(kern, &st->shared_attr[4 * (D == 128) + 2 * kCap + kBias], L::kAllocBytes,
                               pa::shared::R::kLaunchRegs, "shared-prefix");
   if (rc != PA_OK) return rc;
-  if (prm.plan.Np > 0 || prm.plan.Nt > 0)
+  const bool keys = prm.plan.Np > 0 || prm.plan.Nt > 0;
+  if (keys)
     kern<<<prm.plan.ctas, pa::shared::R::kThreads, L::kAllocBytes, stream>>>(maps[0], maps[1], maps[2], maps[3],
                                                                              maps[4], maps[5], prm);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "attn_shared launch");
   // Launched while the first kernel runs (the merge waits for its results), so
-  // that the launch and the merge's own reckoning cost no time between the two.
+  // that the launch and the merge's own reckoning cost no time between the two;
+  // behind a kernel of the caller's, which may still write the lengths, it is not.
   cudaLaunchAttribute overlap;
   overlap.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   overlap.val.programmaticStreamSerializationAllowed = 1;
@@ -649,7 +651,7 @@ int launch_shared(DeviceState* st, const CUtensorMap (&maps)[6], const pa::share
   cfg.blockDim = dim3(pa::shared::merge_warps(prm.plan) * 32);
   cfg.stream = stream;
   cfg.attrs = &overlap;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = keys ? 1 : 0;
   e = cudaLaunchKernelEx(&cfg, pa::shared::shared_merge_kernel<D>, prm, static_cast<__nv_bfloat16*>(o), lse);
   if (e != cudaSuccess) return cuda_fail(e, "attn_shared launch");
   return PA_OK;
