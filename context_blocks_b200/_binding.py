@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -349,7 +350,7 @@ def _check_rows(name, t, ndim, index=None):
     try:
         at = t.get_device()
         if (t.dtype is _t.bf16 and at >= 0 and (index is None or at == index) and t.dim() == ndim
-                and (t.stride(-1) == 1 or t.shape[-1] <= 1)):
+                and (t.is_contiguous() or t.stride(-1) == 1 or t.shape[-1] <= 1)):
             return at
     except AttributeError:
         pass
@@ -406,6 +407,7 @@ def attn_fwd_mod(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, s
         shape = (B, n_docs) if n_docs else (B, 1) if prefix_lens.dim() == 2 else (B,)
         mod.prefix_lens = _check_vector("prefix_lens", prefix_lens, _t.i32, shape, index)
     fresh = out is None
+    lse_at = None if lse is None else _check_vector("lse", lse, _t.f32, (B, Hq, Nq), index)
     if fresh or lse is None:
         with _nullcontext if stream is None else _on_stream(stream, q.device):
             if out is None:
@@ -414,6 +416,7 @@ def attn_fwd_mod(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, s
                     out = q.new_empty(q_shape)
             if lse is None:
                 lse = q.new_empty((B, Hq, Nq), dtype=_t.f32)
+                lse_at = lse.data_ptr()
     if not fresh:
         _check_rows("out", out, 4, index)
         if out.shape != q_shape:
@@ -421,10 +424,9 @@ def attn_fwd_mod(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, s
     strides = None
     if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()):
         strides = _Strides12(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *out.stride()[:3])
-    rc = load_library().pa_attn_fwd_mod(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-                                         _check_vector("lse", lse, _t.f32, (B, Hq, Nq), index), B, Hq, Hkv, Nq,
-                                         Nk, d, strides, 1.0 / math.sqrt(d) if scale is None else scale,
-                                         ctypes.byref(mod), _stream_handle(stream, index))
+    rc = load_library().pa_attn_fwd_mod(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse_at, B, Hq, Hkv,
+                                        Nq, Nk, d, strides, 1.0 / math.sqrt(d) if scale is None else scale,
+                                        ctypes.byref(mod), _stream_handle(stream, index))
     if rc or check:
         _check(rc, "pa_attn_fwd_mod", check)
     return out, lse
@@ -433,6 +435,10 @@ def attn_fwd_mod(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, s
 def shared_prefix_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Np: int, Nt: int, d: int) -> int:
     """Bytes of workspace ``attn_shared_prefix`` needs for these sizes."""
     return int(load_library().pa_attn_shared_prefix_workspace(B, Hq, Hkv, Nq, Np, Nt, d))
+
+
+# A function of the sizes alone, asked for in every decoding step.
+_workspace_bytes = functools.lru_cache(maxsize=256)(shared_prefix_workspace_bytes)
 
 
 def attn_shared_prefix(q, k_prefix, v_prefix, k_tail, v_tail, tail_lens, scale: Optional[float] = None,
@@ -465,15 +471,17 @@ def attn_shared_prefix(q, k_prefix, v_prefix, k_tail, v_tail, tail_lens, scale: 
     sl = _check_vector("slopes", slopes, _t.f32, (Hq,), index)
     lib = load_library()
     fresh, own_space = out is None, workspace is None
+    lse_at = None if lse is None else _check_vector("lse", lse, _t.f32, (B, Hq, Nq), index)
     if fresh or own_space or lse is None:
         with _nullcontext if stream is None else _on_stream(stream, q.device):
             if out is None:
                 out = _t.empty_like(q)
             if lse is None:
                 lse = q.new_empty((B, Hq, Nq), dtype=_t.f32)
+                lse_at = lse.data_ptr()
             if own_space:
                 # in bf16 elements of q: one allocation without a type to look up
-                workspace = q.new_empty((lib.pa_attn_shared_prefix_workspace(B, Hq, Hkv, Nq, Np, Nt, d) // 2,))
+                workspace = q.new_empty((_workspace_bytes(B, Hq, Hkv, Nq, Np, Nt, d) // 2,))
     if not fresh:
         _check_rows("out", out, 4, index)
         if out.shape != q_shape or not out.is_contiguous():
@@ -487,9 +495,8 @@ def attn_shared_prefix(q, k_prefix, v_prefix, k_tail, v_tail, tail_lens, scale: 
         strides = _Strides10(*k_prefix.stride()[:2], *v_prefix.stride()[:2], *k_tail.stride()[:3],
                              *v_tail.stride()[:3])
     rc = lib.pa_attn_shared_prefix(q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), k_tail.data_ptr(),
-                                   v_tail.data_ptr(), lens, out.data_ptr(),
-                                   _check_vector("lse", lse, _t.f32, (B, Hq, Nq), index), B, Hq, Hkv, Nq, Np,
-                                   Nt, d, strides, 1.0 / math.sqrt(d) if scale is None else scale, softcap, sl,
+                                   v_tail.data_ptr(), lens, out.data_ptr(), lse_at, B, Hq, Hkv, Nq, Np, Nt, d,
+                                   strides, 1.0 / math.sqrt(d) if scale is None else scale, softcap, sl,
                                    workspace.data_ptr(), workspace.numel() * workspace.element_size(),
                                    _stream_handle(stream, index))
     if rc or check:
