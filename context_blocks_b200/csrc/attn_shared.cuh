@@ -795,9 +795,12 @@ __global__ void __launch_bounds__(R::kThreads, 1)
         store_raw_row<D>(tO, o + lane * D, mine);
       else
         store_raw_rows<D>(tO, base + L::kStageOff + warp * L::kStageWarpBytes, o, rows - wr);
+      // The merge takes m = -inf for a part in which the row saw nothing (l = 0).  A
+      // maximum skips NaN, so where all scores of a part are NaN m_ref has not
+      // moved while l is NaN: such a part gets a finite m, and its l reaches the row.
       if (mine)
         (x.kind == kPair ? p.pair_ml : x.kind == kOdd ? p.odd_ml : p.tail_ml)[row0 + r] =
-            make_float2(l == 0.f ? -INFINITY : m_ref, l);
+            make_float2(l == 0.f ? -INFINITY : m_ref == -INFINITY ? 0.f : m_ref, l);
       // A value row that is not finite among the new tokens of a request does
       // not reach the tokens before it (see repair_row).
       if (x.kind == kTail && plan.Nq > 1) {

@@ -1,0 +1,83 @@
+"""NaN, Inf and very large numbers in the operands of attn_fwd_mod and
+attn_shared_prefix: they reach the rows that see them, as in the formulas, and
+no others.
+
+Tolerances as derived in tests/test_score_mod.py: 2^-7 max|v| of the visible
+values on O, 3e-4 on LSE.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import context_blocks_b200 as pa
+from oracle import score_mod as oracle
+from tests.test_score_mod import LSE_ABS, _rand, _slopes
+
+NAN, INF = float("nan"), float("inf")
+
+# Plain, capped against the fixed reference, capped with a running maximum, biased, both.
+FORMS = [dict(), dict(softcap=4.0), dict(softcap=60.0), dict(slopes=True), dict(softcap=4.0, slopes=True)]
+
+
+def check_same(o, lse, o_ref, l_ref, v_max):
+    """Equal to the oracle within the tolerances where it is finite, NaN where it
+    is NaN, the same infinity where it is infinite."""
+    o, lse = o.float().cpu().double().numpy(), lse.cpu().double().numpy()
+    for got, want, tol in ((o, o_ref, 2.0 ** -7 * v_max), (lse, l_ref, LSE_ABS)):
+        fin = np.isfinite(want)
+        assert np.array_equal(np.isnan(got), np.isnan(want))
+        assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+        assert np.isfinite(got[fin]).all()
+        assert not fin.any() or np.abs(got[fin] - want[fin]).max() <= tol
+
+
+def _shared(q, kp, vp, kt, vt, lens, kw, v_max):
+    Hq, d = q.shape[1], q.shape[3]
+    args = dict(kw, slopes=_slopes(Hq)) if kw.get("slopes") else kw
+    host = dict(args, slopes=args["slopes"].cpu().numpy()) if kw.get("slopes") else kw
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = pa.attn_shared_prefix(q, kp, vp, kt, vt, n, check=True, **args)
+    with np.errstate(invalid="ignore"):
+        o_ref, l_ref = oracle.shared_prefix(q, kp, vp, kt, vt, lens, d ** -0.5, **host)
+    check_same(o, lse, o_ref, l_ref, v_max)
+    return o, lse
+
+
+# Rows of a request under one K/V head, and of a row tile, in 4, 2 and 1 copies;
+# two row tiles (a pair), three (a pair and an odd one).
+ROWS = [(3, 4, 1), (3, 16, 1), (2, 48, 1), (2, 80, 1), (1, 100, 1), (30, 8, 1), (40, 8, 1), (5, 4, 3), (2, 7, 14)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", FORMS, ids=str)
+@pytest.mark.parametrize("Bn,G,Nq", ROWS)
+@pytest.mark.parametrize("Np", [0, 300])
+def test_nan_in_queries_and_new_keys_of_a_decoding_step(Np, Bn, G, Nq, kw):
+    """A NaN query row; a request whose only key of its own is NaN; one whose last
+    key is, alone in its key tile.  The other requests are as without them."""
+    q, kp, vp = _rand((Bn, 2 * G, Nq, 64), 1, 2.0), _rand((2, Np, 64), 2), _rand((2, Np, 64), 3)
+    kt, vt = _rand((Bn, 2, 140, 64), 4), _rand((Bn, 2, 140, 64), 5)
+    lens = [max(Nq, (1, 129, 70)[b % 3]) for b in range(Bn)]
+    _shared(q, kp, vp, kt, vt, lens, kw, 6.0)
+    q2 = q.clone()
+    q2[Bn // 2, 1, Nq - 1] = NAN
+    _shared(q2, kp, vp, kt, vt, lens, kw, 6.0)
+    for b in range(min(Bn, 2)):
+        k2 = kt.clone()
+        k2[b, 1, lens[b] - 1] = NAN
+        _shared(q, kp, vp, k2, vt, lens, kw, 6.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", FORMS, ids=str)
+@pytest.mark.parametrize("Bn,G,Nq", ROWS)
+def test_nan_key_in_the_prefix(Bn, G, Nq, kw):
+    """All rows under its K/V head are NaN, wherever it stands: alone in the last
+    key tile, among others, and alone in the prefix."""
+    for Np, at in ((257, 256), (257, 40), (1, 0)):
+        q, kp, vp = _rand((Bn, 2 * G, Nq, 64), 1, 2.0), _rand((2, Np, 64), 2), _rand((2, Np, 64), 3)
+        kt, vt = _rand((Bn, 2, 16, 64), 4), _rand((Bn, 2, 16, 64), 5)
+        kp[1, at] = NAN
+        o, lse = _shared(q, kp, vp, kt, vt, [min(16, Nq + b % 3) for b in range(Bn)], kw, 6.0)
+        assert torch.isnan(lse[:, G:]).all() and not torch.isnan(lse[:, :G]).any()
