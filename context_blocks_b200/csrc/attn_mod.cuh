@@ -697,8 +697,8 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
         const int hk = hq / p.G;
         repair_row<D, kCols>(p.q + bt * p.q_s[0] + hq * p.q_s[1] + (wrow + k) * p.q_s[2],
                              p.k + bt * p.k_s[0] + hk * p.k_s[1], p.v + bt * p.v_s[0] + hk * p.v_s[1] + half * kCols,
-                             p.k_s[2], p.v_s[2], j0, j1, 1, 1, 0, wrow + k + p.q_offset, mr, iv, slope2, p.sm, kCap,
-                             kBias, o + k * p.o_s[2], nullptr);
+                             p.k_s[2], p.v_s[2], j0, j1, wrow + k + p.q_offset, mr, iv, slope2, p.sm, kCap, kBias,
+                             o + k * p.o_s[2]);
       }
     }
   }

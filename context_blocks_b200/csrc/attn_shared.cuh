@@ -123,10 +123,14 @@ struct Plan {
 
 struct Params {
   Plan plan;
+  // The operands as they lie in memory, for the merge's redo_row.
   const __nv_bfloat16* q;
+  const __nv_bfloat16* kp;
+  const __nv_bfloat16* vp;
   const __nv_bfloat16* kt;
   const __nv_bfloat16* vt;
-  long long kt_s[3], vt_s[3];  // tail strides: batch, head, row (elements)
+  long long kp_s[2], vp_s[2];  // prefix strides: head, row (elements)
+  long long kt_s[3], vt_s[3];  // tail strides: batch, head, row
   float* pair_o;               // [((segments of a lane + parts) * lanes) * 2][tile_rows][D]
   float2* pair_ml;
   float* odd_o;                // [(Hkv + 2 * ctas) * copies][tile_rows][D]
@@ -295,20 +299,6 @@ __device__ __noinline__ void store_raw_rows(uint32_t tO, uint32_t stg, float* ds
       if (r < rows_left) *reinterpret_cast<uint4*>(dst + r * D + ch * 32 + c * 4) = x;
     }
   }
-}
-
-// Whether a thread's O row is finite throughout.
-template <int D>
-__device__ __noinline__ bool row_is_finite(uint32_t tO) {
-  float sum = 0.f;  // x * 0 is NaN where x is not finite
-#pragma unroll 1
-  for (int ch = 0; ch < D / 16; ++ch) {
-    uint32_t w[16];
-    tmem_ld_x16(tO + ch * 16, w);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) sum = fmaf(__uint_as_float(w[e]), 0.f, sum);
-  }
-  return sum == 0.f;
 }
 
 template <int D, bool kCap, bool kBias>
@@ -791,35 +781,16 @@ __global__ void __launch_bounds__(R::kThreads, 1)
                                           : static_cast<size_t>(x.slot * copies + kq) *
                                                 (x.kind == kOdd ? plan.tile_rows() : plan.rows);
       float* o = (x.kind == kPair ? p.pair_o : x.kind == kOdd ? p.odd_o : p.tail_o) + (row0 + wr) * D;
-      if (copies > 1)
-        store_raw_row<D>(tO, o + lane * D, mine);
-      else
-        store_raw_rows<D>(tO, base + L::kStageOff + warp * L::kStageWarpBytes, o, rows - wr);
       // The merge takes m = -inf for a part in which the row saw nothing (l = 0).  A
       // maximum skips NaN, so where all scores of a part are NaN m_ref has not
       // moved while l is NaN: such a part gets a finite m, and its l reaches the row.
       if (mine)
         (x.kind == kPair ? p.pair_ml : x.kind == kOdd ? p.odd_ml : p.tail_ml)[row0 + r] =
             make_float2(l == 0.f ? -INFINITY : m_ref == -INFINITY ? 0.f : m_ref, l);
-      // A value row that is not finite among the new tokens of a request does
-      // not reach the tokens before it (see repair_row).
-      if (x.kind == kTail && plan.Nq > 1) {
-        unsigned redo = __ballot_sync(0xffffffffu, !row_is_finite<D>(tO) && mine && l > 0.f && l <= FLT_MAX);
-        while (redo != 0u) {
-          const int k = __ffs(redo) - 1;
-          redo &= redo - 1;
-          __syncwarp();
-          const int ps = __shfl_sync(0xffffffffu, pos, k), sn = __shfl_sync(0xffffffffu, seen, k);
-          const float mr = __shfl_sync(0xffffffffu, m_ref, k);
-          const float sl = __shfl_sync(0xffffffffu, slope2, k);
-          // Rows of a K/V head are adjacent.
-          const size_t q_row = (static_cast<size_t>(x.req) * plan.Hq + x.hk * plan.G) * plan.Nq + wr + k;
-          repair_row<D, D>(p.q + q_row * D, p.kt + x.req * p.kt_s[0] + x.hk * p.kt_s[1],
-                        p.vt + x.req * p.vt_s[0] + x.hk * p.vt_s[1], p.kt_s[2], p.vt_s[2], x.t0 * kBN,
-                        min(sn, x.t1 * kBN), kBN / copies, kBN, kq, ps, mr, 1.f, sl, p.sm, kCap, kBias, nullptr,
-                        o + k * D);
-        }
-      }
+      if (copies > 1)
+        store_raw_row<D>(tO, o + lane * D, mine);
+      else
+        store_raw_rows<D>(tO, base + L::kStageOff + warp * L::kStageWarpBytes, o, rows - wr);
     }
   }
 
@@ -837,6 +808,35 @@ __global__ void __launch_bounds__(R::kThreads, 1)
 // blocks of 52 partials a row 10.2 and 16.4, 1024 blocks 11.7 and 7.2.
 inline int merge_warps(const Plan& plan) {
   return plan.B * plan.Hkv <= 4 * plan.ctas ? kMergeWarps : kMergeWarps / 2;
+}
+
+// The columns `bad` (of lane l's D / 32) of a row's O from the keys the row sees,
+// with ref = log2 of the sum of its weights, to o.  The first kernel's matrix
+// products multiply zero weights too: those of the keys that belong to another copy
+// of the row and those of later tokens, and 0 * Inf is NaN.  So a row whose O is
+// not finite while its sum is takes those columns from here.  Rare and slow (one
+// warp, all the row's keys); nothing waits for this kernel with a limit.
+template <int D>
+__device__ __noinline__ void redo_row(const Params& p, int req, int hk, int rr, float ref, unsigned bad,
+                                      __nv_bfloat16* o) {
+  constexpr int kCols = D / 32;
+  const Plan& plan = p.plan;
+  const int lane = threadIdx.x % 32;
+  const bool cap = p.sm.cap_log2 > 0.f, bias = p.sm.slopes != nullptr;
+  const int pos = plan.len(req) - plan.Nq + rr % plan.Nq;  // counted from the tail's start
+  const float slope2 = bias ? __ldg(p.sm.slopes + hk * plan.G + rr / plan.Nq) * 1.4426950408889634f : 0.f;
+  const __nv_bfloat16* q = p.q + ((static_cast<size_t>(req) * plan.Hq + hk * plan.G) * plan.Nq + rr) * D;
+  float qv[kCols], acc[kCols];
+#pragma unroll
+  for (int u = 0; u < kCols; ++u) qv[u] = __bfloat162float(q[lane * kCols + u]), acc[u] = 0.f;
+  if (!add_keys<D, kCols>(qv, p.kp + hk * p.kp_s[0], p.vp + hk * p.vp_s[0], p.kp_s[1], p.vp_s[1], 0, plan.Np,
+                          plan.Np + pos, ref, slope2, p.sm, cap, bias, bad, acc))
+    add_keys<D, kCols>(qv, p.kt + req * p.kt_s[0] + hk * p.kt_s[1], p.vt + req * p.vt_s[0] + hk * p.vt_s[1],
+                       p.kt_s[2], p.vt_s[2], 0, min(max(pos + 1, 0), plan.len(req)), pos, ref, slope2, p.sm, cap, bias,
+                       bad, acc);
+#pragma unroll
+  for (int u = 0; u < kCols; ++u)
+    if ((bad >> u) & 1u) o[lane * kCols + u] = __float2bfloat16(acc[u]);
 }
 
 // Joins the partial results of every row:
@@ -1012,15 +1012,23 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const
       const size_t row = (static_cast<size_t>(req) * plan.Hq + hk * plan.G) * plan.Nq + rr;
       const bool none = l == 0.f;
       const float inv = none ? 0.f : 1.f / l;
+      unsigned bad = 0u;  // columns that are not finite
+#pragma unroll
+      for (int u = 0; u < kCols; ++u) {
+        acc[u] *= inv;
+        if (!(fabsf(acc[u]) <= FLT_MAX)) bad |= 1u << u;
+      }
       if constexpr (D == 128) {
         uint2 v;
-        v.x = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-        v.y = pack_bf16x2(acc[2] * inv, acc[3] * inv);
+        v.x = pack_bf16x2(acc[0], acc[1]);
+        v.y = pack_bf16x2(acc[2], acc[3]);
         *reinterpret_cast<uint2*>(o + row * D + lane * kCols) = v;
       } else {
-        *reinterpret_cast<uint32_t*>(o + row * D + lane * kCols) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+        *reinterpret_cast<uint32_t*>(o + row * D + lane * kCols) = pack_bf16x2(acc[0], acc[1]);
       }
       if (lane == 0) lse[row] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+      if (__any_sync(0xffffffffu, bad != 0u) && l <= FLT_MAX)
+        redo_row<D>(p, req, hk, rr, m + log2f(l), bad, o + row * D);
     }
   }
 }

@@ -736,6 +736,12 @@ int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_pre
   pa::shared::Params prm;
   prm.plan = plan;
   prm.q = static_cast<const __nv_bfloat16*>(q);
+  prm.kp = static_cast<const __nv_bfloat16*>(kp.ptr);
+  prm.vp = static_cast<const __nv_bfloat16*>(vp.ptr);
+  for (int i = 0; i < 2; ++i) {
+    prm.kp_s[i] = kp.s[i + 1];
+    prm.vp_s[i] = vp.s[i + 1];
+  }
   prm.kt = static_cast<const __nv_bfloat16*>(kt.ptr);
   prm.vt = static_cast<const __nv_bfloat16*>(vt.ptr);
   for (int i = 0; i < 3; ++i) {

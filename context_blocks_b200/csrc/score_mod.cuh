@@ -507,20 +507,64 @@ __device__ __noinline__ bool store_rows(uint32_t tO, uint32_t stg, __nv_bfloat16
   return !(max3_nan(top[0], top[1], 0.f) <= FLT_MAX);
 }
 
+// Attention of one row over the keys [j0, j1), by the whole warp: acc += 2^(x_j - ref)
+// v_j.  Lane l holds D / 32 of the query's columns in qv and kV of the value columns,
+// those from v + l * kV on.  It stops where nothing more can change: all columns
+// that are `open` in any lane (bit u: acc[u]) are NaN.  Returns whether it did.
+// Four keys at a time, so that their loads and sums wait together; all fp32.
+template <int D, int kV>
+__device__ __forceinline__ bool add_keys(const float (&qv)[D / 32], const __nv_bfloat16* k, const __nv_bfloat16* v,
+                                         long long k_stride, long long v_stride, int j0, int j1, int pos, float ref,
+                                         float slope2, const ScoreMod& sm, bool cap, bool bias, unsigned open,
+                                         float (&acc)[kV]) {
+  constexpr int kQk = D / 32, kStep = 4;
+  const int lane = threadIdx.x % 32;
+#pragma unroll 1
+  for (int j = j0; j < j1; j += kStep) {
+    float dot[kStep], vv[kStep][kV];
+#pragma unroll
+    for (int e = 0; e < kStep; ++e) {
+      const long long at = min(j + e, j1 - 1);  // past the end: the last key once more, without weight
+      const __nv_bfloat16* kr = k + at * k_stride + lane * kQk;
+      const __nv_bfloat16* vr = v + at * v_stride + lane * kV;
+      dot[e] = 0.f;
+#pragma unroll
+      for (int u = 0; u < kQk; ++u) dot[e] = fmaf(qv[u], __bfloat162float(kr[u]), dot[e]);
+#pragma unroll
+      for (int u = 0; u < kV; ++u) vv[e][u] = __bfloat162float(vr[u]);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+      for (int e = 0; e < kStep; ++e) dot[e] += __shfl_xor_sync(0xffffffffu, dot[e], off);
+    bool settled = true;
+#pragma unroll
+    for (int e = 0; e < kStep; ++e) {
+      if (j + e >= j1) continue;
+      const float p = ex2_approx(mod_one(dot[e], sm, cap, bias, slope2, static_cast<float>(pos - (j + e))) - ref);
+#pragma unroll
+      for (int u = 0; u < kV; ++u) acc[u] = fmaf(p, vv[e][u], acc[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kV; ++u)
+      if (((open >> u) & 1u) && acc[u] == acc[u]) settled = false;
+    if (__all_sync(0xffffffffu, settled)) return true;
+  }
+  return false;
+}
+
 // Recompute one output row with the whole warp, reading only the keys [j0, j1)
 // the row sees.  The tensor cores multiply the zero weight of a hidden key with
 // its value row, so a hidden value that is NaN or Inf would reach the row; a
 // row whose accumulator is not finite is therefore done again here, with the
 // maximum m and sum the softmax found (hidden scores never entered those).
-// Rare and slow (about 40 instructions a key); q, k, v: the row's query, and
+// Rare and slow (some 30 clocks a key); q, k, v: the row's query, and
 // key and value row 0 of its head.  pos: the row's position among the keys.
-// Only keys j with (j % period) / share == which count (share = period: all).
 // kCols of the row's value columns are computed, those from v and o on.
 template <int D, int kCols>
 __device__ __noinline__ void repair_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
-                                        long long k_stride, long long v_stride, int j0, int j1, int share, int period,
-                                        int which, int pos, float m, float inv, float slope2, ScoreMod sm, bool cap,
-                                        bool bias, __nv_bfloat16* o_bf16, float* o_f32) {
+                                        long long k_stride, long long v_stride, int j0, int j1, int pos, float m,
+                                        float inv, float slope2, ScoreMod sm, bool cap, bool bias, __nv_bfloat16* o) {
   constexpr int kQk = D / 32, kV = kCols / 32;
   const int lane = threadIdx.x % 32;
   float qv[kQk], acc[kV];
@@ -528,26 +572,9 @@ __device__ __noinline__ void repair_row(const __nv_bfloat16* q, const __nv_bfloa
   for (int u = 0; u < kQk; ++u) qv[u] = __bfloat162float(q[lane * kQk + u]);
 #pragma unroll
   for (int u = 0; u < kV; ++u) acc[u] = 0.f;
-  for (int j = j0; j < j1; ++j) {
-    if ((j % period) / share != which) continue;
-    const __nv_bfloat16* kr = k + j * k_stride + lane * kQk;
-    const __nv_bfloat16* vr = v + j * v_stride + lane * kV;
-    float dot = 0.f;
+  add_keys<D, kV>(qv, k, v, k_stride, v_stride, j0, j1, pos, m, slope2, sm, cap, bias, (1u << kV) - 1, acc);
 #pragma unroll
-    for (int u = 0; u < kQk; ++u) dot = fmaf(qv[u], __bfloat162float(kr[u]), dot);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-    const float p = ex2_approx(mod_one(dot, sm, cap, bias, slope2, static_cast<float>(pos - j)) - m);
-#pragma unroll
-    for (int u = 0; u < kV; ++u) acc[u] = fmaf(p, __bfloat162float(vr[u]), acc[u]);
-  }
-#pragma unroll
-  for (int u = 0; u < kV; ++u) {
-    if (o_bf16 != nullptr)
-      o_bf16[lane * kV + u] = __float2bfloat16(acc[u] * inv);
-    else
-      o_f32[lane * kV + u] = acc[u] * inv;
-  }
+  for (int u = 0; u < kV; ++u) o[lane * kV + u] = __float2bfloat16(acc[u] * inv);
 }
 
 // 4-D tiled load (coordinates innermost first); c0 * element size must be a

@@ -81,3 +81,22 @@ def test_nan_key_in_the_prefix(Bn, G, Nq, kw):
         kp[1, at] = NAN
         o, lse = _shared(q, kp, vp, kt, vt, [min(16, Nq + b % 3) for b in range(Bn)], kw, 6.0)
         assert torch.isnan(lse[:, G:]).all() and not torch.isnan(lse[:, :G]).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kw", FORMS, ids=str)
+@pytest.mark.parametrize("Bn,G,Nq", ROWS)
+def test_infinite_values_of_a_decoding_step(Bn, G, Nq, kw, d):
+    """Inf in a value column that a row sees is Inf in its O, both signs and NaN
+    are NaN; the other columns, heads, requests and earlier tokens are as without."""
+    Np = 300
+    q, kp, vp = _rand((Bn, 2 * G, Nq, d), 1, 2.0), _rand((2, Np, d), 2), _rand((2, Np, d), 3)
+    kt, vt = _rand((Bn, 2, 16, d), 4), _rand((Bn, 2, 16, d), 5)
+    lens = [min(16, Nq + b % 3) for b in range(Bn)]
+    vp[1, Np - 3, 5], vp[1, Np - 9, 20] = INF, -INF
+    vp[1, Np - 4, 9], vp[1, Np - 2, 9], vp[1, Np - 7, 33] = INF, -INF, NAN
+    for b in range(0, Bn, 3):
+        vt[b, 0, lens[b] - 1, 40] = INF   # the last new token's own
+        vt[b, 0, lens[b]:] = NAN          # behind the tail
+    _shared(q, kp, vp, kt, vt, lens, kw, 6.0)
