@@ -693,11 +693,11 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
         redo &= redo - 1;
         __syncwarp();
         const int j0 = __shfl_sync(0xffffffffu, seen.x, k), j1 = __shfl_sync(0xffffffffu, seen.y, k);
-        const float mr = __shfl_sync(0xffffffffu, m_ref, k), iv = __shfl_sync(0xffffffffu, inv, k);
+        const float ref = __shfl_sync(0xffffffffu, m_ref + lg2_approx(l), k);
         const int hk = hq / p.G;
         repair_row<D, kCols>(p.q + bt * p.q_s[0] + hq * p.q_s[1] + (wrow + k) * p.q_s[2],
                              p.k + bt * p.k_s[0] + hk * p.k_s[1], p.v + bt * p.v_s[0] + hk * p.v_s[1] + half * kCols,
-                             p.k_s[2], p.v_s[2], j0, j1, wrow + k + p.q_offset, mr, iv, slope2, p.sm, kCap, kBias,
+                             p.k_s[2], p.v_s[2], j0, j1, wrow + k + p.q_offset, ref, slope2, p.sm, kCap, kBias,
                              o + k * p.o_s[2]);
       }
     }

@@ -813,8 +813,9 @@ inline int merge_warps(const Plan& plan) {
 // The columns `bad` (of lane l's D / 32) of a row's O from the keys the row sees,
 // with ref = log2 of the sum of its weights, to o.  The first kernel's matrix
 // products multiply zero weights too: those of the keys that belong to another copy
-// of the row and those of later tokens, and 0 * Inf is NaN.  So a row whose O is
-// not finite while its sum is takes those columns from here.  Rare and slow (one
+// of the row and those of later tokens, and 0 * Inf is NaN; and weights against a
+// fixed reference make large values overflow (cap_top).  So a row whose O is not
+// finite while its sum is takes those columns from here.  Rare and slow (one
 // warp, all the row's keys); nothing waits for this kernel with a limit.
 template <int D>
 __device__ __noinline__ void redo_row(const Params& p, int req, int hk, int rr, float ref, unsigned bad,

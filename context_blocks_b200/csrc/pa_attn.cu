@@ -507,7 +507,7 @@ pa::mod::ScoreMod score_mod(float scale, float softcap, const float* slopes) {
   m.cap_k = softcap > 0.f ? 2.f * kLog2e * scale / softcap : 0.f;
   m.cap_log2 = softcap * kLog2e;
   m.cap_u = softcap > 0.f ? scale / softcap : 0.f;
-  m.cap_ref = m.cap_log2 - pa::mod::kCapTop;
+  m.cap_ref = m.cap_log2 - pa::mod::cap_top(m.cap_log2);
   m.cap_fixed = m.cap_log2 <= pa::mod::kCapMax;
   for (int i = 0; i < 6; ++i) m.cap_g[i] = m.cap_log2 * pa::mod::kTanhC[i];
   m.slopes = slopes;

@@ -82,19 +82,22 @@ struct ScoreMod {
   float cap_log2;       // c * log2(e)
   float cap_u;          // scale / c
   float cap_g[6];       // cap_log2 * (coefficients of g)
-  float cap_ref;        // cap_log2 - kCapTop: the fixed reference maximum of capped scores
-  bool cap_fixed;       // whether the weights fit that reference (see kCapTop)
+  float cap_ref;        // cap_log2 - cap_top(): the fixed reference maximum of capped scores
+  bool cap_fixed;       // whether the weights fit that reference (see cap_top)
   const float* slopes;  // [Hq], natural units; read where the kernel is built for a bias
 };
 
 // Capped scores without a bias lie in [-c, c], so the softmax needs no running
-// maximum: the weights 2^(x - m) with the fixed m = c log2 e - kCapTop lie in
-// [2^(kCapTop - 2 c log2 e), 2^kCapTop], far from both ends of bf16's and
-// fp32's exponents as long as c log2 e <= kCapMax (c <= 52): a sum of 2^20
-// weights times values up to 2^66 stays finite, and values down to 2^-22 keep
-// their bits where every score of a row is -c.
-constexpr float kCapTop = 40.f;
+// maximum: with x = s log2 e and the fixed reference m = c log2 e - top, the weights
+// 2^(x - m) lie in [2^(top - 2 c log2 e), 2^top].  top is 8, as far as a running
+// maximum may lag (kRescaleLog2), and where that would bring the smallest weights
+// below 2^-64 just as much more as keeps them there; c log2 e <= kCapMax (c <= 52)
+// keeps it at 86 or less, so a sum of 2^30 weights is finite.  Values down to 2^-62
+// keep their bits even where every score of a row is -c.  Values above some
+// 2^(127 - top) may overflow the accumulator; such rows are done again with weights
+// that sum to one (repair_row, and redo_row in attn_shared.cuh).
 constexpr float kCapMax = 75.f;
+inline float cap_top(float cap_log2) { return fmaxf(kRescaleLog2, 2.f * cap_log2 - 64.f); }
 
 // A row's constants in one tile: dist0 = p_i - (first key of the tile).
 __device__ __forceinline__ float mod_one(float s, const ScoreMod& m, bool cap, bool bias, float slope2, float dist) {
@@ -555,16 +558,17 @@ __device__ __forceinline__ bool add_keys(const float (&qv)[D / 32], const __nv_b
 
 // Recompute one output row with the whole warp, reading only the keys [j0, j1)
 // the row sees.  The tensor cores multiply the zero weight of a hidden key with
-// its value row, so a hidden value that is NaN or Inf would reach the row; a
-// row whose accumulator is not finite is therefore done again here, with the
-// maximum m and sum the softmax found (hidden scores never entered those).
+// its value row, so a hidden value that is NaN or Inf would reach the row; and under
+// a fixed reference large values overflow.  A row whose accumulator is not finite
+// is therefore done again here, with weights that sum to one: ref is the log2 of
+// the sum the softmax found (hidden scores never entered that).
 // Rare and slow (some 30 clocks a key); q, k, v: the row's query, and
 // key and value row 0 of its head.  pos: the row's position among the keys.
 // kCols of the row's value columns are computed, those from v and o on.
 template <int D, int kCols>
 __device__ __noinline__ void repair_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
-                                        long long k_stride, long long v_stride, int j0, int j1, int pos, float m,
-                                        float inv, float slope2, ScoreMod sm, bool cap, bool bias, __nv_bfloat16* o) {
+                                        long long k_stride, long long v_stride, int j0, int j1, int pos, float ref,
+                                        float slope2, ScoreMod sm, bool cap, bool bias, __nv_bfloat16* o) {
   constexpr int kQk = D / 32, kV = kCols / 32;
   const int lane = threadIdx.x % 32;
   float qv[kQk], acc[kV];
@@ -572,9 +576,9 @@ __device__ __noinline__ void repair_row(const __nv_bfloat16* q, const __nv_bfloa
   for (int u = 0; u < kQk; ++u) qv[u] = __bfloat162float(q[lane * kQk + u]);
 #pragma unroll
   for (int u = 0; u < kV; ++u) acc[u] = 0.f;
-  add_keys<D, kV>(qv, k, v, k_stride, v_stride, j0, j1, pos, m, slope2, sm, cap, bias, (1u << kV) - 1, acc);
+  add_keys<D, kV>(qv, k, v, k_stride, v_stride, j0, j1, pos, ref, slope2, sm, cap, bias, (1u << kV) - 1, acc);
 #pragma unroll
-  for (int u = 0; u < kV; ++u) o[lane * kV + u] = __float2bfloat16(acc[u] * inv);
+  for (int u = 0; u < kV; ++u) o[lane * kV + u] = __float2bfloat16(acc[u]);
 }
 
 // 4-D tiled load (coordinates innermost first); c0 * element size must be a

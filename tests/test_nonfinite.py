@@ -100,3 +100,37 @@ def test_infinite_values_of_a_decoding_step(Bn, G, Nq, kw, d):
         vt[b, 0, lens[b] - 1, 40] = INF   # the last new token's own
         vt[b, 0, lens[b]:] = NAN          # behind the tail
     _shared(q, kp, vp, kt, vt, lens, kw, 6.0)
+
+
+CAPS = [0.0, 1.0, 20.0, 50.0, 52.0, 60.0]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", [1e-17, 1e27, 5e37])
+@pytest.mark.parametrize("cap", CAPS)
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_and_small_values(d, cap, size):
+    """Weights that sum to one leave O within the values, whatever their size."""
+    q, k, v = _rand((1, 4, 200, d), 1, 3.0), _rand((1, 2, 333, d), 2), (size * _rand((1, 2, 333, d), 3).clamp(-5, 5)).bfloat16()
+    o, lse = pa.attn_fwd_mod(q, k, v, softcap=cap, causal=True, check=True)
+    check_same(o, lse, *oracle.attention(q.cpu(), k.cpu(), v.cpu(), d ** -0.5, softcap=cap, causal=True), 5 * size)
+    for Bn, G, Nq in ROWS:
+        q = _rand((Bn, 2 * G, Nq, d), 4, 3.0)
+        kt, vt = _rand((Bn, 2, 20, d), 5), (size * _rand((Bn, 2, 20, d), 6).clamp(-5, 5)).bfloat16()
+        _shared(q, k[0], v[0], kt, vt, [min(20, Nq + b % 7) for b in range(Bn)], dict(softcap=cap), 5 * size)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("size", [1e-17, 1e27, 5e37])
+@pytest.mark.parametrize("cap", CAPS[1:])
+def test_large_and_small_values_at_the_far_end_of_the_cap(cap, size):
+    """Every score at -c."""
+    q, k = torch.ones((1, 2, 130, 64), dtype=torch.bfloat16, device="cuda"), \
+        -100.0 * torch.ones((1, 1, 200, 64), dtype=torch.bfloat16, device="cuda")
+    v = (size * _rand((1, 1, 200, 64), 5).clamp(-5, 5)).bfloat16()
+    o, lse = pa.attn_fwd_mod(q, k, v, softcap=cap, check=True)
+    check_same(o, lse, *oracle.attention(q.cpu(), k.cpu(), v.cpu(), 0.125, softcap=cap), 5 * size)
+    for Bn, G in ((2, 4), (2, 80), (300, 1)):
+        q = torch.ones((Bn, G, 1, 64), dtype=torch.bfloat16, device="cuda")
+        _shared(q, k[0], v[0], k[:, :, :0].expand(Bn, 1, 0, 64), v[:, :, :0].expand(Bn, 1, 0, 64), [0] * Bn,
+                dict(softcap=cap), 5 * size)
