@@ -236,11 +236,63 @@ struct Layout {
   static constexpr int kItemOff = kClaimOff + 16;
   static constexpr int kTmemSlotOff = kItemOff + static_cast<int>(sizeof(ItemSlot));
   static constexpr int kAbortOff = kTmemSlotOff + 4;
-  static constexpr int kBytes = kAbortOff + 4;
+  static constexpr int kProgressOff = kAbortOff + 4;  // see mbar_wait_hint
+  static constexpr int kBytes = kProgressOff + 4;
   // Never two CTAs an SM: each takes all of tensor memory.
   static constexpr int kMinOneCtaPerSm = 120 * 1024;
   static constexpr int kAllocBytes = (kBytes + 1024 > kMinOneCtaPerSm) ? (kBytes + 1024) : kMinOneCtaPerSm;
 };
+
+// Rows `redo` of a warp once more, those of their columns in o that are not finite.
+// The tensor cores multiply the zero weight of a hidden key with its value row, so
+// a hidden value that is NaN or Inf reaches the accumulator; and under a fixed
+// reference large values overflow it (cap_top).  Here a row takes only the keys
+// [lo, hi) it sees, with weights that sum to one: ref is the log2 of the sum the
+// softmax found (hidden scores never entered that).  A column with a visible value
+// that is not finite needs no scores; what all rows see is looked through once for
+// all of them.  lo, hi, ref: of the lane's own row; q, o: the warp's first row; k, v:
+// row 0 of its head; pos: the first row's position.  kCols of the value columns
+// are computed, those from v and o on.  Some 30 clocks a key and row.
+template <int D, int kCols>
+__device__ __noinline__ void repair_rows(unsigned redo, const __nv_bfloat16* q, long long q_stride,
+                                         const __nv_bfloat16* k, const __nv_bfloat16* v, long long k_stride,
+                                         long long v_stride, int lo, int hi, int pos, float ref, float slope2,
+                                         const ScoreMod& sm, bool cap, bool bias, __nv_bfloat16* o, long long o_stride,
+                                         uint32_t progress) {
+  constexpr int kQk = D / 32, kV = kCols / 32;
+  const int lane = threadIdx.x % 32;
+  const bool mine = (redo >> lane) & 1u;
+  __syncwarp();  // o has been written by all lanes
+  const int all0 = __reduce_max_sync(0xffffffffu, mine ? lo : 0);
+  const int all1 = max(all0, __reduce_min_sync(0xffffffffu, mine ? hi : 0x7fffffff));
+  unsigned all_up = 0u, all_down = 0u;
+  scan_values<kV>(v, v_stride, all0, all1, all_up, all_down, progress);
+  for (; redo != 0u; redo &= redo - 1) {
+    const int r = __ffs(redo) - 1;
+    const int j0 = __shfl_sync(0xffffffffu, lo, r), j1 = __shfl_sync(0xffffffffu, hi, r);
+    const float rr = __shfl_sync(0xffffffffu, ref, r);
+    unsigned up = all_up, down = all_down;
+    scan_values<kV>(v, v_stride, j0, min(all0, j1), up, down, progress);
+    scan_values<kV>(v, v_stride, max(all1, j0), j1, up, down, progress);
+    __nv_bfloat16* dst = o + r * o_stride + lane * kV;
+    unsigned bad = 0u;
+#pragma unroll
+    for (int u = 0; u < kV; ++u)
+      if (!(fabsf(__bfloat162float(dst[u])) < INFINITY)) bad |= 1u << u;
+    float acc[kV] = {};
+    if (__any_sync(0xffffffffu, (bad & ~(up | down)) != 0u)) {
+      float qv[kQk];
+#pragma unroll
+      for (int u = 0; u < kQk; ++u) qv[u] = __bfloat162float(q[r * q_stride + lane * kQk + u]);
+      add_keys<D, kV>(qv, k, v, k_stride, v_stride, j0, j1, pos + r, rr, slope2, sm, cap, bias, acc, progress);
+    }
+#pragma unroll
+    for (int u = 0; u < kV; ++u) {
+      const bool a = (up >> u) & 1u, b = (down >> u) & 1u;
+      if ((bad >> u) & 1u) dst[u] = __float2bfloat16(a || b ? not_finite(a, b) : acc[u]);
+    }
+  }
+}
 
 template <int D, bool kCap, bool kBias, bool kWide>
 __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
@@ -297,6 +349,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
     mbar_init(bar_drain, 1);
     for (int u = 0; u < 8; ++u) mbar_init(bar_swap0 + 8 * u, 2);  // the two warps of the same rows
     *abort_word = 0;
+    abort_word[1] = 0;
     fence_barrier_init();
   }
   if (warp == R::kTma && lane == 0) {
@@ -317,7 +370,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
   const uint32_t tmem = *tmem_slot;
 
   auto wait_all = [&](uint32_t bar, uint32_t parity) {
-    const bool got = mbar_wait_hint(bar, parity, abort_word, p.status, kStatusTimeout, lim, kSuspendHintNs);
+    const bool got = mbar_wait_hint<true>(bar, parity, abort_word, p.status, kStatusTimeout, lim, kSuspendHintNs);
     return __all_sync(0xffffffffu, got);
   };
   // The it-th item of this CTA, copied out of the slot; false at the end (or
@@ -613,7 +666,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
     int g = 0;    // key tiles over all items: phases of the S barrier
     int n_o = 0;  // items with key tiles: phase of the O barrier
     auto wait_warp = [&](uint32_t bar, uint32_t parity) {
-      const bool got = mbar_wait_hint(bar, parity, abort_word, p.status, kStatusTimeout, lim, kSuspendHintNs);
+      const bool got = mbar_wait_hint<true>(bar, parity, abort_word, p.status, kStatusTimeout, lim, kSuspendHintNs);
       return !__any_sync(0xffffffffu, !got);
     };
     ItemSlot x;
@@ -686,19 +739,13 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
       if (half == 0 && row < p.Nq)
         p.lse[static_cast<size_t>(bh) * p.Nq + row] =
             empty ? -INFINITY : (m_ref + lg2_approx(l)) * 0.69314718055994531f;
-      // A value row that is not finite: leave hidden keys out by recomputing.
-      unsigned redo = __ballot_sync(0xffffffffu, bad && !empty && row < p.Nq && l <= FLT_MAX);
-      while (redo != 0u) {
-        const int k = __ffs(redo) - 1;
-        redo &= redo - 1;
-        __syncwarp();
-        const int j0 = __shfl_sync(0xffffffffu, seen.x, k), j1 = __shfl_sync(0xffffffffu, seen.y, k);
-        const float ref = __shfl_sync(0xffffffffu, m_ref + lg2_approx(l), k);
+      const unsigned redo = __ballot_sync(0xffffffffu, bad && !empty && row < p.Nq && l <= FLT_MAX);
+      if (redo != 0u) {
         const int hk = hq / p.G;
-        repair_row<D, kCols>(p.q + bt * p.q_s[0] + hq * p.q_s[1] + (wrow + k) * p.q_s[2],
-                             p.k + bt * p.k_s[0] + hk * p.k_s[1], p.v + bt * p.v_s[0] + hk * p.v_s[1] + half * kCols,
-                             p.k_s[2], p.v_s[2], j0, j1, wrow + k + p.q_offset, ref, slope2, p.sm, kCap, kBias,
-                             o + k * p.o_s[2]);
+        repair_rows<D, kCols>(redo, p.q + bt * p.q_s[0] + hq * p.q_s[1] + wrow * p.q_s[2], p.q_s[2],
+                              p.k + bt * p.k_s[0] + hk * p.k_s[1], p.v + bt * p.v_s[0] + hk * p.v_s[1] + half * kCols,
+                              p.k_s[2], p.v_s[2], seen.x, seen.y, wrow + p.q_offset, m_ref + lg2_approx(l), slope2, p.sm,
+                              kCap, kBias, o, p.o_s[2], base + L::kProgressOff);
       }
     }
   }

@@ -815,7 +815,8 @@ inline int merge_warps(const Plan& plan) {
 // products multiply zero weights too: those of the keys that belong to another copy
 // of the row and those of later tokens, and 0 * Inf is NaN; and weights against a
 // fixed reference make large values overflow (cap_top).  So a row whose O is not
-// finite while its sum is takes those columns from here.  Rare and slow (one
+// finite while its sum is takes those columns from here, a column with a visible
+// value that is not finite without reckoning scores.  Rare and slow (one
 // warp, all the row's keys); nothing waits for this kernel with a limit.
 template <int D>
 __device__ __noinline__ void redo_row(const Params& p, int req, int hk, int rr, float ref, unsigned bad,
@@ -827,17 +828,26 @@ __device__ __noinline__ void redo_row(const Params& p, int req, int hk, int rr, 
   const int pos = plan.len(req) - plan.Nq + rr % plan.Nq;  // counted from the tail's start
   const float slope2 = bias ? __ldg(p.sm.slopes + hk * plan.G + rr / plan.Nq) * 1.4426950408889634f : 0.f;
   const __nv_bfloat16* q = p.q + ((static_cast<size_t>(req) * plan.Hq + hk * plan.G) * plan.Nq + rr) * D;
+  const __nv_bfloat16* kp = p.kp + hk * p.kp_s[0];
+  const __nv_bfloat16* vp = p.vp + hk * p.vp_s[0];
+  const __nv_bfloat16* kt = p.kt + req * p.kt_s[0] + hk * p.kt_s[1];
+  const __nv_bfloat16* vt = p.vt + req * p.vt_s[0] + hk * p.vt_s[1];
+  const int own = min(max(pos + 1, 0), plan.len(req));  // keys of the tail
+  unsigned up = 0u, down = 0u;
+  scan_values<kCols>(vp, p.vp_s[1], 0, plan.Np, up, down, 0u);
+  scan_values<kCols>(vt, p.vt_s[2], 0, own, up, down, 0u);
   float qv[kCols], acc[kCols];
 #pragma unroll
   for (int u = 0; u < kCols; ++u) qv[u] = __bfloat162float(q[lane * kCols + u]), acc[u] = 0.f;
-  if (!add_keys<D, kCols>(qv, p.kp + hk * p.kp_s[0], p.vp + hk * p.vp_s[0], p.kp_s[1], p.vp_s[1], 0, plan.Np,
-                          plan.Np + pos, ref, slope2, p.sm, cap, bias, bad, acc))
-    add_keys<D, kCols>(qv, p.kt + req * p.kt_s[0] + hk * p.kt_s[1], p.vt + req * p.vt_s[0] + hk * p.vt_s[1],
-                       p.kt_s[2], p.vt_s[2], 0, min(max(pos + 1, 0), plan.len(req)), pos, ref, slope2, p.sm, cap, bias,
-                       bad, acc);
+  if (__any_sync(0xffffffffu, (bad & ~(up | down)) != 0u)) {
+    add_keys<D, kCols>(qv, kp, vp, p.kp_s[1], p.vp_s[1], 0, plan.Np, plan.Np + pos, ref, slope2, p.sm, cap, bias, acc, 0u);
+    add_keys<D, kCols>(qv, kt, vt, p.kt_s[2], p.vt_s[2], 0, own, pos, ref, slope2, p.sm, cap, bias, acc, 0u);
+  }
 #pragma unroll
-  for (int u = 0; u < kCols; ++u)
-    if ((bad >> u) & 1u) o[lane * kCols + u] = __float2bfloat16(acc[u]);
+  for (int u = 0; u < kCols; ++u) {
+    const bool a = (up >> u) & 1u, b = (down >> u) & 1u;
+    if ((bad >> u) & 1u) o[lane * kCols + u] = __float2bfloat16(a || b ? not_finite(a, b) : acc[u]);
+  }
 }
 
 // Joins the partial results of every row:

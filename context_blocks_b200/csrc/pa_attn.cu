@@ -495,7 +495,8 @@ int check_scores(int B, int Hq, int Hkv, int Nq, int d, float scale, float softc
 
 // Limit of a wait in the modified-score kernels, where a warp may wait while
 // another goes over all the keys: the library's limit, and 20 us (ten times
-// what one takes) for every key tile.
+// what one takes) for every key tile.  While rows are repaired (repair_rows in
+// attn_mod.cuh) the limit starts anew as long as they make progress.
 unsigned long long wait_limit_ns(long long key_tiles) {
   return g_wait_limit_ns.load(std::memory_order_relaxed) + 20000ull * static_cast<unsigned long long>(key_tiles);
 }

@@ -95,7 +95,7 @@ struct ScoreMod {
 // keeps it at 86 or less, so a sum of 2^30 weights is finite.  Values down to 2^-62
 // keep their bits even where every score of a row is -c.  Values above some
 // 2^(127 - top) may overflow the accumulator; such rows are done again with weights
-// that sum to one (repair_row, and redo_row in attn_shared.cuh).
+// that sum to one (repair_rows in attn_mod.cuh, redo_row in attn_shared.cuh).
 constexpr float kCapMax = 75.f;
 inline float cap_top(float cap_log2) { return fmaxf(kRescaleLog2, 2.f * cap_log2 - 64.f); }
 
@@ -510,20 +510,63 @@ __device__ __noinline__ bool store_rows(uint32_t tO, uint32_t stg, __nv_bfloat16
   return !(max3_nan(top[0], top[1], 0.f) <= FLT_MAX);
 }
 
+// What a warp does again, where an accumulator is not finite: lane l holds columns
+// l * kV .. of the rows it is given.  Rare, and written for shortness.
+
+// Counts up the CTA's progress word (its shared-memory address; 0: none), so that
+// those who wait for this warp go on waiting (mbar_wait_hint).
+__device__ __forceinline__ void tick(uint32_t progress) {
+  if (progress != 0u && threadIdx.x % 32 == 0)
+    asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(progress) : "memory");
+}
+
+// Columns with +Inf or NaN (`up`) and with -Inf or NaN (`down`) among the value rows
+// [j0, j1): bit u of a lane's masks for its column u.  Ends early where all are both.
+template <int kV>
+__device__ __forceinline__ void scan_values(const __nv_bfloat16* v, long long v_stride, int j0, int j1, unsigned& up,
+                                            unsigned& down, uint32_t progress) {
+  constexpr int kStep = 8;
+  const int lane = threadIdx.x % 32;
+#pragma unroll 1
+  for (int j = j0; j < j1; j += kStep) {
+    if (__all_sync(0xffffffffu, (up & down) == (1u << kV) - 1)) return;
+    if (((j - j0) & 255) == 0) tick(progress);
+    float x[kStep][kV];
+#pragma unroll
+    for (int e = 0; e < kStep; ++e) {
+      const __nv_bfloat16* vr = v + min(j + e, j1 - 1) * v_stride + lane * kV;
+#pragma unroll
+      for (int u = 0; u < kV; ++u) x[e][u] = __bfloat162float(vr[u]);
+    }
+#pragma unroll
+    for (int e = 0; e < kStep; ++e)
+#pragma unroll
+      for (int u = 0; u < kV; ++u) {
+        if (!(x[e][u] < INFINITY)) up |= 1u << u;
+        if (!(x[e][u] > -INFINITY)) down |= 1u << u;
+      }
+  }
+}
+
+// The value of a column whose visible value rows are not all finite (every weight
+// is greater than 0).
+__device__ __forceinline__ float not_finite(bool up, bool down) {
+  return up && down ? __int_as_float(0x7fffffff) : up ? INFINITY : -INFINITY;
+}
+
 // Attention of one row over the keys [j0, j1), by the whole warp: acc += 2^(x_j - ref)
-// v_j.  Lane l holds D / 32 of the query's columns in qv and kV of the value columns,
-// those from v + l * kV on.  It stops where nothing more can change: all columns
-// that are `open` in any lane (bit u: acc[u]) are NaN.  Returns whether it did.
-// Four keys at a time, so that their loads and sums wait together; all fp32.
+// v_j.  Lane l holds D / 32 of the query's columns in qv.  Four keys at a time, so
+// that their loads and sums wait together; all fp32.
 template <int D, int kV>
-__device__ __forceinline__ bool add_keys(const float (&qv)[D / 32], const __nv_bfloat16* k, const __nv_bfloat16* v,
+__device__ __forceinline__ void add_keys(const float (&qv)[D / 32], const __nv_bfloat16* k, const __nv_bfloat16* v,
                                          long long k_stride, long long v_stride, int j0, int j1, int pos, float ref,
-                                         float slope2, const ScoreMod& sm, bool cap, bool bias, unsigned open,
-                                         float (&acc)[kV]) {
+                                         float slope2, const ScoreMod& sm, bool cap, bool bias, float (&acc)[kV],
+                                         uint32_t progress) {
   constexpr int kQk = D / 32, kStep = 4;
   const int lane = threadIdx.x % 32;
 #pragma unroll 1
   for (int j = j0; j < j1; j += kStep) {
+    if (((j - j0) & 255) == 0) tick(progress);
     float dot[kStep], vv[kStep][kV];
 #pragma unroll
     for (int e = 0; e < kStep; ++e) {
@@ -540,7 +583,6 @@ __device__ __forceinline__ bool add_keys(const float (&qv)[D / 32], const __nv_b
     for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
       for (int e = 0; e < kStep; ++e) dot[e] += __shfl_xor_sync(0xffffffffu, dot[e], off);
-    bool settled = true;
 #pragma unroll
     for (int e = 0; e < kStep; ++e) {
       if (j + e >= j1) continue;
@@ -548,37 +590,7 @@ __device__ __forceinline__ bool add_keys(const float (&qv)[D / 32], const __nv_b
 #pragma unroll
       for (int u = 0; u < kV; ++u) acc[u] = fmaf(p, vv[e][u], acc[u]);
     }
-#pragma unroll
-    for (int u = 0; u < kV; ++u)
-      if (((open >> u) & 1u) && acc[u] == acc[u]) settled = false;
-    if (__all_sync(0xffffffffu, settled)) return true;
   }
-  return false;
-}
-
-// Recompute one output row with the whole warp, reading only the keys [j0, j1)
-// the row sees.  The tensor cores multiply the zero weight of a hidden key with
-// its value row, so a hidden value that is NaN or Inf would reach the row; and under
-// a fixed reference large values overflow.  A row whose accumulator is not finite
-// is therefore done again here, with weights that sum to one: ref is the log2 of
-// the sum the softmax found (hidden scores never entered that).
-// Rare and slow (some 30 clocks a key); q, k, v: the row's query, and
-// key and value row 0 of its head.  pos: the row's position among the keys.
-// kCols of the row's value columns are computed, those from v and o on.
-template <int D, int kCols>
-__device__ __noinline__ void repair_row(const __nv_bfloat16* q, const __nv_bfloat16* k, const __nv_bfloat16* v,
-                                        long long k_stride, long long v_stride, int j0, int j1, int pos, float ref,
-                                        float slope2, ScoreMod sm, bool cap, bool bias, __nv_bfloat16* o) {
-  constexpr int kQk = D / 32, kV = kCols / 32;
-  const int lane = threadIdx.x % 32;
-  float qv[kQk], acc[kV];
-#pragma unroll
-  for (int u = 0; u < kQk; ++u) qv[u] = __bfloat162float(q[lane * kQk + u]);
-#pragma unroll
-  for (int u = 0; u < kV; ++u) acc[u] = 0.f;
-  add_keys<D, kV>(qv, k, v, k_stride, v_stride, j0, j1, pos, ref, slope2, sm, cap, bias, (1u << kV) - 1, acc);
-#pragma unroll
-  for (int u = 0; u < kV; ++u) o[lane * kV + u] = __float2bfloat16(acc[u]);
 }
 
 // 4-D tiled load (coordinates innermost first); c0 * element size must be a

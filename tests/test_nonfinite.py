@@ -134,3 +134,52 @@ def test_large_and_small_values_at_the_far_end_of_the_cap(cap, size):
         q = torch.ones((Bn, G, 1, 64), dtype=torch.bfloat16, device="cuda")
         _shared(q, k[0], v[0], k[:, :, :0].expand(Bn, 1, 0, 64), v[:, :, :0].expand(Bn, 1, 0, 64), [0] * Bn,
                 dict(softcap=cap), 5 * size)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", FORMS, ids=str)
+@pytest.mark.parametrize("mask", [dict(), dict(causal=True), dict(doc_offsets=[[0, 100, 170, 290]]),
+                                  dict(causal=True, doc_offsets=[[0, 100, 170, 290]], prefix_lens=[[30, 0, 50]])], ids=str)
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinite_values_reach_the_rows_that_see_them(d, mask, kw):
+    """Inf and NaN in single columns: the same infinity, or NaN, in the rows that
+    see them; rows and columns that do not are as without them."""
+    q, k, v = _rand((1, 4, 300, d), 1, 2.0), _rand((1, 2, 300, d), 2), _rand((1, 2, 300, d), 3)
+    q[:, 0, 150:] *= 0.1
+    v[0, 0, 280, 3], v[0, 0, 160, 7], v[0, 0, 165, 7], v[0, 0, 20, 50] = INF, INF, -INF, -INF
+    v[0, 1, 99, 0], v[0, 1, 295, 1], v[0, 1, 0, 63] = NAN, NAN, INF
+    v[0, 1, 250, :] = INF
+    args, host = dict(kw, **mask), dict(kw, **mask)
+    if kw.get("slopes"):
+        # no weight of a visible key falls out of float32
+        args["slopes"] = torch.tensor([0.05, 0.1, 0.15, 0.2], dtype=torch.float32, device="cuda")
+        host["slopes"] = args["slopes"].cpu().numpy()
+    for n in ("doc_offsets", "prefix_lens"):
+        if n in mask:
+            args[n] = torch.tensor(mask[n], dtype=torch.int32, device="cuda")
+    o, lse = pa.attn_fwd_mod(q, k, v, check=True, **args)
+    with np.errstate(invalid="ignore"):
+        ref = oracle.attention(q.cpu(), k.cpu(), v.cpu(), d ** -0.5, **host)
+    check_same(o, lse, *ref, 6.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_repaired_rows_keep_a_short_wait_from_running_out(softcap):
+    """More items than SMs, values that are not finite hidden from most rows of
+    their tile: others wait while a warp does 32 rows again, far longer than the
+    limit, which counts from the last progress."""
+    q, k, v = (_rand((2, 30, 4096, 64), s) for s in (1, 2, 3))
+    o, lse = pa.attn_fwd_mod(q, k, v, causal=True, softcap=softcap)
+    bad = v.clone()
+    bad[:, :, 1023::1024] = NAN
+    bad[:, :, 1535::1024, ::2] = -INF
+    pa.set_wait_limit_ms(1)
+    try:
+        o2, lse2 = pa.attn_fwd_mod(q, k, bad, causal=True, softcap=softcap, check=True)
+    finally:
+        pa.set_wait_limit_ms(5000)
+    assert (lse2 - lse).abs().max() <= LSE_ABS
+    # recomputed rows do not round their weights to bf16: both are 2^-8 from exact
+    assert (o2[:, :, :1023].float() - o[:, :, :1023].float()).abs().max() <= 2.0 ** -6 * float(v.abs().max())
+    assert torch.isnan(o2[:, :, 1023:]).all()
