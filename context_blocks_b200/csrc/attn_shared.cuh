@@ -182,7 +182,7 @@ struct SharedLayout {
 // tile.  All exponentials on the special-function unit: a warp has few enough.
 template <int D, bool kCap, bool kBias, int kKeys>
 __device__ __forceinline__ void softmax_share(uint32_t tS, uint32_t tO, int kq, int b, float dist0, float slope2,
-                                              const ScoreMod& sm, bool have_o, float& m_ref, float& l,
+                                              const ScoreMod& sm, bool counts, bool have_o, float& m_ref, float& l,
                                               uint32_t bar_part, uint32_t bar_full, int lane) {
   constexpr bool kMod = kCap || kBias;
   const int e0 = kq * kKeys;
@@ -196,7 +196,7 @@ __device__ __forceinline__ void softmax_share(uint32_t tS, uint32_t tO, int kq, 
 #pragma unroll
     for (int e = 0; e < kKeys / 2; ++e) x[e] = f2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
   }
-  if constexpr (kCap) cap_scores<kKeys / 2>(x, sm, 0.f);
+  if constexpr (kCap) cap_scores<kKeys / 2>(x, tS + e0, sm, counts);
   if constexpr (kBias)
     bias_scores<kKeys / 2, !kCap>(x, sm.scale_log2, slope2, dist0 - static_cast<float>(e0), 0, b - e0);
   if (__any_sync(0xffffffffu, b < e0 + kKeys)) hide<kKeys / 2>(x, 0, b - e0);
@@ -758,13 +758,13 @@ __global__ void __launch_bounds__(R::kThreads, 1)
         const float dist0 = static_cast<float>(pos - t * kBN);
         const bool have_o = t < x.t1 - 1;
         if (copies == 4)
-          softmax_share<D, kCap, kBias, 32>(tS, tO, kq, b, dist0, slope2, p.sm, have_o, m_ref, l, bar_p_part0 + 8 * i,
-                                            bar_p_full0 + 8 * i, lane);
+          softmax_share<D, kCap, kBias, 32>(tS, tO, kq, b, dist0, slope2, p.sm, mine, have_o, m_ref, l,
+                                            bar_p_part0 + 8 * i, bar_p_full0 + 8 * i, lane);
         else if (copies == 2)
-          softmax_share<D, kCap, kBias, 64>(tS, tO, kq, b, dist0, slope2, p.sm, have_o, m_ref, l, bar_p_part0 + 8 * i,
-                                            bar_p_full0 + 8 * i, lane);
+          softmax_share<D, kCap, kBias, 64>(tS, tO, kq, b, dist0, slope2, p.sm, mine, have_o, m_ref, l,
+                                            bar_p_part0 + 8 * i, bar_p_full0 + 8 * i, lane);
         else
-          softmax_tile<D, kCap, kBias>(tS, tO, 0, b, dist0, slope2, p.sm, have_o, m_ref, l, bar_p_part0 + 8 * i,
+          softmax_tile<D, kCap, kBias>(tS, tO, 0, b, dist0, slope2, p.sm, mine, have_o, m_ref, l, bar_p_part0 + 8 * i,
                                        bar_p_full0 + 8 * i, lane);
       }
       if (!ok) break;

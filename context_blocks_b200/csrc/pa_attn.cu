@@ -505,7 +505,6 @@ pa::mod::ScoreMod score_mod(float scale, float softcap, const float* slopes) {
   constexpr float kLog2e = 1.4426950408889634f;
   pa::mod::ScoreMod m;
   m.scale_log2 = scale * kLog2e;
-  m.cap_k = softcap > 0.f ? 2.f * kLog2e * scale / softcap : 0.f;
   m.cap_log2 = softcap * kLog2e;
   m.cap_u = softcap > 0.f ? scale / softcap : 0.f;
   m.cap_ref = m.cap_log2 - pa::mod::cap_top(m.cap_log2);

@@ -9,13 +9,17 @@
 //
 // Everything is kept in log2 units (x = s * log2 e), fp32.  tanh(u), u = s / c, is
 // u * g(u^2) with a degree-5 polynomial g (relative error 5.9e-7,
-// gen_tanh_poly.py) where all of a warp's scores of a tile have |u| <= 1, and
-// 1 - 2 / (2^(2 u log2 e) + 1) otherwise: ex2 and rcp of the special-function
-// unit, whose errors (2^-22 relative) become at most c * 2^-21 in the capped
-// score.  The polynomial takes half the special-function work of a score away,
-// which bounded the kernels (8192 capped causal keys, 24 heads: 800 us before, 639
-// us with it).  The unit's own tanh has a relative error of 2^-11, which at c = 50
-// would be 0.02 in the exponent.
+// gen_tanh_poly.py) for |u| <= 1, and 1 - 2 / (2^(2 u log2 e) + 1) beyond: ex2 and
+// rcp of the special-function unit, whose errors (2^-22 relative) become at most
+// c * 2^-21 in the capped score.  Against the fixed reference (c <= 52, cap_top) that
+// is 4e-5 even for small scores, and a warp with a score beyond takes all of a
+// tile's in this way; elsewhere c may be anything, and each score goes by its own u.
+// The polynomial takes half the special-function work of a score away, which bounded
+// the kernels (8192 capped causal keys, 24 heads: 800 us before, 639 us with it).
+// The unit's own tanh has a relative error of 2^-11, which at c = 50 would be 0.02 in
+// the exponent.  Scores of 4096 causal keys, 24 heads, normal with deviation 3, cap
+// 20, 12, 8 and 4: 122, 152, 221 and 221 us; each by its own u against the fixed
+// reference too: 122, 181, 240 and 249.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -78,7 +82,6 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 // Scalars of the score modification, set by the host.
 struct ScoreMod {
   float scale_log2;     // scale * log2(e)
-  float cap_k;          // 2 * scale * log2(e) / c
   float cap_log2;       // c * log2(e)
   float cap_u;          // scale / c
   float cap_g[6];       // cap_log2 * (coefficients of g)
@@ -99,20 +102,29 @@ struct ScoreMod {
 constexpr float kCapMax = 75.f;
 inline float cap_top(float cap_log2) { return fmaxf(kRescaleLog2, 2.f * cap_log2 - 64.f); }
 
+// The capped score for |u| > 1, plus top - c log2 e.
+__device__ __forceinline__ float cap_far(float u, float cap_log2, float top) {
+  return fmaf(rcp_approx(ex2_approx(u * (2.f * 1.4426950408889634f)) + 1.f), -2.f * cap_log2, top);
+}
+
 // A row's constants in one tile: dist0 = p_i - (first key of the tile).
 __device__ __forceinline__ float mod_one(float s, const ScoreMod& m, bool cap, bool bias, float slope2, float dist) {
-  float x;
-  if (cap)
-    x = fmaf(rcp_approx(ex2_approx(s * m.cap_k) + 1.f), -2.f * m.cap_log2, m.cap_log2);
-  else
-    x = s * m.scale_log2;
+  float x = s * m.scale_log2;
+  if (cap) {
+    const float u = s * m.cap_u, w = u * u;
+    float y = m.cap_g[5];
+#pragma unroll
+    for (int i = 4; i >= 0; --i) y = fmaf(y, w, m.cap_g[i]);
+    x = fabsf(u) <= 1.f ? y * u : cap_far(u, m.cap_log2, m.cap_log2);
+  }
   if (bias) x = fmaf(-slope2, fabsf(dist), x);
   return x;
 }
 
-// Whether all of the warp's scores lie where the polynomial holds.
+// Whether all of the warp's scores lie where the polynomial holds; those of a thread
+// whose row does not count are whatever its Q rows in shared memory were left with.
 template <int kPairs>
-__device__ __forceinline__ bool cap_by_polynomial(const uint64_t (&x)[kPairs], const ScoreMod& sm) {
+__device__ __forceinline__ bool cap_by_polynomial(const uint64_t (&x)[kPairs], const ScoreMod& sm, bool counts) {
   float a4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int e = 0; e < kPairs; ++e) {
@@ -121,44 +133,55 @@ __device__ __forceinline__ bool cap_by_polynomial(const uint64_t (&x)[kPairs], c
     a4[e & 3] = max3_abs(a4[e & 3], x0, x1);
   }
   const float amax = max3_abs(max3_abs(a4[0], a4[1], a4[2]), a4[3], 0.f) * sm.cap_u;
-  return __all_sync(0xffffffffu, amax <= 1.f);
+  return __all_sync(0xffffffffu, amax <= 1.f || !counts);
 }
 
 // kPairs pairs of raw scores to capped scores (log2 units) plus `add`, by the
-// polynomial where the whole warp's scores allow it.  The steps go over the
-// pairs in turn, so that each has the others' latency to wait in.
+// polynomial.  The steps go over the pairs in turn, so that each has the others'
+// latency to wait in.
 template <int kPairs>
-__device__ __forceinline__ void cap_scores(uint64_t (&x)[kPairs], const ScoreMod& sm, float add) {
+__device__ __forceinline__ void cap_near(uint64_t (&x)[kPairs], const ScoreMod& sm, float add) {
   constexpr int kGroup = kPairs < 8 ? kPairs : 8;
-  if (cap_by_polynomial<kPairs>(x, sm)) {
-    const uint64_t k2 = f2(sm.cap_u, sm.cap_u), add2 = f2(add, add);
-    uint64_t g[6];
+  const uint64_t k2 = f2(sm.cap_u, sm.cap_u), add2 = f2(add, add);
+  uint64_t g[6];
 #pragma unroll
-    for (int u = 0; u < 6; ++u) g[u] = f2(sm.cap_g[u], sm.cap_g[u]);
+  for (int u = 0; u < 6; ++u) g[u] = f2(sm.cap_g[u], sm.cap_g[u]);
 #pragma unroll
-    for (int e0 = 0; e0 < kPairs; e0 += kGroup) {
-      uint64_t w[kGroup], y[kGroup];
+  for (int e0 = 0; e0 < kPairs; e0 += kGroup) {
+    uint64_t w[kGroup], y[kGroup];
 #pragma unroll
-      for (int e = 0; e < kGroup; ++e) x[e0 + e] = f2_mul(x[e0 + e], k2);
+    for (int e = 0; e < kGroup; ++e) x[e0 + e] = f2_mul(x[e0 + e], k2);
 #pragma unroll
-      for (int e = 0; e < kGroup; ++e) w[e] = f2_mul(x[e0 + e], x[e0 + e]);
+    for (int e = 0; e < kGroup; ++e) w[e] = f2_mul(x[e0 + e], x[e0 + e]);
 #pragma unroll
-      for (int e = 0; e < kGroup; ++e) y[e] = f2_fma(g[5], w[e], g[4]);
+    for (int e = 0; e < kGroup; ++e) y[e] = f2_fma(g[5], w[e], g[4]);
 #pragma unroll
-      for (int u = 3; u >= 0; --u)
+    for (int u = 3; u >= 0; --u)
 #pragma unroll
-        for (int e = 0; e < kGroup; ++e) y[e] = f2_fma(y[e], w[e], g[u]);
+      for (int e = 0; e < kGroup; ++e) y[e] = f2_fma(y[e], w[e], g[u]);
 #pragma unroll
-      for (int e = 0; e < kGroup; ++e) x[e0 + e] = f2_fma(y[e], x[e0 + e], add2);
-    }
-  } else {
-    const uint64_t m2 = f2(-2.f * sm.cap_log2, -2.f * sm.cap_log2), t2 = f2(sm.cap_log2 + add, sm.cap_log2 + add);
+    for (int e = 0; e < kGroup; ++e) x[e0 + e] = f2_fma(y[e], x[e0 + e], add2);
+  }
+}
+
+// The same for any scores and any cap: those of |u| > 1 once more from their raw
+// values, still in tensor memory at tS.
+template <int kPairs>
+__device__ __forceinline__ void cap_scores(uint64_t (&x)[kPairs], uint32_t tS, const ScoreMod& sm, bool counts) {
+  const bool near = cap_by_polynomial<kPairs>(x, sm, counts);
+  cap_near<kPairs>(x, sm, 0.f);
+  if (near) return;
 #pragma unroll
-    for (int e = 0; e < kPairs; ++e) {
-      float u0, u1;
-      f2_split(f2_mul(x[e], f2(sm.cap_k, sm.cap_k)), u0, u1);
-      f2_split(f2_add(f2(ex2_approx(u0), ex2_approx(u1)), f2(1.f, 1.f)), u0, u1);
-      x[e] = f2_fma(f2(rcp_approx(u0), rcp_approx(u1)), m2, t2);
+  for (int e0 = 0; e0 < kPairs; e0 += 8) {
+    uint32_t r[16];
+    tmem_ld_x16(tS + 2 * e0, r);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float u0 = __uint_as_float(r[2 * e]) * sm.cap_u, u1 = __uint_as_float(r[2 * e + 1]) * sm.cap_u;
+      float y0, y1;
+      f2_split(x[e0 + e], y0, y1);
+      x[e0 + e] = f2(fabsf(u0) <= 1.f ? y0 : cap_far(u0, sm.cap_log2, sm.cap_log2),
+                     fabsf(u1) <= 1.f ? y1 : cap_far(u1, sm.cap_log2, sm.cap_log2));
     }
   }
 }
@@ -206,14 +229,14 @@ __device__ __forceinline__ void capped_weights(uint64_t (&x)[kPairs], const Scor
   l += s0 + s1;
 }
 
-// -inf where key 2 e or 2 e + 1 of the pairs is not in [a, b).
+// `with` where key 2 e or 2 e + 1 of the pairs is not in [a, b).
 template <int kPairs>
-__device__ __forceinline__ void hide(uint64_t (&x)[kPairs], int a, int b) {
+__device__ __forceinline__ void hide(uint64_t (&x)[kPairs], int a, int b, float with = -INFINITY) {
 #pragma unroll
   for (int e = 0; e < kPairs; ++e) {
     float x0, x1;
     f2_split(x[e], x0, x1);
-    x[e] = f2((2 * e < a || 2 * e >= b) ? -INFINITY : x0, (2 * e + 1 < a || 2 * e + 1 >= b) ? -INFINITY : x1);
+    x[e] = f2((2 * e < a || 2 * e >= b) ? with : x0, (2 * e + 1 < a || 2 * e + 1 >= b) ? with : x1);
   }
 }
 
@@ -246,36 +269,47 @@ __device__ __forceinline__ void bias_scores(uint64_t (&x)[kPairs], float mul, fl
   }
 }
 
-// A softmax step of one row a thread over 64 keys with the fixed reference: scores
-// at tS in tensor memory, weights (bf16 pairs, 32 columns) to tP, which may lie
-// over scores this thread has taken.  The row sees the keys [a, b) of the 64.
-// No maximum, no rescaling of O, nothing to agree on with another thread; l
-// grows by the weights' sum.
-__device__ __forceinline__ void capped_keys(uint32_t tS, uint32_t tP, int a, int b, const ScoreMod& sm, float& l,
-                                            uint32_t bar_p, int lane) {
+// Weights (bf16 pairs) to tensor memory, handed over on `bar`.
+__device__ __forceinline__ void hand_over(uint32_t tP, const uint32_t (&pk)[32], uint32_t bar, int lane) {
+  tmem_st_x32(tP, pk);
+  tmem_st_wait();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+// capped_keys where some key is hidden from some row of the warp or some score is
+// past the polynomial's end; returns the sum of the weights.
+__device__ __forceinline__ float capped_keys_cut(uint32_t tS, uint32_t tP, int a, int b, bool counts,
+                                                 const ScoreMod& sm, uint32_t bar_p, int lane) {
   constexpr int kPairs = 32;
-  const bool edge = __any_sync(0xffffffffu, a > 0 || b < 2 * kPairs);
-  if (!__any_sync(0xffffffffu, max(a, 0) < min(b, 2 * kPairs))) {  // no row of this warp sees any of it
-    const uint32_t none[32] = {};
-    tmem_st_x32(tP, none);
-    tmem_st_wait();
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar_p);
-    return;
-  }
-  uint64_t x[kPairs];
-  {
-    uint32_t sr[2 * kPairs];
-    tmem_ld_x64(tS, sr);
-#pragma unroll
-    for (int e = 0; e < kPairs; ++e) x[e] = f2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
-  }
   uint32_t pk[kPairs];
-  if (!edge && cap_by_polynomial<kPairs>(x, sm)) {
-    capped_weights<kPairs>(x, sm, pk, l);
+  float l = 0.f;
+  if (!__any_sync(0xffffffffu, max(a, 0) < min(b, 2 * kPairs))) {  // no row of this warp sees any of it
+#pragma unroll
+    for (int e = 0; e < kPairs; ++e) pk[e] = 0u;
   } else {
-    cap_scores<kPairs>(x, sm, -sm.cap_ref);
+    uint64_t x[kPairs];
+    {
+      uint32_t sr[2 * kPairs];
+      tmem_ld_x64(tS, sr);
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) x[e] = f2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+    }
+    const bool edge = __any_sync(0xffffffffu, a > 0 || b < 2 * kPairs);
+    if (edge) hide<kPairs>(x, a, b, 0.f);  // so that hidden scores have no part in how the others are taken
+    if (cap_by_polynomial<kPairs>(x, sm, counts)) {
+      cap_near<kPairs>(x, sm, -sm.cap_ref);
+    } else {
+      const uint64_t k2 = f2(sm.cap_u, sm.cap_u);
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) {
+        float u0, u1;
+        f2_split(f2_mul(x[e], k2), u0, u1);
+        x[e] = f2(cap_far(u0, sm.cap_log2, sm.cap_log2 - sm.cap_ref),
+                  cap_far(u1, sm.cap_log2, sm.cap_log2 - sm.cap_ref));
+      }
+    }
     if (edge) hide<kPairs>(x, a, b);
     uint64_t l2[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
@@ -288,29 +322,54 @@ __device__ __forceinline__ void capped_keys(uint32_t tS, uint32_t tP, int a, int
     }
     float s0, s1;
     f2_split(f2_add(l2[0], l2[1]), s0, s1);
-    l += s0 + s1;
+    l = s0 + s1;
   }
-  tmem_st_x32(tP, pk);
-  tmem_st_wait();
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_arrive(bar_p);
+  hand_over(tP, pk, bar_p, lane);
+  return l;
+}
+
+// A softmax step of one row a thread over 64 keys with the fixed reference: scores
+// at tS in tensor memory, weights (bf16 pairs, 32 columns) to tP, which may lie
+// over scores this thread has taken.  The row, where it counts, sees the keys
+// [a, b) of the 64.
+// No maximum, no rescaling of O, nothing to agree on with another thread; l
+// grows by the weights' sum.
+__device__ __forceinline__ void capped_keys(uint32_t tS, uint32_t tP, int a, int b, bool counts, const ScoreMod& sm,
+                                            float& l, uint32_t bar_p, int lane) {
+  constexpr int kPairs = 32;
+  if (!__any_sync(0xffffffffu, a > 0 || b < 2 * kPairs)) {
+    uint64_t x[kPairs];
+    {
+      uint32_t sr[2 * kPairs];
+      tmem_ld_x64(tS, sr);
+#pragma unroll
+      for (int e = 0; e < kPairs; ++e) x[e] = f2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
+    }
+    if (cap_by_polynomial<kPairs>(x, sm, counts)) {
+      uint32_t pk[kPairs];
+      capped_weights<kPairs>(x, sm, pk, l);
+      hand_over(tP, pk, bar_p, lane);
+      return;
+    }
+  }
+  l += capped_keys_cut(tS, tP, a, b, counts, sm, bar_p, lane);
 }
 
 // One 128-key tile of one row a thread: S from tensor memory at tS, P (bf16
 // pairs) written back over it and handed over in two halves.  The row sees
 // keys [a, b) of the tile.  m_ref, l: the row's running reference maximum and
 // sum; tO: its O accumulator, rescaled when the maximum moves (`have_o`: it
-// holds something).  A row that has seen nothing keeps m_ref = -inf and l = 0.
+// holds something).  A row that has seen nothing keeps m_ref = -inf and l = 0; one
+// that does not count (`counts`) makes no difference to others.
 template <int D, bool kCap, bool kBias>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int a, int b, float dist0, float slope2,
-                                             const ScoreMod& sm, bool have_o, float& m_ref, float& l,
+                                             const ScoreMod& sm, bool counts, bool have_o, float& m_ref, float& l,
                                              uint32_t bar_part, uint32_t bar_full, int lane) {
   if constexpr (kCap && !kBias) {
     if (sm.cap_fixed) {
       if (max(a, 0) < min(b, kBN)) m_ref = sm.cap_ref;  // stays -inf until the row sees a key
-      capped_keys(tS, tS, a, b, sm, l, bar_part, lane);
-      capped_keys(tS + 64, tS + 32, a - 64, b - 64, sm, l, bar_full, lane);
+      capped_keys(tS, tS, a, b, counts, sm, l, bar_part, lane);
+      capped_keys(tS + 64, tS + 32, a - 64, b - 64, counts, sm, l, bar_full, lane);
       return;
     }
   }
@@ -342,7 +401,7 @@ __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int a, in
     uint64_t x[kBN / 2];
 #pragma unroll
     for (int e = 0; e < kBN / 2; ++e) x[e] = f2(s[2 * e], s[2 * e + 1]);
-    if constexpr (kCap) cap_scores<kBN / 2>(x, sm, 0.f);
+    if constexpr (kCap) cap_scores<kBN / 2>(x, tS, sm, counts);
     if constexpr (kBias) bias_scores<kBN / 2, !kCap>(x, c, slope2, dist0, a, b);
     if (edge) hide<kBN / 2>(x, a, b);
     float m8[8];
