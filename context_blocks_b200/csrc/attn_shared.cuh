@@ -810,24 +810,30 @@ inline int merge_warps(const Plan& plan) {
   return plan.B * plan.Hkv <= 4 * plan.ctas ? kMergeWarps : kMergeWarps / 2;
 }
 
-// The columns `bad` (of lane l's D / 32) of a row's O from the keys the row sees,
-// with ref = log2 of the sum of its weights, to o.  The first kernel's matrix
-// products multiply zero weights too: those of the keys that belong to another copy
-// of the row and those of later tokens, and 0 * Inf is NaN; and weights against a
-// fixed reference make large values overflow (cap_top).  So a row whose O is not
-// finite while its sum is takes those columns from here, a column with a visible
-// value that is not finite without reckoning scores.  Rare and slow (one
-// warp, all the row's keys); nothing waits for this kernel with a limit.
+// The columns of a row's O that are not finite once more, from the keys the row sees
+// and with weights that sum to one, by its LSE.  The first kernel's matrix products
+// multiply zero weights too: those of the keys that belong to another copy of the
+// row and those of later tokens, and 0 * Inf is NaN; and weights against a fixed
+// reference make large values overflow (cap_top).  A column with a visible value that
+// is not finite needs no scores.  Rare and slow (one warp, all the row's keys); nothing
+// waits for this kernel with a limit.
 template <int D>
-__device__ __noinline__ void redo_row(const Params& p, int req, int hk, int rr, float ref, unsigned bad,
-                                      __nv_bfloat16* o) {
+__device__ __noinline__ void redo_row(const Params& p, int rr, __nv_bfloat16* o, const float* lse) {
   constexpr int kCols = D / 32;
   const Plan& plan = p.plan;
   const int lane = threadIdx.x % 32;
+  const int req = blockIdx.x / plan.Hkv, hk = blockIdx.x % plan.Hkv;
   const bool cap = p.sm.cap_log2 > 0.f, bias = p.sm.slopes != nullptr;
   const int pos = plan.len(req) - plan.Nq + rr % plan.Nq;  // counted from the tail's start
   const float slope2 = bias ? __ldg(p.sm.slopes + hk * plan.G + rr / plan.Nq) * 1.4426950408889634f : 0.f;
-  const __nv_bfloat16* q = p.q + ((static_cast<size_t>(req) * plan.Hq + hk * plan.G) * plan.Nq + rr) * D;
+  const size_t row = (static_cast<size_t>(req) * plan.Hq + hk * plan.G) * plan.Nq + rr;
+  const __nv_bfloat16* q = p.q + row * D;
+  const float ref = lse[row] * 1.4426950408889634f;
+  o += row * D + lane * kCols;
+  unsigned bad = 0u;
+#pragma unroll
+  for (int u = 0; u < kCols; ++u)
+    if (!(fabsf(__bfloat162float(o[u])) < INFINITY)) bad |= 1u << u;
   const __nv_bfloat16* kp = p.kp + hk * p.kp_s[0];
   const __nv_bfloat16* vp = p.vp + hk * p.vp_s[0];
   const __nv_bfloat16* kt = p.kt + req * p.kt_s[0] + hk * p.kt_s[1];
@@ -846,7 +852,7 @@ __device__ __noinline__ void redo_row(const Params& p, int req, int hk, int rr, 
 #pragma unroll
   for (int u = 0; u < kCols; ++u) {
     const bool a = (up >> u) & 1u, b = (down >> u) & 1u;
-    if ((bad >> u) & 1u) o[lane * kCols + u] = __float2bfloat16(a || b ? not_finite(a, b) : acc[u]);
+    if ((bad >> u) & 1u) o[u] = __float2bfloat16(a || b ? not_finite(a, b) : acc[u]);
   }
 }
 
@@ -940,7 +946,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const
   int group = warps;  // warps a row
   while (group > 1 && group * plan.rows > warps) group /= 2;
   const int wi = warp % group;
-  for (int r0 = 0; r0 < plan.rows; r0 += warps / group) {
+  unsigned redo = 0u;  // which of this warp's rows (32 at most: 128 to four warps) to do again
+  for (int r0 = 0, it = 0; r0 < plan.rows; r0 += warps / group, ++it) {
     const int rr = r0 + warp / group;
     const bool row_ok = rr < plan.rows;
     // Row of the workspace that holds partial k.
@@ -1023,11 +1030,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const
       const size_t row = (static_cast<size_t>(req) * plan.Hq + hk * plan.G) * plan.Nq + rr;
       const bool none = l == 0.f;
       const float inv = none ? 0.f : 1.f / l;
-      unsigned bad = 0u;  // columns that are not finite
+      float top = 0.f;  // the largest magnitude, or NaN
 #pragma unroll
       for (int u = 0; u < kCols; ++u) {
         acc[u] *= inv;
-        if (!(fabsf(acc[u]) <= FLT_MAX)) bad |= 1u << u;
+        top = max3_nan(top, acc[u], 0.f);
       }
       if constexpr (D == 128) {
         uint2 v;
@@ -1038,9 +1045,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const
         *reinterpret_cast<uint32_t*>(o + row * D + lane * kCols) = pack_bf16x2(acc[0], acc[1]);
       }
       if (lane == 0) lse[row] = none ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-      if (__any_sync(0xffffffffu, bad != 0u) && l <= FLT_MAX)
-        redo_row<D>(p, req, hk, rr, m + log2f(l), bad, o + row * D);
+      if (__any_sync(0xffffffffu, !(top <= FLT_MAX)) && l <= FLT_MAX) redo |= 1u << it;
     }
+  }
+  for (; redo != 0u; redo &= redo - 1) {
+    __syncwarp();  // o and lse have been written by all lanes
+    redo_row<D>(p, (__ffs(redo) - 1) * (warps / group) + warp / group, o, lse);
   }
 }
 
