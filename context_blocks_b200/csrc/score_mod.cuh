@@ -244,7 +244,8 @@ __device__ __forceinline__ void hide(uint64_t (&x)[kPairs], int a, int b, float 
 // which those in [a, b) count.  The distance is linear in the key on either side
 // of the row's own position: unless a row sees keys on both sides, the bias is
 // a base for every eight keys plus one of four pairs of multiples of the slope,
-// two packed operations a pair.
+// two packed operations a pair.  The two are added before the score: at the row's
+// own position they cancel exactly, whatever the slope.
 template <int kPairs, bool kMul>
 __device__ __forceinline__ void bias_scores(uint64_t (&x)[kPairs], float mul, float slope2, float dist0, int a, int b) {
   const bool behind = dist0 >= static_cast<float>(min(b, 2 * kPairs) - 1);  // all keys that count
@@ -256,7 +257,8 @@ __device__ __forceinline__ void bias_scores(uint64_t (&x)[kPairs], float mul, fl
 #pragma unroll
     for (int e = 0; e < kPairs; ++e) {
       const float at = sl * (static_cast<float>(2 * (e & ~3)) - dist0);
-      x[e] = f2_add(kMul ? f2_fma(x[e], f2(mul, mul), f2(at, at)) : f2_add(x[e], f2(at, at)), step[e & 3]);
+      const uint64_t far = f2_add(f2(at, at), step[e & 3]);
+      x[e] = kMul ? f2_fma(x[e], f2(mul, mul), far) : f2_add(x[e], far);
     }
   } else {
 #pragma unroll
