@@ -400,9 +400,12 @@ def attn_fwd_mod(q, k, v, scale: Optional[float] = None, softcap: float = 0.0, s
         if doc_offsets.dim() != 2 or doc_offsets.shape[1] < 2:
             raise ValueError("doc_offsets must be [B, n_docs + 1] with n_docs >= 1")
         n_docs = doc_offsets.shape[1] - 1
+    if q_offset is None:
+        q_offset = Nk - Nq
+    elif not -(1 << 30) <= q_offset <= 1 << 30:  # as a C int it would wrap round
+        raise ValueError(f"|q_offset| must be <= 2^30 (got {q_offset})")
     mod = ScoreMod(softcap, 1 if causal else 0, _check_vector("slopes", slopes, _t.f32, (Hq,), index), None,
-                   _check_vector("doc_offsets", doc_offsets, _t.i32, (B, n_docs + 1), index), n_docs,
-                   Nk - Nq if q_offset is None else q_offset)
+                   _check_vector("doc_offsets", doc_offsets, _t.i32, (B, n_docs + 1), index), n_docs, q_offset)
     if prefix_lens is not None:
         shape = (B, n_docs) if n_docs else (B, 1) if prefix_lens.dim() == 2 else (B,)
         mod.prefix_lens = _check_vector("prefix_lens", prefix_lens, _t.i32, shape, index)
