@@ -187,6 +187,7 @@ struct PairOrder {
 struct ItemSlot {
   int item;
   int first[2], last[2];  // key tiles [first, last) of query tile 0 and 1
+  int end;                // no row of the item sees a key at `end` or behind it
   int doc0, doc1;         // documents of the item's first and last row
 };
 
@@ -383,6 +384,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
     x.item = slot->item;
     x.first[0] = slot->first[0], x.first[1] = slot->first[1];
     x.last[0] = slot->last[0], x.last[1] = slot->last[1];
+    x.end = slot->end;
     x.doc0 = slot->doc0, x.doc1 = slot->doc1;
     __syncwarp();
     if (lane == 0) mbar_arrive(bar_item_empty);
@@ -467,6 +469,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
           slot->first[i] = hi[i] > 0 ? lo[i] / kBN : 0;
           slot->last[i] = hi[i] > 0 ? (hi[i] + kBN - 1) / kBN : 0;
         }
+        slot->end = max(hi[0], hi[1]);
         slot->doc0 = doc0;
         slot->doc1 = doc1;
       }
@@ -595,6 +598,22 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
           break;
         }
         ++idx;
+        // Keys behind all that some row of the item sees (padding behind the last
+        // document, the free end of a cache): their weights are 0, but a value left
+        // there may be NaN or Inf, so their rows are cleared while the weights are
+        // still reckoned.  Leaving out the steps of 16 keys instead made the issue of
+        // all others longer (4608 keys behind a prefix: 142 and 144 us).
+        const int valid = x.end - j * kBN;
+        const bool cut = valid < kBN;
+        if (cut) {
+          // A row has 8 * kBoxes pieces of 16 bytes, one a lane.
+          constexpr int kLanes = 8 * L::kBoxes;
+          const uint32_t v0 = sRing + sv * L::kTileBytes + (lane % kLanes) / 8 * L::kBoxBytes + lane % 8 * 16;
+          for (int r = valid + lane / kLanes; r < kBN; r += 32 / kLanes)
+            st_shared_v4(v0 + r * 128, 0u, 0u, 0u, 0u);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
         const bool more = j > a;
         int sk = 0;
         for (int i = 0; i < 2 && ok; ++i) {
@@ -606,7 +625,9 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
               break;
             }
             tc_fence_after();
-            if (leader) issue_pv(i, sv, acc, 0);
+            if (leader) {
+              issue_pv(i, sv, acc, 0);
+            }
             __syncwarp();
             if (!wait_all(bar_p_full0 + 8 * i, ph)) {
               ok = false;

@@ -183,3 +183,24 @@ def test_repaired_rows_keep_a_short_wait_from_running_out(softcap):
     # recomputed rows do not round their weights to bf16: both are 2^-8 from exact
     assert (o2[:, :, :1023].float() - o[:, :, :1023].float()).abs().max() <= 2.0 ** -6 * float(v.abs().max())
     assert torch.isnan(o2[:, :, 1023:]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", FORMS, ids=str)
+@pytest.mark.parametrize("d", [64, 128])
+def test_keys_behind_all_rows_reach_are_left_out(d, kw):
+    """What padding and the free end of a cache were left with changes no bit of
+    rows that share a key tile with it: it is not even repaired."""
+    args = dict(kw, slopes=_slopes(4)) if kw.get("slopes") else kw
+    for Nq, Nk, docs, off, end in ((300, 300, [0, 100, 170, 290], 0, 290), (300, 300, [0, 211], 0, 211),
+                                   (40, 517, None, 100, 140), (1, 517, None, 127, 128), (1, 517, None, 128, 129),
+                                   (1, 517, None, 144, 145), (600, 700, [70, 75], 0, 75), (517, 517, [17, 30, 500], 0, 500)):
+        q, k, v = _rand((2, 4, Nq, d), 1, 2.0), _rand((2, 2, Nk, d), 2), _rand((2, 2, Nk, d), 3)
+        more = {} if docs is None else dict(doc_offsets=torch.tensor([docs] * 2, dtype=torch.int32, device="cuda"))
+        for causal in ((True,) if docs is None else (False, True)):
+            o, lse = pa.attn_fwd_mod(q, k, v, causal=causal, q_offset=off, check=True, **args, **more)
+            k2, v2 = k.clone(), v.clone()
+            k2[:, :, end:], v2[:, :, end:] = NAN, INF
+            o2, lse2 = pa.attn_fwd_mod(q, k2, v2, causal=causal, q_offset=off, check=True, **args, **more)
+            # causal: rows before the item's last see less than it does, but those keys are real
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
