@@ -24,7 +24,8 @@ LIB_PATH = os.path.join(PKG_DIR, "libpa_attn.so")
 SOURCES = [os.path.join(CSRC, "pa_attn.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("ptx.cuh", "fwd_common.cuh", "attn_fwd.cuh", "attn_mod.cuh",
                                                   "attn_shared.cuh", "block_norm.cuh", "lse_merge.cuh",
-                                                  "quantize.cuh", "residual_diff.cuh", "score_mod.cuh")] + [
+                                                  "quantize.cuh", "residual_diff.cuh", "score_mod.cuh",
+                                                  "shared_plan.cuh")] + [
     os.path.join(INCLUDE, "pa_attn.h")]
 
 NVCC_FLAGS = [

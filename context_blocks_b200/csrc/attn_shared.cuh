@@ -51,6 +51,7 @@
 
 #include "attn_mod.cuh"
 #include "score_mod.cuh"
+#include "shared_plan.cuh"
 
 namespace pa {
 namespace shared {
@@ -59,67 +60,9 @@ using namespace mod;
 
 using R = Roles<false>;  // warps and registers of the single-warpgroup kernel
 
-constexpr int kMaxCtas = 160;  // sizes the workspace; the grid is one CTA an SM, at most this many
 constexpr int kMergeWarps = 8;
 constexpr int kLoadWarp = 9;   // + stream
-// What a pair's key tile and a unit of the singles cost, in parts of one another:
-// how the CTAs are dealt to the two kinds.  128 requests on 32768 capped keys,
-// tails of 16, 512 and 1024 tokens: 112, 132 and 162 us at 15 : 6; at 12 : 6 113,
-// 143 and 174; at 18 : 6 107, 136 and 160; at 22 : 6 121, 153 and 179.
-constexpr int kPairCost = 15, kSingleCost = 6;
-
-// A line of n units cut into `parts` parts, none empty, sizes differing by one.
-struct Cut {
-  int n, parts, q, r;
-  __device__ Cut(int n_, int most) : n(n_), parts(max(min(n_, most), 1)), q(n_ / parts), r(n_ - q * parts) {}
-  __device__ int begin(int c) const { return c * q + min(c, r); }
-  __device__ int holder(int u) const { return u < r * (q + 1) ? u / (q + 1) : r + (u - r * (q + 1)) / q; }
-};
-
-// Shapes of a call.
-struct Plan {
-  int B, Hq, Hkv, G, Nq;
-  int rows;          // rows of one request under one K/V head: G * Nq
-  int tile_reqs;     // requests in a row tile: 128 / rows, at most B
-  int row_tiles;     // ceil(B / tile_reqs); 0 without a prefix
-  int Np, Nt;
-  int prefix_tiles;  // key tiles of the prefix
-  int ctas;
-  const int* tail_lens;
-
-  __host__ __device__ int tile_rows() const { return tile_reqs * rows; }
-  __host__ __device__ int pairs() const { return row_tiles / 2; }
-  __host__ __device__ bool odd() const { return (row_tiles & 1) != 0; }
-  __host__ __device__ int pair_units() const { return Hkv * pairs() * prefix_tiles; }
-  // Pairs side by side, lane l of them taken by the CTAs c with c mod lanes = l;
-  // with more pairs than CTAs a lane has several, l, l + lanes, ..
-  __host__ __device__ int lanes(int pair_ctas) const { return pairs() < pair_ctas ? pairs() : pair_ctas; }
-  __host__ __device__ int lane_pairs(int lanes, int l) const { return (pairs() - l + lanes - 1) / lanes; }
-  __host__ __device__ int odd_units() const { return odd() ? Hkv * prefix_tiles : 0; }
-  // Copies of a row tile's rows.
-  __host__ __device__ static int copies(int n) { return n <= 32 ? 4 : n <= 64 ? 2 : 1; }
-  __device__ int len(int b) const { return min(max(__ldg(tail_lens + b), 0), Nt); }
-  __device__ static int tiles_of(int keys) { return (keys + kBN - 1) / kBN; }
-  // CTAs that take pairs, given the key tiles (under one K/V head) of all tails
-  // and the number of tails that have any; a tail's start costs about a tile.
-  __device__ int pair_ctas(int tiles, int tails) const {
-    const long long p = static_cast<long long>(pair_units()) * kPairCost;
-    const long long s = (odd_units() + (tiles + tails) * static_cast<long long>(Hkv)) * kSingleCost;
-    if (p == 0) return 0;
-    if (s == 0) return ctas <= pairs() ? ctas : ctas - ctas % pairs();
-    // Rounded the same way in both kernels.
-    const float share = __fdiv_rn(__ll2float_rn(p), __ll2float_rn(p + s));
-    const int n = min(max(__float2int_rn(__fmul_rn(static_cast<float>(ctas), share)), 1), ctas - 1);
-    return n <= pairs() ? n : n - n % pairs();  // as many for every pair
-  }
-  // Units of the line before a tail's own tiles, for its start: one where the prefix
-  // has more row tiles x key tiles than the tails (`tiles` of them).  Counted and
-  // not: 7 requests of 119056 + 333 keys 234 and 258 us, 32 of 32768 + 300 52 and 57,
-  // 128 on pairs of 32768 + 1024 132 and 142.  Where tails are most of the work,
-  // HBM evens out their starts, and a coarser line only costs: 100 requests of
-  // 1000 + 600 47 and 41, 128 of 100 + 2000 75 and 73, 32 of 4608 + 1152 35 and 33.
-  __device__ int start_units(int tiles) const { return row_tiles * prefix_tiles >= tiles ? 1 : 0; }
-};
+static_assert(kBM == kPlanRows && kBN == kPlanKeys, "tiles of the plan");
 
 struct Params {
   Plan plan;
@@ -360,23 +303,20 @@ __global__ void __launch_bounds__(R::kThreads, 1)
   }
   // The load warps reckon while the barriers and tensor memory are set up: all
   // units of tails under one K/V head, and the CTAs that take pairs.
-  int tails = 0, pair_ctas = 0, start = 0;
+  int tiles = 0, some = 0, pair_ctas = 0;
   if (warp == kLoadWarp || warp == kLoadWarp + 1) {
-    int some = 0;
     for (int b0 = 0; b0 < plan.B; b0 += 128) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int b = b0 + u * 32 + lane;
         const int n = b < plan.B ? Plan::tiles_of(plan.len(b)) : 0;
-        tails += n;
+        tiles += n;
         some += n > 0;
       }
     }
-    tails = __reduce_add_sync(0xffffffffu, tails);
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
     some = __reduce_add_sync(0xffffffffu, some);
-    pair_ctas = plan.pair_ctas(tails, some);
-    start = plan.start_units(tails);
-    tails += start * some;
+    pair_ctas = plan.pair_ctas(tiles, some);
   }
   if (warp == kLoadWarp && lane == 0) {
     prefetch_tensormap(&tm_qp);
@@ -502,20 +442,21 @@ __global__ void __launch_bounds__(R::kThreads, 1)
       if (i == 0) {
         slot0 = 0, n_slots = kStages;
         const int lanes = plan.lanes(pair_ctas), l = blockIdx.x % lanes, c = blockIdx.x / lanes;
-        const Cut cut(plan.lane_pairs(lanes, l) * plan.Hkv * plan.prefix_tiles, pair_ctas / lanes);
+        const Cut cut = plan.pair_line(pair_ctas, lanes, l);
         const int u0 = c < cut.parts ? cut.begin(c) : 0, u1 = c < cut.parts ? cut.begin(c + 1) : 0;
         for (int u = u0; u < u1 && ok;) {
           const int s = u / plan.prefix_tiles, t0 = u - s * plan.prefix_tiles;
           const int t1 = min(plan.prefix_tiles, t0 + u1 - u);
-          run(kPair, s % plan.Hkv, 2 * (l + s / plan.Hkv * lanes) * plan.tile_reqs, t0, t1, (s + c) * lanes + l,
-              plan.Np);
+          run(kPair, s % plan.Hkv, 2 * (l + s / plan.Hkv * lanes) * plan.tile_reqs, t0, t1,
+              Plan::pair_slot(s, c, lanes, l), plan.Np);
           u += t1 - t0;
         }
         if (ok) publish(kEnd, 0, 0, 0, 0, 0, 0, true);
       }
     } else {
       const int singles = plan.ctas - pair_ctas;
-      const Cut cut(plan.odd_units() + tails * plan.Hkv, 2 * singles);
+      const int start = plan.start_units(tiles);
+      const Cut cut = plan.single_line(pair_ctas, tiles, some);
       // Streams of different CTAs are neighbours on the line, so that few units
       // go to many SMs.
       const int c = i * singles + static_cast<int>(blockIdx.x) - pair_ctas;
@@ -524,7 +465,7 @@ __global__ void __launch_bounds__(R::kThreads, 1)
       for (; u < min(u1, plan.odd_units()) && ok;) {
         const int s = u / plan.prefix_tiles, t0 = u - s * plan.prefix_tiles;
         const int t1 = min(plan.prefix_tiles, t0 + u1 - u);
-        run(kOdd, s, (plan.row_tiles - 1) * plan.tile_reqs, t0, t1, s + c, plan.Np);
+        run(kOdd, s, (plan.row_tiles - 1) * plan.tile_reqs, t0, t1, Plan::single_slot(s, c), plan.Np);
         u += t1 - t0;
       }
       int at = plan.odd_units();  // place of request b0's first unit
@@ -551,7 +492,8 @@ __global__ void __launch_bounds__(R::kThreads, 1)
             const int a = a0 + hk * (knt + start) + start;  // the first tile's place
             if (a >= u1) break;
             if (a + knt > u0)
-              run(kTail, hk, b0 + k, max(u0 - a, 0), min(u1 - a, knt), (b0 + k) * plan.Hkv + hk + c, kn);
+              run(kTail, hk, b0 + k, max(u0 - a, 0), min(u1 - a, knt),
+                  Plan::single_slot(plan.tail_segment(b0 + k, hk), c), kn);
           }
         }
       }
@@ -900,37 +842,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) shared_merge_kernel(const
     some = __reduce_add_sync(0xffffffffu, some);
     some_before = __reduce_add_sync(0xffffffffu, some_before);
 
-    // Parts [p0, p1) of the pairs' or the singles' line hold the prefix under this
-    // row tile, [t0, t1) of the singles' the tail.
-    const int n_tail = Plan::tiles_of(plan.len(req));
-    const int pair_ctas = plan.pair_ctas(all, some), start = plan.start_units(all);
-    const int mt = req / plan.tile_reqs;
-    const bool pair = mt < 2 * plan.pairs();
-    const int copies_p = pair ? 1 : Plan::copies(plan.tile_rows()), copies_t = Plan::copies(plan.rows);
-    // The prefix under this row tile: its segment on the line of its pair's lane, or
-    // on the singles'.
-    const int lanes = pair ? plan.lanes(pair_ctas) : 1, my_lane = pair ? mt / 2 % lanes : 0;
-    const int seg_p = pair ? mt / 2 / lanes * plan.Hkv + hk : hk, seg_t = req * plan.Hkv + hk;
-    const Cut singles(plan.odd_units() + (all + start * some) * plan.Hkv, 2 * (plan.ctas - pair_ctas));
-    int p0 = 0, p1 = 0, t0 = 0, t1 = 0;
-    if (plan.row_tiles > 0) {
-      const Cut cut = pair ? Cut(plan.lane_pairs(lanes, my_lane) * plan.Hkv * plan.prefix_tiles, pair_ctas / lanes)
-                           : singles;
-      p0 = cut.holder(seg_p * plan.prefix_tiles);
-      p1 = cut.holder((seg_p + 1) * plan.prefix_tiles - 1) + 1;
-    }
-    if (n_tail > 0) {
-      const int at = plan.odd_units() + (before + start * some_before) * plan.Hkv + hk * (n_tail + start) + start;
-      t0 = singles.holder(at);
-      t1 = singles.holder(at + n_tail - 1) + 1;
-    }
+    const Plan::Parts x = plan.parts(req, hk, all, some, before, some_before);
     if (lane == 0) {
-      s_pair = pair;
-      s_base_p = pair ? 2 * ((seg_p + p0) * lanes + my_lane) + (mt & 1) : (seg_p + p0) * copies_p;
-      s_step_p = pair ? 2 * lanes : 1;
-      s_n_p = (p1 - p0) * copies_p;
-      s_base_t = (seg_t + t0) * copies_t;
-      s_n_parts = (p1 - p0) * copies_p + (t1 - t0) * copies_t;
+      s_pair = x.pair;
+      s_base_p = x.base_p;
+      s_step_p = x.step_p;
+      s_n_p = x.n_p;
+      s_base_t = x.base_t;
+      s_n_parts = x.n_p + x.n_t;
     }
   }
   __syncthreads();

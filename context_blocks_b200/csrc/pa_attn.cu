@@ -576,56 +576,6 @@ int launch_block_norm(DeviceState* st, const pa::norm::Params& prm, bool x32, cu
   return x32 ? launch_block_norm_x<true>(st, prm, stream) : launch_block_norm_x<false>(st, prm, stream);
 }
 
-// Shapes of a shared-prefix call; false where the rows of one request under one
-// K/V head do not fit a row tile, or the key tiles a 32-bit count.
-bool shared_plan(int B, int Hq, int Hkv, int Nq, int Np, int Nt, int ctas, pa::shared::Plan* plan) {
-  const long long rows = static_cast<long long>(Hq / Hkv) * Nq;
-  if (rows < 1 || rows > pa::kBM) return false;
-  plan->B = B;
-  plan->Hq = Hq;
-  plan->Hkv = Hkv;
-  plan->G = Hq / Hkv;
-  plan->Nq = Nq;
-  plan->rows = static_cast<int>(rows);
-  plan->tile_reqs = std::min(B, pa::kBM / plan->rows);
-  plan->row_tiles = Np > 0 ? (B + plan->tile_reqs - 1) / plan->tile_reqs : 0;
-  plan->Np = Np;
-  plan->Nt = Nt;
-  plan->prefix_tiles = (Np + pa::kBN - 1) / pa::kBN;
-  plan->ctas = ctas;
-  plan->tail_lens = nullptr;
-  // The kernels count key tiles in 32 bits.
-  const long long units = static_cast<long long>(Hkv) * (static_cast<long long>(plan->prefix_tiles) * plan->row_tiles +
-                                                         static_cast<long long>(B) * ((Nt + pa::kBN - 1) / pa::kBN));
-  return units < (1ll << 30);
-}
-
-// Byte offsets of the parts of a shared-prefix workspace (each on a 256-byte
-// boundary), and their end.
-struct SharedWorkspace {
-  uint64_t pair_o, pair_ml, odd_o, odd_ml, tail_o, tail_ml, end;
-};
-
-SharedWorkspace shared_workspace(const pa::shared::Plan& plan, int d) {
-  using pa::shared::kMaxCtas;
-  auto up = [](uint64_t n) { return (n + 255) & ~255ull; };
-  const uint64_t rows = plan.rows, tile = plan.tile_rows();
-  // (segments of a lane + parts) * lanes, for any number of lanes up to the pairs.
-  const uint64_t pair = plan.pairs() > 0 ? (2ull * plan.Hkv * plan.pairs() + kMaxCtas) * 2 * tile : 0;
-  const uint64_t odd = plan.odd() ? (plan.Hkv + 2ull * kMaxCtas) * plan.copies(plan.tile_rows()) * tile : 0;
-  const uint64_t tail =
-      plan.Nt > 0 ? (static_cast<uint64_t>(plan.B) * plan.Hkv + 2ull * kMaxCtas) * plan.copies(plan.rows) * rows : 0;
-  SharedWorkspace w;
-  w.pair_o = 0;
-  w.pair_ml = up(pair * d * 4);
-  w.odd_o = w.pair_ml + up(pair * 8);
-  w.odd_ml = w.odd_o + up(odd * d * 4);
-  w.tail_o = w.odd_ml + up(odd * 8);
-  w.tail_ml = w.tail_o + up(tail * d * 4);
-  w.end = w.tail_ml + up(tail * 8);
-  return w;
-}
-
 template <int D, bool kCap, bool kBias>
 int launch_shared(DeviceState* st, const CUtensorMap (&maps)[6], const pa::shared::Params& prm, void* o, float* lse,
                   cudaStream_t stream) {
@@ -664,9 +614,9 @@ extern "C" {
 size_t pa_attn_shared_prefix_workspace(int B, int Hq, int Hkv, int Nq, int Np, int Nt, int d) {
   pa::shared::Plan plan;
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Nq < 1 || Np < 0 || Nt < 0 || (d != 64 && d != 128) ||
-      static_cast<long long>(B) * Hq > 65535 || !shared_plan(B, Hq, Hkv, Nq, Np, Nt, 1, &plan))
+      static_cast<long long>(B) * Hq > 65535 || !pa::shared::make_plan(B, Hq, Hkv, Nq, Np, Nt, 1, &plan))
     return 0;
-  return static_cast<size_t>(shared_workspace(plan, d).end);
+  return static_cast<size_t>(pa::shared::workspace(plan, d).end);
 }
 
 int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_prefix, const void* k_tail,
@@ -681,7 +631,7 @@ int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_pre
   if (Np > kMaxRows || Nt > kMaxRows - Np) return fail(PA_ERR_UNSUPPORTED, "Np + Nt must be <= 2^30");
   if (Nq == 0) return PA_OK;
   pa::shared::Plan plan;
-  if (!shared_plan(B, Hq, Hkv, Nq, Np, Nt, 1, &plan))
+  if (!pa::shared::make_plan(B, Hq, Hkv, Nq, Np, Nt, 1, &plan))
     return fail(PA_ERR_UNSUPPORTED, "(Hq / Hkv) * Nq must be <= %d, the key tiles of all requests < 2^30", pa::kBM);
   if (!tail_lens || !lse) return fail(PA_ERR_INVALID_ARG, "null pointer argument");
   if (!aligned(tail_lens, 4) || !aligned(lse, 4))
@@ -697,7 +647,7 @@ int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_pre
   const Operand vt = Nt ? operand(v_tail, "v_tail", B, Hkv, Nt, d, strides ? strides + 7 : nullptr) : oq;
   for (const Operand* x : {&oq, &oo, &kp, &vp, &kt, &vt})
     if ((rc = check_operand(*x, false)) != PA_OK) return rc;
-  const SharedWorkspace ws = shared_workspace(plan, d);
+  const pa::shared::Workspace ws = pa::shared::workspace(plan, d);
   if (ws.end > 0) {
     if (!workspace) return fail(PA_ERR_INVALID_ARG, "null pointer argument (workspace)");
     if (!aligned(workspace, 16)) return fail(PA_ERR_MISALIGNED, "workspace must be 16-byte aligned");
