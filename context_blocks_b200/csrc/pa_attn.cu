@@ -614,7 +614,7 @@ extern "C" {
 size_t pa_attn_shared_prefix_workspace(int B, int Hq, int Hkv, int Nq, int Np, int Nt, int d) {
   pa::shared::Plan plan;
   if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv || Nq < 1 || Np < 0 || Nt < 0 || (d != 64 && d != 128) ||
-      static_cast<long long>(B) * Hq > 65535 || !pa::shared::make_plan(B, Hq, Hkv, Nq, Np, Nt, 1, &plan))
+      static_cast<long long>(B) * Hq > 65535 || !pa::shared::make_plan(B, Hq, Hkv, Nq, Np, Nt, 1, 1, &plan))
     return 0;
   return static_cast<size_t>(pa::shared::workspace(plan, d).end);
 }
@@ -631,7 +631,8 @@ int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_pre
   if (Np > kMaxRows || Nt > kMaxRows - Np) return fail(PA_ERR_UNSUPPORTED, "Np + Nt must be <= 2^30");
   if (Nq == 0) return PA_OK;
   pa::shared::Plan plan;
-  if (!pa::shared::make_plan(B, Hq, Hkv, Nq, Np, Nt, 1, &plan))
+  const int pair_cost = pa::shared::pair_cost(softcap > 0.f, slopes != nullptr);
+  if (!pa::shared::make_plan(B, Hq, Hkv, Nq, Np, Nt, 1, pair_cost, &plan))
     return fail(PA_ERR_UNSUPPORTED, "(Hq / Hkv) * Nq must be <= %d, the key tiles of all requests < 2^30", pa::kBM);
   if (!tail_lens || !lse) return fail(PA_ERR_INVALID_ARG, "null pointer argument");
   if (!aligned(tail_lens, 4) || !aligned(lse, 4))

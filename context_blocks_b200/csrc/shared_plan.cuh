@@ -21,10 +21,17 @@ namespace shared {
 
 constexpr int kMaxCtas = 160;  // sizes the workspace; the grid is one CTA an SM, at most this many
 // What a pair's key tile and a unit of the singles cost, in parts of one another:
-// how the CTAs are dealt to the two kinds.  128 requests on 32768 capped keys,
-// tails of 16, 512 and 1024 tokens: 112, 132 and 162 us at 15 : 6; at 12 : 6 113,
-// 143 and 174; at 18 : 6 107, 136 and 160; at 22 : 6 121, 153 and 179.
-constexpr int kPairCost = 15, kSingleCost = 6;
+// how the CTAs are dealt to the two kinds.  Both the cap and the bias lengthen the
+// softmax that bounds pairs, and hide behind the loads of singles.  Five shapes (64 to
+// 256 requests, groups of 2 to 8 heads, prefixes of 8192 to 32768 keys, tails of 64 to
+// 1024), each at 9, 12, 15, 18, 22 and 27 : 6, d 128 and 64, relative to 15 : 6 in the
+// geometric mean:
+//   plain   1.09 1.03 1 1.07 1.17 1.31     1.13 1.04 1 1.01 1.10 1.20
+//   capped  1.12 1.04 1 1.04 1.13 1.26     1.14 1.05 1 1.04 1.12 1.24
+//   biased  1.13 1.05 1 1.00 1.08 1.20     1.14 1.06 1 0.99 1.02 1.13
+//   both    1.16 1.06 1 0.99 0.94 0.95     1.16 1.07 1 0.99 0.95 0.95
+constexpr int kSingleCost = 6;
+inline int pair_cost(bool cap, bool bias) { return cap && bias ? 22 : 15; }
 
 PA_HD inline int clamp(int x, int lo, int hi) { return x < lo ? lo : x > hi ? hi : x; }
 PA_HD inline float to_float(long long x) { return static_cast<float>(x); }
@@ -55,6 +62,7 @@ struct Plan {
   int Np, Nt;
   int prefix_tiles;  // key tiles of the prefix
   int ctas;
+  int pair_cost;     // see pair_cost()
   const int* tail_lens;
 
   PA_HD int tile_rows() const { return tile_reqs * rows; }
@@ -73,7 +81,7 @@ struct Plan {
   // CTAs that take pairs, given the key tiles (under one K/V head) of all tails
   // and the number of tails that have any; a tail's start costs about a tile.
   PA_HD int pair_ctas(int tiles, int tails) const {
-    const long long p = static_cast<long long>(pair_units()) * kPairCost;
+    const long long p = static_cast<long long>(pair_units()) * pair_cost;
     const long long s = (odd_units() + (tiles + tails) * static_cast<long long>(Hkv)) * kSingleCost;
     if (p == 0) return 0;
     if (s == 0) return ctas <= pairs() ? ctas : ctas - ctas % pairs();
@@ -150,7 +158,7 @@ struct Plan {
 
 // Shapes of a call; false where the rows of one request under one K/V head do not
 // fit a row tile, or the key tiles a 32-bit count.
-inline bool make_plan(int B, int Hq, int Hkv, int Nq, int Np, int Nt, int ctas, Plan* plan) {
+inline bool make_plan(int B, int Hq, int Hkv, int Nq, int Np, int Nt, int ctas, int pair_cost, Plan* plan) {
   const long long rows = static_cast<long long>(Hq / Hkv) * Nq;
   if (rows < 1 || rows > kPlanRows) return false;
   plan->B = B;
@@ -165,6 +173,7 @@ inline bool make_plan(int B, int Hq, int Hkv, int Nq, int Np, int Nt, int ctas, 
   plan->Nt = Nt;
   plan->prefix_tiles = Plan::tiles_of(Np);
   plan->ctas = ctas;
+  plan->pair_cost = pair_cost;
   plan->tail_lens = nullptr;
   // The kernels count key tiles in 32 bits.
   const long long units = static_cast<long long>(Hkv) * (static_cast<long long>(plan->prefix_tiles) * plan->row_tiles +

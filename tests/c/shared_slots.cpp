@@ -145,7 +145,8 @@ int main(int argc, char** argv) {
     const int B = pick({1, 2, 3, 5, 17, 32, 64, 100, 130, 257, 700});
     const int Np = pick({0, 1, 100, 128, 129, 1000, 5000, 33000, 119056}), Nt = pick({0, 1, 16, 128, 129, 500, 2100});
     Plan p;
-    if (!make_plan(B, G * Hkv, Hkv, Nq, Np, Nt, pick({2, 3, 7, 20, 132, 148, 160}), &p)) continue;
+    if (!make_plan(B, G * Hkv, Hkv, Nq, Np, Nt, pick({2, 3, 7, 20, 132, 148, 160}),
+                   pair_cost(rng() % 2, rng() % 2), &p)) continue;
     std::vector<int> lens(B);
     const int most = pick({0, 1, 2}), third = static_cast<int>(rng() % 3);
     for (int& n : lens) {
