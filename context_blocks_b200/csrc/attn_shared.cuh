@@ -24,7 +24,8 @@
 // without host knowledge of them.  The part of a segment that falls to one part of the
 // line is a piece; segment + part is another number for every piece, since both
 // only grow along the line, and names the place of its partial results in the
-// caller's workspace: normalised fp32 O rows and their LSE (base 2).
+// caller's workspace: O rows as the accumulators hold them, fp32, and each row's
+// maximum (base 2) and sum of weights.
 // shared_merge_kernel joins them, finding them by the same arithmetic.
 //
 // The streams of a single CTA run independently, so that one stream's loads,
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(R::kThreads, 1)
     int idx = 0;  // ring position
     int g = 0;    // key tiles so far: phase of the P barriers (the same for both streams of a pair CTA)
     int q_used = 0;
-    Piece x;
+    Piece x = {};
     // A piece, for the streams [i0, i1): constants, see attn_mod.cuh.
     auto work = [&](auto lo, auto hi) {
       constexpr int i0 = decltype(lo)::value, i1 = decltype(hi)::value;
