@@ -719,7 +719,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
         if constexpr (kWide)
           capped_keys(tS, tS, seen.x - k0, seen.y - k0, true, p.sm, l, (half ? bar_p_full0 : bar_p_part0) + 8 * i, lane);
         else
-          softmax_tile<D, kCap, kBias>(tS, tO, seen.x - k0, seen.y - k0, static_cast<float>(pos - k0), slope2, p.sm,
+          softmax_tile<D, kCap, kBias, false>(tS, tO, seen.x - k0, seen.y - k0, static_cast<float>(pos - k0), slope2, p.sm,
                                        true, j < last - 1, m_ref, l, bar_p_part0 + 8 * i, bar_p_full0 + 8 * i, lane);
       }
       if (!ok) break;

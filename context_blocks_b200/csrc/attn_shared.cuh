@@ -707,8 +707,8 @@ __global__ void __launch_bounds__(R::kThreads, 1)
           softmax_share<D, kCap, kBias, 64>(tS, tO, kq, b, dist0, slope2, p.sm, mine, have_o, m_ref, l,
                                             bar_p_part0 + 8 * i, bar_p_full0 + 8 * i, lane);
         else
-          softmax_tile<D, kCap, kBias>(tS, tO, 0, b, dist0, slope2, p.sm, mine, have_o, m_ref, l, bar_p_part0 + 8 * i,
-                                       bar_p_full0 + 8 * i, lane);
+          softmax_tile<D, kCap, kBias, kCap && !kBias>(tS, tO, 0, b, dist0, slope2, p.sm, mine, have_o, m_ref, l,
+                                                       bar_p_part0 + 8 * i, bar_p_full0 + 8 * i, lane);
       }
       if (!ok) break;
       {

@@ -362,12 +362,13 @@ __device__ __forceinline__ void capped_keys(uint32_t tS, uint32_t tP, int a, int
 // keys [a, b) of the tile.  m_ref, l: the row's running reference maximum and
 // sum; tO: its O accumulator, rescaled when the maximum moves (`have_o`: it
 // holds something).  A row that has seen nothing keeps m_ref = -inf and l = 0; one
-// that does not count (`counts`) makes no difference to others.
-template <int D, bool kCap, bool kBias>
+// that does not count (`counts`) makes no difference to others.  kFixed: capped scores
+// may be against the fixed reference (sm.cap_fixed).
+template <int D, bool kCap, bool kBias, bool kFixed>
 __device__ __forceinline__ void softmax_tile(uint32_t tS, uint32_t tO, int a, int b, float dist0, float slope2,
                                              const ScoreMod& sm, bool counts, bool have_o, float& m_ref, float& l,
                                              uint32_t bar_part, uint32_t bar_full, int lane) {
-  if constexpr (kCap && !kBias) {
+  if constexpr (kFixed) {
     if (sm.cap_fixed) {
       if (max(a, 0) < min(b, kBN)) m_ref = sm.cap_ref;  // stays -inf until the row sees a key
       capped_keys(tS, tS, a, b, counts, sm, l, bar_part, lane);
