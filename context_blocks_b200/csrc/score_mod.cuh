@@ -244,12 +244,16 @@ __device__ __forceinline__ void hide(uint64_t (&x)[kPairs], int a, int b, float 
 // which those in [a, b) count.  The distance is linear in the key on either side
 // of the row's own position: unless a row sees keys on both sides, the bias is
 // a base for every eight keys plus one of four pairs of multiples of the slope,
-// two packed operations a pair.  The two are added before the score: at the row's
-// own position they cancel exactly, whatever the slope.
+// two packed operations a pair.  In between a score is rounded beside up to seven
+// slopes (2^-15 at kLinearSlope), so beyond that every key's distance is taken by
+// itself.  Adding the base and the multiple first would do for all slopes, but made 4096
+// causal biased keys, 24 heads, take 130 us instead of 118.
+constexpr float kLinearSlope = 64.f;  // log2 units
 template <int kPairs, bool kMul>
 __device__ __forceinline__ void bias_scores(uint64_t (&x)[kPairs], float mul, float slope2, float dist0, int a, int b) {
   const bool behind = dist0 >= static_cast<float>(min(b, 2 * kPairs) - 1);  // all keys that count
-  if (__all_sync(0xffffffffu, behind || dist0 <= static_cast<float>(max(a, 0)))) {
+  if (__all_sync(0xffffffffu,
+                 (behind || dist0 <= static_cast<float>(max(a, 0))) && fabsf(slope2) <= kLinearSlope)) {
     const float sl = behind ? slope2 : -slope2;
     uint64_t step[4];
 #pragma unroll
@@ -257,8 +261,7 @@ __device__ __forceinline__ void bias_scores(uint64_t (&x)[kPairs], float mul, fl
 #pragma unroll
     for (int e = 0; e < kPairs; ++e) {
       const float at = sl * (static_cast<float>(2 * (e & ~3)) - dist0);
-      const uint64_t far = f2_add(f2(at, at), step[e & 3]);
-      x[e] = kMul ? f2_fma(x[e], f2(mul, mul), far) : f2_add(x[e], far);
+      x[e] = f2_add(kMul ? f2_fma(x[e], f2(mul, mul), f2(at, at)) : f2_add(x[e], f2(at, at)), step[e & 3]);
     }
   } else {
 #pragma unroll
