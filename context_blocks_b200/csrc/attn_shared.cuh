@@ -783,14 +783,13 @@ __device__ __noinline__ void redo_row(const Params& p, int rr, __nv_bfloat16* o,
   const __nv_bfloat16* vt = p.vt + req * p.vt_s[0] + hk * p.vt_s[1];
   const int own = min(max(pos + 1, 0), plan.len(req));  // keys of the tail
   unsigned up = 0u, down = 0u;
-  scan_values<kCols>(vp, p.vp_s[1], 0, plan.Np, up, down, 0u);
-  scan_values<kCols>(vt, p.vt_s[2], 0, own, up, down, 0u);
-  float qv[kCols], acc[kCols];
-#pragma unroll
-  for (int u = 0; u < kCols; ++u) qv[u] = __bfloat162float(q[lane * kCols + u]), acc[u] = 0.f;
+  scan_values<kCols>(vp, p.vp_s[1], 0, plan.Np, up, down);
+  scan_values<kCols>(vt, p.vt_s[2], 0, own, up, down);
+  float qv[kCols], acc[kCols] = {};
+  load_row_part<kCols>(q + lane * kCols, qv);
   if (__any_sync(0xffffffffu, (bad & ~(up | down)) != 0u)) {
-    add_keys<D, kCols>(qv, kp, vp, p.kp_s[1], p.vp_s[1], 0, plan.Np, plan.Np + pos, ref, slope2, p.sm, cap, bias, acc, 0u);
-    add_keys<D, kCols>(qv, kt, vt, p.kt_s[2], p.vt_s[2], 0, own, pos, ref, slope2, p.sm, cap, bias, acc, 0u);
+    add_keys<D, kCols, 4>(qv, kp, vp, p.kp_s[1], p.vp_s[1], 0, plan.Np, plan.Np + pos, ref, slope2, p.sm, cap, bias, acc);
+    add_keys<D, kCols, 4>(qv, kt, vt, p.kt_s[2], p.vt_s[2], 0, own, pos, ref, slope2, p.sm, cap, bias, acc);
   }
 #pragma unroll
   for (int u = 0; u < kCols; ++u) {

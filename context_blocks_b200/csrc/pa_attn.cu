@@ -494,11 +494,15 @@ int check_scores(int B, int Hq, int Hkv, int Nq, int d, float scale, float softc
 }
 
 // Limit of a wait in the modified-score kernels, where a warp may wait while
-// another goes over all the keys: the library's limit, and 20 us (ten times
-// what one takes) for every key tile.  While rows are repaired (repair_rows in
-// attn_mod.cuh) the limit starts anew as long as they make progress.
-unsigned long long wait_limit_ns(long long key_tiles) {
-  return g_wait_limit_ns.load(std::memory_order_relaxed) + 20000ull * static_cast<unsigned long long>(key_tiles);
+// another goes over all the keys: the library's limit, and for every key tile
+//   kTileNs    20 us, ten times what a tile takes
+//   kRepairNs  5 ms, for a kernel in which the other may then do 32 rows again
+//              (repair_rows in attn_mod.cuh): 1200 ns a key and row, of which it took
+//              420 where all SMs were at it (16384 keys, capped, d 128)
+constexpr unsigned long long kTileNs = 20000, kRepairNs = 5000000;
+
+unsigned long long wait_limit_ns(long long key_tiles, unsigned long long ns_per_tile) {
+  return g_wait_limit_ns.load(std::memory_order_relaxed) + ns_per_tile * static_cast<unsigned long long>(key_tiles);
 }
 
 pa::mod::ScoreMod score_mod(float scale, float softcap, const float* slopes) {
@@ -708,7 +712,7 @@ int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_pre
   prm.tail_ml = reinterpret_cast<float2*>(w + ws.tail_ml);
   prm.sm = score_mod(scale, softcap, slopes);
   prm.status = st->status;
-  prm.timeout_ns = wait_limit_ns(plan.prefix_tiles + (Nt + pa::kBN - 1) / pa::kBN);
+  prm.timeout_ns = wait_limit_ns(plan.prefix_tiles + (Nt + pa::kBN - 1) / pa::kBN, kTileNs);
   return by_mod(d, softcap > 0.f, slopes != nullptr, [&](auto dd, auto cap, auto bias) {
     return launch_shared<decltype(dd)::value, decltype(cap)::value, decltype(bias)::value>(
         st, maps, prm, o, lse, static_cast<cudaStream_t>(stream));
@@ -792,7 +796,7 @@ int pa_attn_fwd_mod(const void* q, const void* k, const void* v, void* o, float*
   prm.n_docs = n_docs;
   prm.sm = score_mod(scale, mod->softcap, mod->slopes);
   prm.status = st->status;
-  prm.timeout_ns = wait_limit_ns((Nk + pa::kBN - 1) / pa::kBN);
+  prm.timeout_ns = wait_limit_ns((Nk + pa::kBN - 1) / pa::kBN, kRepairNs);
   return by_mod(d, mod->softcap > 0.f, mod->slopes != nullptr, [&](auto dd, auto cap, auto bias) {
     return launch_mod<decltype(dd)::value, decltype(cap)::value, decltype(bias)::value>(
         st, tq, tk, tv, prm, static_cast<cudaStream_t>(stream));

@@ -93,27 +93,17 @@ __device__ __forceinline__ bool mbar_try_wait_hint(uint32_t bar, uint32_t parity
 }
 
 // mbar_wait with a suspend-time hint on every probe; same bound and abort
-// behaviour (the time limit is checked after every 4 probes).  With kProgress the
-// word behind the abort word is counted up by work of unusual length that others
-// wait for, itself of a bounded number of steps: the limit starts anew whenever it
-// has moved.
-template <bool kProgress = false>
+// behaviour (the time limit is checked after every 4 probes).
 __device__ __forceinline__ bool mbar_wait_hint(uint32_t bar, uint32_t parity, volatile int* abort_word,
                                                int* status, int code, uint64_t limit_ns, uint32_t hint_ns) {
   if (mbar_try_wait_hint(bar, parity, hint_ns)) return true;
-  uint64_t t0 = globaltimer_ns();
-  int before = kProgress ? abort_word[1] : 0;
+  const uint64_t t0 = globaltimer_ns();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 4; ++i)
       if (mbar_try_wait_hint(bar, parity, hint_ns)) return true;
     if (abort_word != nullptr && *abort_word) return false;
     if (globaltimer_ns() - t0 > limit_ns) {
-      if (kProgress && abort_word[1] != before) {
-        before = abort_word[1];
-        t0 = globaltimer_ns();
-        continue;
-      }
       if (abort_word != nullptr) *abort_word = 1;
       atomicCAS(status, 0, code);
       return false;

@@ -578,31 +578,39 @@ __device__ __noinline__ bool store_rows(uint32_t tO, uint32_t stg, __nv_bfloat16
 // What a warp does again, where an accumulator is not finite: lane l holds columns
 // l * kV .. of the rows it is given.  Rare, and written for shortness.
 
-// Counts up the CTA's progress word (its shared-memory address; 0: none), so that
-// those who wait for this warp go on waiting (mbar_wait_hint).
-__device__ __forceinline__ void tick(uint32_t progress) {
-  if (progress != 0u && threadIdx.x % 32 == 0)
-    asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(progress) : "memory");
+// n bf16 from an address that is a multiple of their size.
+template <int n>
+__device__ __forceinline__ void load_row_part(const __nv_bfloat16* p, float (&x)[n]) {
+  static_assert(n == 1 || n == 2 || n == 4, "as many columns as a lane may hold");
+  if constexpr (n == 1) {
+    x[0] = __bfloat162float(*p);
+  } else {
+    uint32_t w[n / 2];
+    if constexpr (n == 2) {
+      w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x, w[1] = v.y;
+    }
+#pragma unroll
+    for (int u = 0; u < n / 2; ++u)
+      x[2 * u] = __uint_as_float(w[u] << 16), x[2 * u + 1] = __uint_as_float(w[u] & 0xffff0000u);
+  }
 }
 
 // Columns with +Inf or NaN (`up`) and with -Inf or NaN (`down`) among the value rows
 // [j0, j1): bit u of a lane's masks for its column u.  Ends early where all are both.
 template <int kV>
 __device__ __forceinline__ void scan_values(const __nv_bfloat16* v, long long v_stride, int j0, int j1, unsigned& up,
-                                            unsigned& down, uint32_t progress) {
+                                            unsigned& down) {
   constexpr int kStep = 8;
   const int lane = threadIdx.x % 32;
 #pragma unroll 1
   for (int j = j0; j < j1; j += kStep) {
     if (__all_sync(0xffffffffu, (up & down) == (1u << kV) - 1)) return;
-    if (((j - j0) & 255) == 0) tick(progress);
     float x[kStep][kV];
 #pragma unroll
-    for (int e = 0; e < kStep; ++e) {
-      const __nv_bfloat16* vr = v + min(j + e, j1 - 1) * v_stride + lane * kV;
-#pragma unroll
-      for (int u = 0; u < kV; ++u) x[e][u] = __bfloat162float(vr[u]);
-    }
+    for (int e = 0; e < kStep; ++e) load_row_part<kV>(v + min(j + e, j1 - 1) * v_stride + lane * kV, x[e]);
 #pragma unroll
     for (int e = 0; e < kStep; ++e)
 #pragma unroll
@@ -620,29 +628,30 @@ __device__ __forceinline__ float not_finite(bool up, bool down) {
 }
 
 // Attention of one row over the keys [j0, j1), by the whole warp: acc += 2^(x_j - ref)
-// v_j.  Lane l holds D / 32 of the query's columns in qv.  Four keys at a time, so
-// that their loads and sums wait together; all fp32.
-template <int D, int kV>
+// v_j.  Lane l holds D / 32 of the query's columns in qv.  kStep keys at a time, so
+// that their loads and sums wait together; all fp32.  8 and 4 in repair_rows: 67 and
+// 83 ns a key and row (4096 keys, d 64); the merge's registers allow 4.
+template <int D, int kV, int kStep = 8>
 __device__ __forceinline__ void add_keys(const float (&qv)[D / 32], const __nv_bfloat16* k, const __nv_bfloat16* v,
                                          long long k_stride, long long v_stride, int j0, int j1, int pos, float ref,
-                                         float slope2, const ScoreMod& sm, bool cap, bool bias, float (&acc)[kV],
-                                         uint32_t progress) {
-  constexpr int kQk = D / 32, kStep = 4;
+                                         float slope2, const ScoreMod& sm, bool cap, bool bias,
+                                         float (&acc)[kV]) {
+  constexpr int kQk = D / 32;
   const int lane = threadIdx.x % 32;
 #pragma unroll 1
   for (int j = j0; j < j1; j += kStep) {
-    if (((j - j0) & 255) == 0) tick(progress);
-    float dot[kStep], vv[kStep][kV];
+    float dot[kStep], kk[kStep][kQk], vv[kStep][kV];
 #pragma unroll
     for (int e = 0; e < kStep; ++e) {
       const long long at = min(j + e, j1 - 1);  // past the end: the last key once more, without weight
-      const __nv_bfloat16* kr = k + at * k_stride + lane * kQk;
-      const __nv_bfloat16* vr = v + at * v_stride + lane * kV;
+      load_row_part<kQk>(k + at * k_stride + lane * kQk, kk[e]);
+      load_row_part<kV>(v + at * v_stride + lane * kV, vv[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < kStep; ++e) {
       dot[e] = 0.f;
 #pragma unroll
-      for (int u = 0; u < kQk; ++u) dot[e] = fmaf(qv[u], __bfloat162float(kr[u]), dot[e]);
-#pragma unroll
-      for (int u = 0; u < kV; ++u) vv[e][u] = __bfloat162float(vr[u]);
+      for (int u = 0; u < kQk; ++u) dot[e] = fmaf(qv[u], kk[e][u], dot[e]);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)

@@ -167,8 +167,7 @@ def test_infinite_values_reach_the_rows_that_see_them(d, mask, kw):
 @pytest.mark.parametrize("softcap", [0.0, 20.0])
 def test_repaired_rows_keep_a_short_wait_from_running_out(softcap):
     """More items than SMs, values that are not finite hidden from most rows of
-    their tile: others wait while a warp does 32 rows again, far longer than the
-    limit, which counts from the last progress."""
+    their tile: others wait while a warp does 32 rows again, which the limit allows for."""
     q, k, v = (_rand((2, 30, 4096, 64), s) for s in (1, 2, 3))
     o, lse = pa.attn_fwd_mod(q, k, v, causal=True, softcap=softcap)
     bad = v.clone()
