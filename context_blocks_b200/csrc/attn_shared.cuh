@@ -37,7 +37,8 @@
 // 5.6 (24 heads, 119056 keys, 21 rows).  The copies' results are joined like those
 // of different pieces.  Without starts on the line, the streams at its end had some
 // forty short tails each there and finished 60 us behind the others; with them the
-// kernel takes 222 us for 1.47 GB, 6.6 TB/s.
+// kernel takes 230 us for 1.47 GB read again and again (6.4 TB/s, L2 keeps a part) and
+// 260 to 280 us in a call whose buffers change (5.4 TB/s).
 //
 // Warps: 0-3, 4-7 softmax of stream 0 and 1 (208 registers); 8, 11 MMA issue of
 // stream 0 and 1 (8 issues for both in a pair CTA); 9, 10 pieces and TMA loads
