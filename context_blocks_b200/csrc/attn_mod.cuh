@@ -36,12 +36,16 @@
 // costs more than it gains (4096 keys, 24 heads: 207 us against 181).
 //
 // Bound: the chain from a tile's scores to its weights, which the tensor pipe waits
-// for as in the plain forward (4096 x 4096 keys, 24 heads: 181 us, 0.69 of the
-// matrix rate); with a cap the FMA pipe, on which the polynomial runs (8192 capped
-// causal keys, 24 heads: 430 us, FMA 56 % busy, special-function unit and tensor
-// pipe 48 %); with short documents an item's start and end, some 8 000 clocks beside
+// for (4608 x 4608 keys unmasked, 24 heads: 216 us, 0.73 of the matrix rate, where the
+// plain forward takes 196 us, 0.80; which of the 4-D maps, the claimed items, the
+// order of issue and 40 bytes of spilled registers it owes that to has not been
+// measured); with a cap the FMA pipe, on which the polynomial runs (8192 capped
+// causal keys, 24 heads: 421 us, FMA 56 % busy, special-function unit and tensor
+// pipe 47 %); with short documents an item's start and end, some 8 000 clocks beside
 // the 5 000 to 7 500 of a tile that the mask cuts (8192 keys in 24 documents, 24
-// heads, biased: 110 us, tensor pipe 25 % busy).
+// heads, biased: 109 us, tensor pipe 25 % busy); with fewer items than SMs the
+// longest item, 2.2 us a key tile however few its rows (1 row of 24 heads on 8192
+// keys: 107 us, its bytes 5).
 #pragma once
 
 #include <cuda_bf16.h>

@@ -18,8 +18,8 @@
 // the kernels (8192 capped causal keys, 24 heads: 800 us before, 639 us with it).
 // The unit's own tanh has a relative error of 2^-11, which at c = 50 would be 0.02 in
 // the exponent.  Scores of 4096 causal keys, 24 heads, normal with deviation 3, cap
-// 20, 12, 8 and 4: 122, 152, 221 and 221 us; each by its own u against the fixed
-// reference too: 122, 181, 240 and 249.
+// 20, 12 and 4: 130, 160 and 224 us; each by its own u against the fixed reference
+// too: 132, 181 and 249.
 // Roundings to fewer bits than fp32, and why.
 //   Weights to bf16 for P.V: a matrix instruction takes A and B of one type, and V is
 //   bf16; a second product with the weights' lower halves would cost half the matrix
@@ -27,7 +27,8 @@
 //   leaves the errors of a row's weights independent.  O errs by 0.8e-3 to 1.7e-3
 //   (relative L2, normal values), its own rounding to bf16 by 1.65e-3.
 //   One in four exponentials by a degree-3 polynomial (1.4e-4, a thirtieth of the
-//   above) where nothing is hidden or capped: 4 % faster in the plain forward.
+//   above) where nothing is hidden or capped: 1 in 8 gave the plain forward 0.4 to 1 %
+//   and 1 in 4 another 1 to 2 % on short keys.
 //   ex2, lg2 and rcp of the special-function unit: 2^-22, below fp32 sums of a row.
 #pragma once
 
