@@ -712,7 +712,9 @@ int pa_attn_shared_prefix(const void* q, const void* k_prefix, const void* v_pre
   prm.tail_ml = reinterpret_cast<float2*>(w + ws.tail_ml);
   prm.sm = score_mod(scale, softcap, slopes);
   prm.status = st->status;
-  prm.timeout_ns = wait_limit_ns(plan.prefix_tiles + (Nt + pa::kBN - 1) / pa::kBN, kTileNs);
+  // The load warps look through all requests' lengths for their pieces: 200 ns a
+  // request, some ten times what it takes.
+  prm.timeout_ns = wait_limit_ns(plan.prefix_tiles + (Nt + pa::kBN - 1) / pa::kBN, kTileNs) + 200ull * B;
   return by_mod(d, softcap > 0.f, slopes != nullptr, [&](auto dd, auto cap, auto bias) {
     return launch_shared<decltype(dd)::value, decltype(cap)::value, decltype(bias)::value>(
         st, maps, prm, o, lse, static_cast<cudaStream_t>(stream));

@@ -501,7 +501,8 @@ int pa_selftest_timeout(int limit_us, void* stream);
  * makes no progress for this long gives up and reports PA_ERR_TIMEOUT (in
  * pa_attn_fwd_mod and pa_attn_shared_prefix, where a warp may wait while another
  * goes over all the keys, after 5 ms and 20 us more for every 128 keys; in the
- * former the other may also recompute rows that a hidden NaN or Inf has reached).  Raise
+ * former the other may also recompute rows that a hidden NaN or Inf has reached, in
+ * the latter it looks through the requests, 200 ns more for each).  Raise
  * it where the GPU is time-sliced among many processes and a kernel may be
  * held off the GPU for long stretches.  Returns PA_OK or PA_ERR_INVALID_ARG.
  */

@@ -158,6 +158,14 @@ int main(int argc, char** argv) {
     p.tail_lens = lens.data();
     check_call(p);
   }
+  for (int Np : {0, 128, 300}) {  // as many requests as there may be
+    Plan p;
+    std::vector<int> lens(65535);
+    for (int& n : lens) n = static_cast<int>(rng() % 9);
+    if (!make_plan(65535, 1, 1, 1, Np, 8, 148, pair_cost(false, false), &p)) return 1;
+    p.tail_lens = lens.data();
+    check_call(p);
+  }
   std::puts("slots checked");
   return 0;
 }

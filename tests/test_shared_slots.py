@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import context_blocks_b200 as pa
-from tests.test_score_mod import _rand, _slopes
+from tests.test_score_mod import LSE_ABS, _rand, _slopes
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -32,6 +32,35 @@ def program(tmp_path_factory):
 def test_pieces_and_slots_of_random_calls(program, seed):
     r = subprocess.run([program, str(seed), "400"], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and "slots checked" in r.stdout, r.stderr
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Np", [0, 128])
+def test_as_many_requests_as_there_may_be(Np):
+    """65535 requests with the shortest wait: looking for pieces among their lengths
+    is part of the limit.  Against a float64 evaluation of all of them; tolerances as
+    derived in tests/test_score_mod.py."""
+    Bn, Nt, d = 65535, 8, 64
+    q, kp, vp = _rand((Bn, 1, 1, d), 1, 2.0), _rand((1, Np, d), 2), _rand((1, Np, d), 3)
+    kt, vt = _rand((Bn, 1, Nt, d), 4), _rand((Bn, 1, Nt, d), 5)
+    n = (torch.arange(Bn, device="cuda") * 7 % (Nt + 1)).to(torch.int32)
+    pa.set_wait_limit_ms(1)
+    try:
+        o, lse = pa.attn_shared_prefix(q, kp, vp, kt, vt, n, check=True)
+    finally:
+        pa.set_wait_limit_ms(5000)
+    s_p = (q[:, 0].double() @ kp[0].double().t()).view(Bn, 1, Np) * d ** -0.5
+    s_t = torch.einsum("bd,bnd->bn", q[:, 0, 0].double(), kt[:, 0].double()) * d ** -0.5
+    s_t = s_t.masked_fill(torch.arange(Nt, device="cuda") >= n[:, None], float("-inf"))
+    s = torch.cat([s_p[:, 0], s_t], 1)
+    want = torch.logsumexp(s, 1)
+    none = want == float("-inf")
+    p = torch.exp(s - want.masked_fill(none, 0.0)[:, None])
+    ref = p[:, :Np] @ vp[0].double() + torch.einsum("bn,bnd->bd", p[:, Np:], vt[:, 0].double())
+    got = lse[:, 0, 0].double()
+    assert torch.equal(none, got == float("-inf")) and (o[none] == 0).all()
+    assert (got - want)[~none].abs().max() <= LSE_ABS
+    assert (o[:, 0, 0].double() - ref).abs().max() <= 2.0 ** -7 * 6.0
 
 
 @pytest.mark.gpu
