@@ -256,9 +256,9 @@ struct Layout {
 // that is not finite needs no scores; what all rows see is looked through once for
 // all of them.  lo, hi, ref: of the lane's own row; q, o: the warp's first row; k, v:
 // row 0 of its head; pos: the first row's position.  kCols of the value columns
-// are computed, those from v and o on.  NaN
-// hidden from the last row block of 4096 causal keys, 24 heads, d 128: 10 ms in all
-// (0.12 without); visible, at every 128th key: 0.47 ms.
+// are computed, those from v and o on.  NaN hidden from the last row block of 4096
+// causal keys, 24 heads, d 128: 10 ms in all (0.12 without); visible, at every 128th
+// key: 0.47 ms.
 template <int D, int kCols>
 __device__ __noinline__ void repair_rows(unsigned redo, const __nv_bfloat16* q, long long q_stride,
                                          const __nv_bfloat16* k, const __nv_bfloat16* v, long long k_stride,
@@ -627,9 +627,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
               break;
             }
             tc_fence_after();
-            if (leader) {
-              issue_pv(i, sv, acc, 0);
-            }
+            if (leader) issue_pv(i, sv, acc, 0);
             __syncwarp();
             if (!wait_all(bar_p_full0 + 8 * i, ph)) {
               ok = false;
@@ -721,8 +719,9 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1)
         if constexpr (kWide)
           capped_keys(tS, tS, seen.x - k0, seen.y - k0, true, p.sm, l, (half ? bar_p_full0 : bar_p_part0) + 8 * i, lane);
         else
-          softmax_tile<D, kCap, kBias, false>(tS, tO, seen.x - k0, seen.y - k0, static_cast<float>(pos - k0), slope2, p.sm,
-                                       true, j < last - 1, m_ref, l, bar_p_part0 + 8 * i, bar_p_full0 + 8 * i, lane);
+          softmax_tile<D, kCap, kBias, false>(tS, tO, seen.x - k0, seen.y - k0, static_cast<float>(pos - k0), slope2,
+                                              p.sm, true, j < last - 1, m_ref, l, bar_p_part0 + 8 * i,
+                                              bar_p_full0 + 8 * i, lane);
       }
       if (!ok) break;
       if (first < last) {
